@@ -244,6 +244,115 @@ qk_status qk_rmsnorm_matmul_batch_static(const qk_matmul_desc *descs, int count,
 int64_t qk_rmsnorm_scratch_bytes(int qtype, int gateup, int64_t M, int64_t K);
 
 /*
+ * int8 activations that are quantized already (by qk_add_rmsnorm_q8, say):
+ * one token's x as K int8 values x_q8 and K / 32 fp32 scales x_d,
+ *   y[n] = sum_k x_d[k / 32] x_q8[k] w[n][k],
+ * with the arithmetic of qk_matmul_batch_q8x: for the x_q8 and x_d that
+ * qk_matmul_batch_q8x would compute from an fp16 x the results are
+ * bit-identical.  up_blocks != NULL: the fused gate/up + SwiGLU, y fp16.
+ * M must be 0 or 1 and K one that the decode GEMV can stage, as there; x_q8
+ * and x_d are 16-byte aligned.  Rules and errors as in qk_matmul_batch_q8x.
+ */
+typedef struct qk_matmul_q8_desc {
+  int qtype;
+  const void *blocks;
+  const void *up_blocks;
+  const int8_t *x_q8;
+  const float *x_d;
+  void *y;
+  int64_t M, N, K;
+} qk_matmul_q8_desc;
+
+qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc *descs, int count, qk_stream_t stream);
+
+/* Element types of a residual stream. */
+#define QK_F16 0
+#define QK_F32 1
+
+/*
+ * Residual addition and RMSNorm between two linears (DAMASCUS project
+ * overview, "[04] one decode step": residual, then RMSNorm, before the QKV
+ * projections and before the FFN).  For each of M rows of K values
+ *   h = residual + delta                              (fp32 sum)
+ *   residual_out = h                                  (rounded to the residual's type)
+ *   xhat = fp16( h / sqrt(mean_k h^2 + eps) * gamma ) (fp32 arithmetic on the unrounded h)
+ * residual is fp16 or fp32 (residual_type QK_F16 / QK_F32), delta the fp32
+ * output of a linear, or NULL for h = residual; gamma fp16[K].  residual_out
+ * may be the residual itself (in place) or NULL (not wanted); xhat feeds the
+ * linears.  K is a positive multiple of 8 below 2^31, M at most 2^31 - 1.
+ * Outputs may not overlap each other or an input, save residual_out ==
+ * residual.  h^2 must stay within fp32.
+ * qk_add_rmsnorm_q8 writes the activations in int8 instead, quantized from
+ * the fp16 xhat as the q8x matmuls quantize (per 32 values d = amax / 127,
+ * q = round(xhat / d), ties away from zero, d = 0 gives q = 0; finite xhat):
+ * xq int8 [M][K] and xd fp32 [M][K / 32], one row of which is the x of
+ * qk_matmul_batch_q8.  K is a multiple of 32 there.
+ * M = 0 is a no-op.
+ */
+qk_status qk_add_rmsnorm(const void *residual, int residual_type, const float *delta, const uint16_t *gamma_f16,
+                         float eps, void *residual_out, uint16_t *xhat_f16, int64_t M, int64_t K, qk_stream_t stream);
+qk_status qk_add_rmsnorm_q8(const void *residual, int residual_type, const float *delta, const uint16_t *gamma_f16,
+                            float eps, void *residual_out, int8_t *xq, float *xd, int64_t M, int64_t K,
+                            qk_stream_t stream);
+
+/* Which dimensions of a head turn together: (2i, 2i + 1) or (i, i + n_rot / 2). */
+#define QK_ROPE_INTERLEAVED 0
+#define QK_ROPE_HALF 1
+
+/*
+ * Rotary positions, and the new rows of the KV cache ("[04] one decode step":
+ * RoPE between the QKV projections and the attention over the cache; "[06] the
+ * target": theta = 500000).  From the fp32 outputs q [M][H][D], k and v
+ * [M][H_kv][D] of the QKV projections: q_f16 [M][H][D], and rows pos0 ..
+ * pos0 + M - 1 of k_cache and v_cache [H_kv][L_max][D], all fp16; other cache
+ * rows are left as they were.  Token i is at position p = pos0 + i; pair j of
+ * the first n_rot dimensions of every q and k head turns by p * inv_freq[j]:
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin);
+ * the other dimensions, and v, are only rounded.  inv_freq: n_rot / 2 doubles
+ * in device memory (qk_rope_inv_freq makes them), so that the angle of a far
+ * position keeps its fraction of a turn.  D is a multiple of 8, at most 512;
+ * n_rot even, 0 .. D (0: nothing turns, inv_freq may be NULL); pos0 + M <=
+ * L_max < 2^31; H and H_kv at most 1024; magnitude finite.  No two buffers
+ * may overlap.  M = 0 is a no-op.
+ */
+qk_status qk_rope_kv_append(const float *q, const float *k, const float *v, const double *inv_freq, uint16_t *q_f16,
+                            uint16_t *k_cache, uint16_t *v_cache, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                            int64_t n_rot, int64_t pos0, int64_t L_max, int layout, float magnitude,
+                            qk_stream_t stream);
+
+/*
+ * Host-only: the rotation frequencies, in radians per position, into
+ * out[0 .. n_rot / 2 - 1] (host memory; the caller copies them to the device).
+ *   f_i = theta^(-2 i / n_rot) / freq_factors[i]  (freq_factors NULL: 1),
+ * then, by `scaling`:
+ *   QK_ROPE_SCALE_NONE    f_i
+ *   QK_ROPE_SCALE_LINEAR  f_i / factor
+ *   QK_ROPE_SCALE_BANDED  (1 - g) f_i / factor + g f_i, with
+ *     g = clamp((t_i - low_turns) / (high_turns - low_turns), 0, 1) and
+ *     t_i = original_len f_i / (2 pi), the turns of pair i over the context the
+ *     model was trained with: pairs of many turns keep their frequency, pairs
+ *     of few are slowed by `factor`.  (YaRN's ramp, Peng et al. 2023, has
+ *     low_turns 1 and high_turns 32, and a magnitude of 0.1 ln(factor) + 1 for
+ *     qk_rope_kv_append; Llama-3.2's own scaling low_turns 1 and high_turns 4.)
+ * theta and factor must be positive and finite, freq_factors positive and
+ * finite, high_turns > low_turns >= 0 and original_len > 0 where they are
+ * used, n_rot even and 0 .. 512; else QK_ERR_SHAPE.
+ */
+#define QK_ROPE_SCALE_NONE 0
+#define QK_ROPE_SCALE_LINEAR 1
+#define QK_ROPE_SCALE_BANDED 2
+typedef struct qk_rope_config {
+  double theta;
+  int scaling;
+  double factor;
+  double low_turns, high_turns;
+  int64_t original_len;
+  const float *freq_factors; /* host memory, n_rot / 2 values, or NULL */
+} qk_rope_config;
+
+qk_status qk_rope_inv_freq(const qk_rope_config *config, int64_t n_rot, double *out);
+
+/*
  * Grouped-query attention over a KV cache (DAMASCUS project overview, "[02]
  * the pipeline", compartment 06: a decoder layer is GQA with a KV cache; "[04]
  * one decode step": after the QKV projections and RoPE, attention over the
@@ -268,6 +377,46 @@ int64_t qk_rmsnorm_scratch_bytes(int qtype, int gateup, int64_t M, int64_t K);
 qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache, float *out,
                            int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0, int64_t L_max, float scale,
                            qk_stream_t stream);
+
+/*
+ * qk_gqa_attention with a sliding window and sinks, and an fp16 output that
+ * the O projection reads as it is: query i at position p = pos0 + i sees
+ * position j <= p when j > p - window or j < sinks (the window's last `window`
+ * positions, itself included, and the first `sinks` of the sequence).  window
+ * and sinks are >= 0; a window of at least pos0 + M is plain causal attention,
+ * and a query that sees nothing (window = sinks = 0) gives zeros.  Only the
+ * rows of the caches that some query of the call sees are used: rows between
+ * the sinks and the first query's window, and rows past the last query, may
+ * hold anything.  (A non-finite value in a row that only later queries of a
+ * prefill see can still reach the outputs of earlier queries.)  Other
+ * arguments, limits and errors as in qk_gqa_attention; out: [M][H][D] fp16,
+ * within about 2^-10 * max|v| of the exact value plus its own rounding.
+ */
+qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,
+                                  uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,
+                                  int64_t L_max, float scale, int64_t window, int64_t sinks, qk_stream_t stream);
+
+/*
+ * Log probabilities from the LM head's logits (the pages' "[02] the pipeline",
+ * compartments 06 and 07: the tied LM head's logits go to the sampler).  For
+ * each row m of logits fp32 [M][V], with lse = log sum_v exp(logits[m][v]):
+ *   logprob[m]          = logits[m][tokens[m]] - lse
+ *   entropy[m]          = lse - sum_v p_v logits[m][v],  p_v = exp(logits[m][v] - lse)
+ *   top_ids[m][i]       = the token of the i-th largest logit, i = 0 .. top_n - 1
+ *   top_logprobs[m][i]  = its log probability.
+ * Equal logits order by the lower token.  -inf logits (banned tokens) have
+ * probability 0 and add nothing to the entropy; NaN logits order below -inf.
+ * A row that holds NaN or +inf, or nothing but -inf, has NaN log probabilities
+ * and entropy; its top_ids are still the order above.  A token outside 0 ..
+ * V - 1 (padding) gives a NaN logprob.  logprob and tokens go together
+ * (both NULL: not wanted), so do top_ids and top_logprobs (top_n = 0); entropy
+ * may be NULL.  0 <= top_n <= 32 and top_n <= V; V below 2^31, M at most
+ * 2^31 - 1.  Rows need not be 16-byte aligned (any V), the buffers do.  No
+ * output may overlap another or an input.  M = 0 is a no-op; V = 0 is
+ * QK_ERR_SHAPE.
+ */
+qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob, float *entropy, int top_n,
+                      int32_t *top_ids, float *top_logprobs, int64_t M, int64_t V, qk_stream_t stream);
 
 /*
  * Synchronise `stream`, then report and clear the device-side status flags

@@ -22,7 +22,10 @@ __all__ = [
     "qk_decode_uses_gemv", "qk_uses_gemv", "qk_gemm_plan", "qk_rmsnorm_matmul_batch", "qk_rmsnorm_matmul_q4k",
     "qk_rmsnorm_matmul_q6k", "qk_rmsnorm_gateup_swiglu_q4k", "qk_rmsnorm_scratch_bytes",
     "qk_rmsnorm_matmul_batch_static", "qk_status_string", "qk_version", "QK_BLOCK_BYTES", "qk_matmul_desc",
-    "qk_gemm_plan_info", "qk_gqa_attention",
+    "qk_gemm_plan_info", "qk_gqa_attention", "qk_gqa_attention_window", "qk_matmul_batch_q8", "qk_matmul_q8_desc",
+    "qk_add_rmsnorm", "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_rope_config", "qk_logprobs",
+    "QK_F16", "QK_F32", "QK_ROPE_INTERLEAVED", "QK_ROPE_HALF", "QK_ROPE_SCALE_NONE", "QK_ROPE_SCALE_LINEAR",
+    "QK_ROPE_SCALE_BANDED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,9 +37,13 @@ SYMBOLS = ("qk_dequant_q4k", "qk_dequant_q6k", "qk_matmul_q4k", "qk_matmul_q6k",
            "qk_uses_gemv", "qk_gemm_plan", "qk_rmsnorm_matmul_batch", "qk_rmsnorm_matmul_q4k",
            "qk_rmsnorm_matmul_q6k", "qk_rmsnorm_gateup_swiglu_q4k", "qk_rmsnorm_scratch_bytes",
     "qk_rmsnorm_matmul_batch_static", "qk_status_string",
-           "qk_version", "qk_gqa_attention")
+           "qk_version", "qk_gqa_attention", "qk_gqa_attention_window", "qk_matmul_batch_q8", "qk_add_rmsnorm",
+           "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_logprobs")
 
 QK_Q4_K, QK_Q6_K = 0, 1
+QK_F16, QK_F32 = 0, 1
+QK_ROPE_INTERLEAVED, QK_ROPE_HALF = 0, 1
+QK_ROPE_SCALE_NONE, QK_ROPE_SCALE_LINEAR, QK_ROPE_SCALE_BANDED = 0, 1, 2
 
 
 class qk_matmul_desc(ctypes.Structure):
@@ -44,6 +51,20 @@ class qk_matmul_desc(ctypes.Structure):
     _fields_ = [("qtype", ctypes.c_int), ("blocks", ctypes.c_void_p), ("up_blocks", ctypes.c_void_p),
                 ("x_f16", ctypes.c_void_p), ("y", ctypes.c_void_p), ("M", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class qk_matmul_q8_desc(ctypes.Structure):
+    """Mirror of ``qk_matmul_q8_desc`` in include/qk.h."""
+    _fields_ = [("qtype", ctypes.c_int), ("blocks", ctypes.c_void_p), ("up_blocks", ctypes.c_void_p),
+                ("x_q8", ctypes.c_void_p), ("x_d", ctypes.c_void_p), ("y", ctypes.c_void_p), ("M", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class qk_rope_config(ctypes.Structure):
+    """Mirror of ``qk_rope_config`` in include/qk.h."""
+    _fields_ = [("theta", ctypes.c_double), ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("original_len", ctypes.c_int64),
+                ("freq_factors", ctypes.POINTER(ctypes.c_float))]
 
 
 class qk_gemm_plan_info(ctypes.Structure):
@@ -108,6 +129,20 @@ def lib():
         L.qk_gemm_plan.argtypes = [i32, i32, i64, i64, i64, ctypes.POINTER(qk_gemm_plan_info)]
         L.qk_gqa_attention.restype = i32
         L.qk_gqa_attention.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, f32, vp]
+        L.qk_gqa_attention_window.restype = i32
+        L.qk_gqa_attention_window.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, f32, i64, i64, vp]
+        L.qk_matmul_batch_q8.restype = i32
+        L.qk_matmul_batch_q8.argtypes = [ctypes.POINTER(qk_matmul_q8_desc), i32, vp]
+        L.qk_add_rmsnorm.restype = i32
+        L.qk_add_rmsnorm.argtypes = [vp, i32, vp, vp, f32, vp, vp, i64, i64, vp]
+        L.qk_add_rmsnorm_q8.restype = i32
+        L.qk_add_rmsnorm_q8.argtypes = [vp, i32, vp, vp, f32, vp, vp, vp, i64, i64, vp]
+        L.qk_rope_kv_append.restype = i32
+        L.qk_rope_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32, f32, vp]
+        L.qk_rope_inv_freq.restype = i32
+        L.qk_rope_inv_freq.argtypes = [ctypes.POINTER(qk_rope_config), i64, ctypes.POINTER(ctypes.c_double)]
+        L.qk_logprobs.restype = i32
+        L.qk_logprobs.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, vp]
         L.qk_status_string.restype, L.qk_status_string.argtypes = ctypes.c_char_p, [i32]
         L.qk_version.restype, L.qk_version.argtypes = i32, []
         _lib = L
@@ -117,6 +152,9 @@ def lib():
 # dtypes accepted for fp16 buffers (x, the SwiGLU output): fp16 itself or its bits
 _F16 = ("torch.float16", "torch.uint16", "torch.int16")
 _F32 = ("torch.float32",)
+_F64 = ("torch.float64",)
+_I8 = ("torch.int8",)
+_I32 = ("torch.int32",)
 
 
 def _buf(t, nbytes: int, what: str, dtypes=None) -> int:
@@ -251,6 +289,98 @@ def qk_matmul_q8x_q6k(blocks, x_f16, y, M: int, N: int, K: int, stream=None) -> 
     qk_matmul_batch_q8x([dict(qtype=QK_Q6_K, blocks=blocks, x_f16=x_f16, y=y, M=M, N=N, K=K)], stream)
 
 
+def qk_matmul_batch_q8(problems, stream=None) -> None:
+    """qk_matmul_batch_q8x for x that is in int8 already (see include/qk.h).  Each
+    problem is a dict with keys qtype, blocks, x_q8 (int8 [M][K]), x_d (fp32
+    [M][K / 32]), y, M, N, K and optionally up_blocks; M <= 1."""
+    arr = (qk_matmul_q8_desc * max(1, len(problems)))()
+    for i, p in enumerate(problems):
+        qt = p["qtype"]
+        qt = int({"q4k": QK_Q4_K, "q6k": QK_Q6_K}.get(qt, qt))
+        M, N, K = int(p["M"]), int(p["N"]), int(p["K"])
+        what = "qk_matmul_batch_q8[%d]" % i
+        up = p.get("up_blocks")
+        wb = _weight_bytes(qt, N, K)
+        arr[i] = qk_matmul_q8_desc(qt, _buf(p["blocks"], wb, what + ": blocks"), _buf(up, wb, what + ": up_blocks"),
+                                   _buf(p["x_q8"], _n(M) * _n(K), what + ": x_q8", _I8),
+                                   _buf(p["x_d"], _n(M) * (_n(K) // 32) * 4, what + ": x_d", _F32),
+                                   _buf(p["y"], _n(M) * _n(N) * (2 if up is not None else 4), what + ": y",
+                                        _F16 if up is not None else _F32), M, N, K)
+    _check(lib().qk_matmul_batch_q8(arr, len(problems), _stream(stream)), "qk_matmul_batch_q8")
+
+
+def _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K):
+    """Addresses and element type of an add_rmsnorm call's inputs and residual output."""
+    if residual_type is None:
+        if isinstance(residual, int) or residual is None:
+            raise ValueError("%s: residual_type is needed for a raw address" % what)
+        residual_type = QK_F32 if str(residual.dtype) in _F32 else QK_F16
+    n = _n(M) * _n(K)
+    types, size = (_F32, 4) if residual_type == QK_F32 else (_F16, 2)
+    return (_buf(residual, n * size, what + ": residual", types), int(residual_type),
+            _buf(delta, 4 * n, what + ": delta", _F32), _buf(gamma_f16, 2 * _n(K), what + ": gamma_f16", _F16),
+            _buf(residual_out, n * size, what + ": residual_out", types))
+
+
+def qk_add_rmsnorm(residual, delta, gamma_f16, eps: float, residual_out, xhat_f16, M: int, K: int,
+                   residual_type=None, stream=None) -> None:
+    """h = residual + delta, residual_out = h, xhat = fp16(RMSNorm(h) * gamma) (see
+    include/qk.h).  residual is fp16 or fp32 (residual_type QK_F16 / QK_F32, by
+    default the tensor's own); delta and residual_out may be None."""
+    what = "qk_add_rmsnorm"
+    r, t, d, g, o = _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K)
+    x = _buf(xhat_f16, 2 * _n(M) * _n(K), what + ": xhat_f16", _F16)
+    _check(lib().qk_add_rmsnorm(r, t, d, g, float(eps), o, x, int(M), int(K), _stream(stream)), what)
+
+
+def qk_add_rmsnorm_q8(residual, delta, gamma_f16, eps: float, residual_out, xq, xd, M: int, K: int,
+                      residual_type=None, stream=None) -> None:
+    """qk_add_rmsnorm with the activations in int8 (xq [M][K], xd fp32 [M][K / 32]):
+    the x of qk_matmul_batch_q8."""
+    what = "qk_add_rmsnorm_q8"
+    r, t, d, g, o = _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K)
+    q = _buf(xq, _n(M) * _n(K), what + ": xq", _I8)
+    s = _buf(xd, _n(M) * (_n(K) // 32) * 4, what + ": xd", _F32)
+    _check(lib().qk_add_rmsnorm_q8(r, t, d, g, float(eps), o, q, s, int(M), int(K), _stream(stream)), what)
+
+
+def qk_rope_inv_freq(n_rot: int, theta: float, scaling: int = QK_ROPE_SCALE_NONE, factor: float = 1.0,
+                     low_turns: float = 1.0, high_turns: float = 4.0, original_len: int = 8192,
+                     freq_factors=None) -> list:
+    """The n_rot / 2 rotation frequencies (radians per position) for
+    qk_rope_kv_append's inv_freq, as Python floats; host only (see include/qk.h)."""
+    half = _n(n_rot) // 2
+    ff = None
+    if freq_factors is not None:
+        ff = [float(f) for f in freq_factors]
+        if len(ff) < half:
+            raise ValueError("qk_rope_inv_freq: %d freq_factors, n_rot %d needs %d" % (len(ff), n_rot, half))
+        ff = (ctypes.c_float * max(1, len(ff)))(*ff)
+    cfg = qk_rope_config(float(theta), int(scaling), float(factor), float(low_turns), float(high_turns),
+                         int(original_len), ff)
+    out = (ctypes.c_double * max(1, half))()
+    _check(lib().qk_rope_inv_freq(ctypes.byref(cfg), int(n_rot), out), "qk_rope_inv_freq")
+    return list(out[:half])
+
+
+def qk_rope_kv_append(q, k, v, inv_freq, q_f16, k_cache, v_cache, M: int, H: int, H_kv: int, D: int, n_rot: int,
+                      pos0: int, L_max: int, layout: int = QK_ROPE_INTERLEAVED, magnitude: float = 1.0,
+                      stream=None) -> None:
+    """Rotary positions on the QKV projections' outputs and the new cache rows (see
+    include/qk.h): q, k, v fp32 [M][heads][D], inv_freq float64 [n_rot / 2], q_f16
+    [M][H][D] fp16, caches [H_kv][L_max][D] fp16."""
+    what = "qk_rope_kv_append"
+    qn, kn, cn = _n(M) * _n(H) * _n(D), _n(M) * _n(H_kv) * _n(D), _n(H_kv) * _n(L_max) * _n(D)
+    _check(lib().qk_rope_kv_append(_buf(q, 4 * qn, what + ": q", _F32), _buf(k, 4 * kn, what + ": k", _F32),
+                                   _buf(v, 4 * kn, what + ": v", _F32),
+                                   _buf(inv_freq, 4 * _n(n_rot), what + ": inv_freq", _F64),
+                                   _buf(q_f16, 2 * qn, what + ": q_f16", _F16),
+                                   _buf(k_cache, 2 * cn, what + ": k_cache", _F16),
+                                   _buf(v_cache, 2 * cn, what + ": v_cache", _F16), int(M), int(H), int(H_kv), int(D),
+                                   int(n_rot), int(pos0), int(L_max), int(layout), float(magnitude),
+                                   _stream(stream)), what)
+
+
 def qk_rmsnorm_scratch_bytes(qtype, M: int, K: int, gateup: bool = False) -> int:
     """Scratch bytes an M-token problem needs under the RMSNorm entry points
     (0 when the GEMV fuses the norm); host only."""
@@ -367,6 +497,38 @@ def qk_gqa_attention(q_f16, k_cache, v_cache, out, M: int, H: int, H_kv: int, D:
                                   _buf(v_cache, 2 * cn, what + ": v_cache", _F16),
                                   _buf(out, 4 * qn, what + ": out", _F32), int(M), int(H), int(H_kv), int(D),
                                   int(pos0), int(L_max), float(scale), _stream(stream)), what)
+
+
+def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_kv: int, D: int, pos0: int,
+                            L_max: int, scale: float, window: int, sinks: int = 0, stream=None) -> None:
+    """qk_gqa_attention with a sliding window of `window` positions and the first
+    `sinks` positions always visible (see include/qk.h); out [M][H][D] fp16."""
+    what = "qk_gqa_attention_window"
+    qn = _n(M) * _n(H) * _n(D)
+    cn = _n(H_kv) * _n(L_max) * _n(D)
+    _check(lib().qk_gqa_attention_window(_buf(q_f16, 2 * qn, what + ": q_f16", _F16),
+                                         _buf(k_cache, 2 * cn, what + ": k_cache", _F16),
+                                         _buf(v_cache, 2 * cn, what + ": v_cache", _F16),
+                                         _buf(out_f16, 2 * qn, what + ": out_f16", _F16), int(M), int(H), int(H_kv),
+                                         int(D), int(pos0), int(L_max), float(scale), int(window), int(sinks),
+                                         _stream(stream)), what)
+
+
+def qk_logprobs(logits, tokens, logprob, entropy, top_n: int, top_ids, top_logprobs, M: int, V: int,
+                stream=None) -> None:
+    """Log probabilities of given tokens, entropy and the top_n alternatives of each
+    row of logits fp32 [M][V] (see include/qk.h): tokens int32 [M], logprob and
+    entropy fp32 [M], top_ids int32 and top_logprobs fp32 [M][top_n].  tokens and
+    logprob may both be None, so may entropy, and top_ids and top_logprobs for
+    top_n = 0."""
+    what = "qk_logprobs"
+    m = 4 * _n(M)
+    _check(lib().qk_logprobs(_buf(logits, m * _n(V), what + ": logits", _F32),
+                             _buf(tokens, m, what + ": tokens", _I32), _buf(logprob, m, what + ": logprob", _F32),
+                             _buf(entropy, m, what + ": entropy", _F32), int(top_n),
+                             _buf(top_ids, m * _n(top_n), what + ": top_ids", _I32),
+                             _buf(top_logprobs, m * _n(top_n), what + ": top_logprobs", _F32), int(M), int(V),
+                             _stream(stream)), what)
 
 
 def qk_get_device_status(stream=None) -> None:

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <algorithm>
@@ -92,13 +93,75 @@ qk_status dequant(QType t, const void* blocks, int64_t n_blocks, float* out, cud
   return map_cuda(qk::launch_dequant(t, blocks, n_blocks, out, s));
 }
 
+// A buffer of a call: checked for NULL, alignment and accessibility, and every
+// output against every other buffer.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  bool output;
+};
+
+qk_status check_spans_host(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!s[i].p) return QK_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(s[i].p)) return QK_ERR_ALIGN;
+  return QK_OK;
+}
+
+qk_status check_spans_device(const Span* s, int n) {
+  qk_status st = check_device();
+  if (st != QK_OK) return st;
+  for (int i = 0; i < n; ++i)
+    if ((st = check_pointer(s[i].p)) != QK_OK) return st;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (i != j && s[i].output && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return QK_ERR_ALIAS;
+  return QK_OK;
+}
+
+// qk_add_rmsnorm (xhat set) and qk_add_rmsnorm_q8 (xq and xd set).
+qk_status add_rmsnorm(const void* residual, int type, const float* delta, const uint16_t* gamma, float eps,
+                      void* residual_out, uint16_t* xhat, int8_t* xq, float* xd, bool q8, int64_t M, int64_t K,
+                      cudaStream_t s) {
+  if (type != QK_F16 && type != QK_F32) return QK_ERR_SHAPE;
+  if (M < 0 || M >= kMaxDim || K <= 0 || K >= kMaxDim || K % (q8 ? 32 : 8) != 0) return QK_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return QK_ERR_SHAPE;  // finite, non-negative
+  if (M == 0) return QK_OK;
+  const int64_t n = M * K;  // < 2^62
+  int64_t bytes4;
+  if (!mul_ok(n, 4, &bytes4)) return QK_ERR_SHAPE;
+  const int64_t rbytes = type == QK_F32 ? bytes4 : 2 * n;
+  Span b[6];
+  int c = 0;
+  if (q8) {
+    b[c++] = {xq, n, true};
+    b[c++] = {xd, n / 8, true};
+  } else {
+    b[c++] = {xhat, 2 * n, true};
+  }
+  b[c++] = {gamma, 2 * K, false};
+  if (delta) b[c++] = {delta, bytes4, false};
+  b[c++] = {residual, rbytes, false};
+  if (residual_out && residual_out != residual) b[c++] = {residual_out, rbytes, true};
+  qk_status st = check_spans_host(b, c);
+  if (st == QK_OK) st = check_spans_device(b, c);
+  if (st != QK_OK) return st;
+  // in place the residual is an output too
+  if (residual_out == residual && (overlaps(residual, rbytes, gamma, 2 * K) ||
+                                   (delta && overlaps(residual, rbytes, delta, bytes4))))
+    return QK_ERR_ALIAS;
+  return map_cuda(qk::launch_add_rmsnorm(residual, type == QK_F32, delta, gamma, eps, residual_out, xhat, xq, xd, M, K,
+                                         s));
+}
+
 struct Checked {
   int64_t w_bytes, x_bytes, y_bytes;
 };
 
 // Host-only checks of one problem (no CUDA call); fills the byte extents.
 qk_status validate_host(QType t, const void* W, const void* W_up, const uint16_t* x, const void* y, int64_t M,
-                        int64_t N, int64_t K, bool gateup, Checked* c) {
+                        int64_t N, int64_t K, bool gateup, Checked* c, int x_size = 2) {
   if (M < 0 || N < 0 || K < 0) return QK_ERR_SHAPE;
   if (K == 0 || K % qk::kQK != 0) return QK_ERR_SHAPE;
   if (M > kMaxM || N >= kMaxDim || K >= kMaxDim) return QK_ERR_SHAPE;
@@ -111,7 +174,7 @@ qk_status validate_host(QType t, const void* W, const void* W_up, const uint16_t
   if (!aligned16(W) || !aligned16(x) || !aligned16(y) || (gateup && !aligned16(W_up))) return QK_ERR_ALIGN;
   int64_t x_elems, y_elems;
   if (!mul_ok(N, (K / qk::kQK) * qk::block_bytes(t), &c->w_bytes) || !mul_ok(M, K, &x_elems) ||
-      !mul_ok(x_elems, 2, &c->x_bytes) || !mul_ok(M, N, &y_elems) || !mul_ok(y_elems, gateup ? 2 : 4, &c->y_bytes))
+      !mul_ok(x_elems, x_size, &c->x_bytes) || !mul_ok(M, N, &y_elems) || !mul_ok(y_elems, gateup ? 2 : 4, &c->y_bytes))
     return QK_ERR_SHAPE;
   return QK_OK;
 }
@@ -154,14 +217,14 @@ qk_status matmul(QType t, const void* W, const void* W_up, const uint16_t* x, vo
 }
 
 // Host and device checks of a grouped call, including that no y overlaps
-// another entry's input or output.
-qk_status validate_batch(const qk_matmul_desc* d, int count, std::vector<Checked>& ck) {
+// another entry's input or output.  x_size: bytes of one activation.
+qk_status validate_batch(const qk_matmul_desc* d, int count, std::vector<Checked>& ck, int x_size = 2) {
   ck.assign((size_t)count, Checked{});
   for (int i = 0; i < count; ++i) {
     if (d[i].qtype != QK_Q4_K && d[i].qtype != QK_Q6_K) return QK_ERR_SHAPE;
     const QType t = d[i].qtype == QK_Q4_K ? qk::kQ4K : qk::kQ6K;
     const qk_status st = validate_host(t, d[i].blocks, d[i].up_blocks, d[i].x_f16, d[i].y, d[i].M, d[i].N, d[i].K,
-                                       d[i].up_blocks != nullptr, &ck[(size_t)i]);
+                                       d[i].up_blocks != nullptr, &ck[(size_t)i], x_size);
     if (st != QK_OK) return st;
   }
   for (int i = 0; i < count; ++i) {
@@ -329,7 +392,18 @@ qk_status qk_dequant_q6k(const void* blocks, int64_t n_blocks, float* out, qk_st
 
 // int8 activations: validated problems with M <= 1, all on the decode GEMV
 // (a problem it cannot stage is refused: there is no other int8 path).
-qk_status matmul_batch_q8x(const qk_matmul_desc* d, int count, cudaStream_t s) {
+static qk_status run_batch_q8(std::vector<qk::GemvDesc>& d, cudaStream_t s) {
+  for (const qk::GemvDesc& g : d)
+    if (!qk::gemv_plan_fits(&g, 1)) return QK_ERR_SHAPE;
+  for (size_t i = 0; i < d.size(); i += (size_t)qk::kMaxGemvProbs) {
+    const int n = (int)std::min(d.size() - i, (size_t)qk::kMaxGemvProbs);
+    const qk_status st = map_cuda(qk::launch_gemv_batch(&d[i], n, s));
+    if (st != QK_OK) return st;
+  }
+  return QK_OK;
+}
+
+static qk_status matmul_batch_q8x(const qk_matmul_desc* d, int count, cudaStream_t s) {
   if (count < 0) return QK_ERR_SHAPE;
   if (count == 0) return QK_OK;
   if (!d) return QK_ERR_NULL;
@@ -344,15 +418,9 @@ qk_status matmul_batch_q8x(const qk_matmul_desc* d, int count, cudaStream_t s) {
     qk::GemvDesc g{d[i].qtype == QK_Q4_K ? qk::kQ4K : qk::kQ6K, d[i].blocks, d[i].up_blocks, d[i].x_f16, d[i].y,
                    1, d[i].N, d[i].K, nullptr, 0.f};
     g.q8x = true;
-    if (!qk::gemv_plan_fits(&g, 1)) return QK_ERR_SHAPE;
     group.push_back(g);
-    if ((int)group.size() == qk::kMaxGemvProbs) {
-      if ((st = map_cuda(qk::launch_gemv_batch(group.data(), (int)group.size(), s))) != QK_OK) return st;
-      group.clear();
-    }
   }
-  if (!group.empty()) st = map_cuda(qk::launch_gemv_batch(group.data(), (int)group.size(), s));
-  return st;
+  return run_batch_q8(group, s);
 }
 
 qk_status qk_matmul_batch_q8x(const qk_matmul_desc* descs, int count, qk_stream_t stream) {
@@ -369,6 +437,40 @@ qk_status qk_matmul_q8x_q6k(const void* blocks, const uint16_t* x_f16, float* y,
                             qk_stream_t stream) {
   const qk_matmul_desc d{QK_Q6_K, blocks, nullptr, x_f16, y, M, N, K};
   return qk_matmul_batch_q8x(&d, 1, stream);
+}
+
+// x already in int8, with its scales.
+qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc* descs, int count, qk_stream_t stream) {
+  if (count < 0) return QK_ERR_SHAPE;
+  if (count == 0) return QK_OK;
+  if (!descs) return QK_ERR_NULL;
+  std::vector<qk_matmul_desc> d((size_t)count);
+  for (int i = 0; i < count; ++i) {
+    const qk_matmul_q8_desc& p = descs[i];
+    if (p.M > 1) return QK_ERR_SHAPE;
+    d[(size_t)i] = qk_matmul_desc{p.qtype, p.blocks, p.up_blocks, reinterpret_cast<const uint16_t*>(p.x_q8), p.y,
+                                  p.M, p.N, p.K};
+    if (p.M == 0 || p.N == 0) continue;
+    if (!p.x_d) return QK_ERR_NULL;
+    if (!aligned16(p.x_d)) return QK_ERR_ALIGN;
+  }
+  std::vector<Checked> ck;
+  qk_status st = validate_batch(d.data(), count, ck, 1);
+  if (st != QK_OK) return st;
+  std::vector<qk::GemvDesc> group;
+  for (int i = 0; i < count; ++i) {
+    const qk_matmul_q8_desc& p = descs[i];
+    if (p.M == 0 || p.N == 0) continue;
+    if ((st = check_pointer(p.x_d)) != QK_OK) return st;
+    for (int j = 0; j < count; ++j)
+      if (ck[(size_t)j].y_bytes && overlaps(descs[j].y, ck[(size_t)j].y_bytes, p.x_d, p.K / 8)) return QK_ERR_ALIAS;
+    qk::GemvDesc g{p.qtype == QK_Q4_K ? qk::kQ4K : qk::kQ6K, p.blocks, p.up_blocks, d[(size_t)i].x_f16, p.y,
+                   1, p.N, p.K, nullptr, 0.f};
+    g.q8x = true;
+    g.xd = p.x_d;
+    group.push_back(g);
+  }
+  return run_batch_q8(group, reinterpret_cast<cudaStream_t>(stream));
 }
 
 qk_status qk_matmul_q4k(const void* blocks, const uint16_t* x_f16, float* y, int64_t M, int64_t N, int64_t K,
@@ -483,6 +585,113 @@ qk_status qk_gqa_attention(const uint16_t* q_f16, const uint16_t* k_cache, const
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
+qk_status qk_gqa_attention_window(const uint16_t* q_f16, const uint16_t* k_cache, const uint16_t* v_cache,
+                                  uint16_t* out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,
+                                  int64_t L_max, float scale, int64_t window, int64_t sinks, qk_stream_t stream) {
+  if (M < 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || H / H_kv > 8 || D != 128 || pos0 < 0 || L_max <= 0 ||
+      M > L_max - pos0 || H > 1024 || L_max >= kMaxDim || window < 0 || sinks < 0 || M > kMaxM)
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  const int64_t q_bytes = M * H * D * 2, c_bytes = H_kv * L_max * D * 2;  // below 2^53
+  const Span b[4] = {{q_f16, q_bytes, false}, {k_cache, c_bytes, false}, {v_cache, c_bytes, false},
+                     {out_f16, q_bytes, true}};
+  qk_status st = check_spans_host(b, 4);
+  if (st == QK_OK) st = check_spans_device(b, 4);
+  if (st != QK_OK) return st;
+  return map_cuda(qk::launch_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M, (int)H, (int)H_kv, pos0, L_max,
+                                                  scale, window, sinks, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qk_status qk_add_rmsnorm(const void* residual, int residual_type, const float* delta, const uint16_t* gamma_f16,
+                         float eps, void* residual_out, uint16_t* xhat_f16, int64_t M, int64_t K, qk_stream_t stream) {
+  return add_rmsnorm(residual, residual_type, delta, gamma_f16, eps, residual_out, xhat_f16, nullptr, nullptr, false,
+                     M, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qk_status qk_add_rmsnorm_q8(const void* residual, int residual_type, const float* delta, const uint16_t* gamma_f16,
+                            float eps, void* residual_out, int8_t* xq, float* xd, int64_t M, int64_t K,
+                            qk_stream_t stream) {
+  return add_rmsnorm(residual, residual_type, delta, gamma_f16, eps, residual_out, nullptr, xq, xd, true, M, K,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+qk_status qk_rope_kv_append(const float* q, const float* k, const float* v, const double* inv_freq, uint16_t* q_f16,
+                            uint16_t* k_cache, uint16_t* v_cache, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                            int64_t n_rot, int64_t pos0, int64_t L_max, int layout, float magnitude,
+                            qk_stream_t stream) {
+  if (M < 0 || H <= 0 || H_kv <= 0 || H > 1024 || H_kv > 1024 || D <= 0 || D > 512 || D % 8 != 0 || n_rot < 0 ||
+      n_rot > D || n_rot % 2 != 0 || pos0 < 0 || L_max <= 0 || L_max >= kMaxDim || M > L_max - pos0 ||
+      (layout != QK_ROPE_INTERLEAVED && layout != QK_ROPE_HALF) || !std::isfinite(magnitude))
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  const int64_t qn = M * H * D, kn = M * H_kv * D, cn = H_kv * L_max * D;  // below 2^50
+  const Span b[7] = {{q, 4 * qn, false},      {k, 4 * kn, false},       {v, 4 * kn, false},      {q_f16, 2 * qn, true},
+                     {k_cache, 2 * cn, true}, {v_cache, 2 * cn, true}, {inv_freq, 4 * n_rot, false}};
+  const int nb = n_rot > 0 ? 7 : 6;
+  qk_status st = check_spans_host(b, nb);
+  if (st == QK_OK) st = check_spans_device(b, nb);
+  if (st != QK_OK) return st;
+  const qk::RopeArgs a{q, k, v, inv_freq, q_f16, k_cache, v_cache, M, pos0, L_max, (int)H, (int)H_kv, (int)D,
+                       (int)n_rot, layout == QK_ROPE_HALF ? 1 : 0, magnitude};
+  return map_cuda(qk::launch_rope_kv(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qk_status qk_rope_inv_freq(const qk_rope_config* c, int64_t n_rot, double* out) {
+  if (!c) return QK_ERR_NULL;
+  if (n_rot < 0 || n_rot > 512 || n_rot % 2 != 0) return QK_ERR_SHAPE;
+  auto positive = [](double x) { return x > 0 && std::isfinite(x); };
+  if (!positive(c->theta)) return QK_ERR_SHAPE;
+  if (c->scaling != QK_ROPE_SCALE_NONE && c->scaling != QK_ROPE_SCALE_LINEAR && c->scaling != QK_ROPE_SCALE_BANDED)
+    return QK_ERR_SHAPE;
+  if (c->scaling != QK_ROPE_SCALE_NONE && !positive(c->factor)) return QK_ERR_SHAPE;
+  if (c->scaling == QK_ROPE_SCALE_BANDED &&
+      (!(c->low_turns >= 0) || !(c->high_turns > c->low_turns) || !std::isfinite(c->high_turns) || c->original_len <= 0))
+    return QK_ERR_SHAPE;
+  if (n_rot > 0 && !out) return QK_ERR_NULL;
+  if (c->freq_factors)
+    for (int64_t i = 0; i < n_rot / 2; ++i)
+      if (!positive(c->freq_factors[i])) return QK_ERR_SHAPE;
+  for (int64_t i = 0; i < n_rot / 2; ++i) {
+    double f = std::pow(c->theta, -2.0 * (double)i / (double)n_rot);
+    if (c->freq_factors) f /= (double)c->freq_factors[i];
+    if (c->scaling == QK_ROPE_SCALE_LINEAR) {
+      f /= c->factor;
+    } else if (c->scaling == QK_ROPE_SCALE_BANDED) {
+      const double turns = (double)c->original_len * f / (2.0 * 3.14159265358979323846);
+      const double g = std::min(1.0, std::max(0.0, (turns - c->low_turns) / (c->high_turns - c->low_turns)));
+      f = (1.0 - g) * f / c->factor + g * f;
+    }
+    out[i] = f;
+  }
+  return QK_OK;
+}
+
+qk_status qk_logprobs(const float* logits, const int32_t* tokens, float* logprob, float* entropy, int top_n,
+                      int32_t* top_ids, float* top_logprobs, int64_t M, int64_t V, qk_stream_t stream) {
+  if (M < 0 || M >= kMaxDim || V <= 0 || V >= kMaxDim || top_n < 0 || top_n > 32 || top_n > V) return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  if ((tokens == nullptr) != (logprob == nullptr)) return QK_ERR_NULL;
+  int64_t bytes;
+  if (!mul_ok(M * V, 4, &bytes)) return QK_ERR_SHAPE;
+  Span b[6];
+  int c = 0;
+  b[c++] = {logits, bytes, false};
+  if (tokens) {
+    b[c++] = {tokens, 4 * M, false};
+    b[c++] = {logprob, 4 * M, true};
+  }
+  if (entropy) b[c++] = {entropy, 4 * M, true};
+  if (top_n > 0) {
+    b[c++] = {top_ids, 4 * M * top_n, true};
+    b[c++] = {top_logprobs, 4 * M * top_n, true};
+  }
+  qk_status st = check_spans_host(b, c);
+  if (st == QK_OK) st = check_spans_device(b, c);
+  if (st != QK_OK || c == 1) return st;
+  const qk::LogprobArgs a{logits, tokens, logprob, entropy, top_logprobs, top_ids, M, (int)V, top_n};
+  return map_cuda(qk::launch_logprobs(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 qk_status qk_get_device_status(qk_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QK_ERR_CUDA;
   const uint32_t v =
@@ -538,6 +747,6 @@ const char* qk_status_string(qk_status status) {
   }
 }
 
-int qk_version(void) { return 100; }
+int qk_version(void) { return 200; }
 
 }  // extern "C"

@@ -13,6 +13,11 @@
 // 0 .. pos0 + i); caches [H_kv][L_max][128] fp16, head-major, so one head's
 // positions are contiguous rows of 256 bytes; out [M][H][128] fp32.
 //
+// qk_gqa_attention_window: position j <= p is visible to position p when
+// j > p - window or j < sinks; out is fp16.  The same kernels with kWin: they
+// walk two runs of tiles, the sinks' and the window's, and never load a
+// position that no query of the CTA sees.
+//
 // Decode (M = 1): a cluster of C CTAs per key/value head splits the visible
 // positions into C ranges.  The G query heads of the group are the rows of
 // one 16-row MMA tile (mma.sync: the dot products are tiny next to the cache
@@ -126,32 +131,60 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// What qk_gqa_attention_window adds: the maps tm_k, tm_v start at the first
+// window position (decode) or at position 0 (prefill), tm_ks, tm_vs hold the
+// sinks alone, so that no other position can enter a tile.
+struct WinArgs {
+  int64_t window, sinks;  // prefill: as the call gives them; decode: positions in the window and sink maps
+  __half* out;
+};
+
 // One query token.  CTA rank r of the cluster for key/value head g takes
 // positions [r n / C, (r + 1) n / C) in 64-position tiles; its G query heads
 // are the rows of one 16-row MMA tile (rows past G are zero).  Warps 0-3 take
 // the even tiles and warps 4-7 the odd ones, warp w positions 16 (w % 4) ..
 // +15 of each; every warp keeps its own running max, sum and output.
+// kWin: the tiles are the sinks' (from tm_ks, tm_vs) and then the window's,
+// and the ranks split their list.
+template <bool kWin>
 __global__ void __launch_bounds__(kDecThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                        const __half* __restrict__ q, float* __restrict__ out, int G, int64_t n, float scale_log2e,
-                       int C) {
+                       int C, const WinArgs W) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   DecShared& S = *reinterpret_cast<DecShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 2, tq = lane & 3;
   const int g = blockIdx.y;
   const uint32_t rank = cluster_rank();
-  const int64_t j0 = (int64_t)rank * n / C, j1 = (int64_t)(rank + 1) * n / C;
-  const int nt = (int)((j1 - j0 + kPK - 1) / kPK);
+  int64_t j0 = 0, j1 = 0;
+  int nt, tile0 = 0, sink_tiles = 0;
+  if (kWin) {
+    sink_tiles = (int)((W.sinks + kPK - 1) / kPK);
+    const int64_t tiles = sink_tiles + (W.window + kPK - 1) / kPK;
+    tile0 = (int)((int64_t)rank * tiles / C);
+    nt = (int)((int64_t)(rank + 1) * tiles / C) - tile0;
+  } else {
+    j0 = (int64_t)rank * n / C;
+    j1 = (int64_t)(rank + 1) * n / C;
+    nt = (int)((j1 - j0 + kPK - 1) / kPK);
+  }
 
   auto issue = [&](int t) {
     const int s = t % kDecStages;
-    const int y = (int)(j0 + (int64_t)t * kPK);
+    int y = (int)(j0 + (int64_t)t * kPK);
+    const CUtensorMap *mk = &tm_k, *mv = &tm_v;
+    if (kWin) {
+      const bool sink = tile0 + t < sink_tiles;
+      y = (tile0 + t - (sink ? 0 : sink_tiles)) * kPK;
+      if (sink) mk = &tm_ks, mv = &tm_vs;
+    }
     mbar_arrive_expect_tx(&S.full[s], 2u * kPTile);
-    tma_load_3d(S.k[s], &tm_k, 0, y, g, &S.full[s]);
-    tma_load_3d(S.k[s] + kPBox, &tm_k, 64, y, g, &S.full[s]);
-    tma_load_3d(S.v[s], &tm_v, 0, y, g, &S.full[s]);
-    tma_load_3d(S.v[s] + kPBox, &tm_v, 64, y, g, &S.full[s]);
+    tma_load_3d(S.k[s], mk, 0, y, g, &S.full[s]);
+    tma_load_3d(S.k[s] + kPBox, mk, 64, y, g, &S.full[s]);
+    tma_load_3d(S.v[s], mv, 0, y, g, &S.full[s]);
+    tma_load_3d(S.v[s] + kPBox, mv, 64, y, g, &S.full[s]);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDecStages; ++s) {
@@ -222,7 +255,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         mma16816(sc[1], qa[kk], b[2], b[3]);
       }
       // scale; positions past this rank's range are the next rank's (or past n)
-      const int64_t key0 = j0 + (int64_t)t * kPK + 16 * slice;
+      int64_t key0 = j0 + (int64_t)t * kPK + 16 * slice;
+      if (kWin) {  // positions of the tile's map, which end at j1
+        const bool sink = tile0 + t < sink_tiles;
+        key0 = (int64_t)(tile0 + t - (sink ? 0 : sink_tiles)) * kPK + 16 * slice;
+        j1 = sink ? W.sinks : W.window;
+      }
       float tmax[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -319,7 +357,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         lsum = fmaf(c, S.red[r][row][1], lsum);
         acc = fmaf(c, S.red[r][row][2 + d], acc);
       }
-      out[(int64_t)(g * G + row) * kD + d] = acc / lsum;
+      if (kWin)
+        W.out[(int64_t)(g * G + row) * kD + d] = __float2half_rn(acc / lsum);
+      else
+        out[(int64_t)(g * G + row) * kD + d] = acc / lsum;
     }
   }
 }
@@ -386,10 +427,14 @@ __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int kk) {
 // shared memory), rescale of its part of O in tensor memory when the
 // max grew by more than 2^8, P = 2^(s - m) rounded to fp16 into tensor memory
 // (the A operand of P.V, two buffers), row sums.
+// kWin: the tiles are the sinks' and then those from the first position that
+// the block's first query sees; where sinks and window meet, one run from 0.
+template <bool kWin>
 __global__ void __launch_bounds__(kTThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v, float* __restrict__ out, int H, int G, int64_t M,
-                           int64_t pos0, float scale_log2e) {
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
+                           const __grid_constant__ CUtensorMap tm_vs, float* __restrict__ out, int H, int G, int64_t M,
+                           int64_t pos0, float scale_log2e, const WinArgs W) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   TcShared& S = *reinterpret_cast<TcShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -400,7 +445,29 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int h = (int)blockIdx.x, g = h / G;
   const int64_t q0 = (int64_t)qb * kTQ;
   const int64_t last_q = q0 + kTQ - 1 < M - 1 ? q0 + kTQ - 1 : M - 1;
-  const int nt = (int)((pos0 + last_q) / kTK) + 1;
+  int nt, sink_tiles = 0;
+  int64_t first = 0;  // kWin: the first position of the window's run of tiles
+  if (kWin) {
+    const int64_t last = pos0 + last_q;
+    first = pos0 + q0 - W.window + 1;
+    if (W.window == 0) {  // the sinks alone
+      sink_tiles = (int)(((W.sinks <= last ? W.sinks : last + 1) + kTK - 1) / kTK);
+      nt = sink_tiles;
+    } else {
+      if (first <= W.sinks)
+        first = 0;
+      else
+        sink_tiles = (int)((W.sinks + kTK - 1) / kTK);
+      nt = sink_tiles + (int)((last - first + kTK) / kTK);
+    }
+  } else {
+    nt = (int)((pos0 + last_q) / kTK) + 1;
+  }
+  // Position of the first row of tile t: in the sinks' map, or in the cache.
+  auto tile_pos = [&](int t) -> int64_t {
+    if (!kWin) return (int64_t)t * kTK;
+    return t < sink_tiles ? (int64_t)t * kTK : first + (int64_t)(t - sink_tiles) * kTK;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 1);
@@ -449,8 +516,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nk >= kTStages) ok = mbar_wait(&S.k_empty[st], (uint32_t)((nk >> 1) - 1) & 1u, abort_flag, &g_attn_status);
         if (!ok) return;
         mbar_arrive_expect_tx(&S.k_full[st], (uint32_t)kTTile);
-        tma_load_3d(S.k[st], &tm_k, 0, nk * kTK, g, &S.k_full[st]);
-        tma_load_3d(S.k[st] + kTBox, &tm_k, 64, nk * kTK, g, &S.k_full[st]);
+        const CUtensorMap* mk = kWin && nk < sink_tiles ? &tm_ks : &tm_k;
+        tma_load_3d(S.k[st], mk, 0, (int)tile_pos(nk), g, &S.k_full[st]);
+        tma_load_3d(S.k[st] + kTBox, mk, 64, (int)tile_pos(nk), g, &S.k_full[st]);
         ++nk;
       };
       auto issue_v = [&]() {
@@ -458,8 +526,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nv >= kTStages) ok = mbar_wait(&S.v_empty[st], (uint32_t)((nv >> 1) - 1) & 1u, abort_flag, &g_attn_status);
         if (!ok) return;
         mbar_arrive_expect_tx(&S.v_full[st], (uint32_t)kTTile);
-        tma_load_3d(S.v[st], &tm_v, 0, nv * kTK, g, &S.v_full[st]);
-        tma_load_3d(S.v[st] + kTBox, &tm_v, 64, nv * kTK, g, &S.v_full[st]);
+        const CUtensorMap* mv = kWin && nv < sink_tiles ? &tm_vs : &tm_v;
+        tma_load_3d(S.v[st], mv, 0, (int)tile_pos(nv), g, &S.v_full[st]);
+        tma_load_3d(S.v[st] + kTBox, mv, 64, (int)tile_pos(nv), g, &S.v_full[st]);
         ++nv;
       };
       issue_k();
@@ -534,15 +603,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint32_t t_s = tmem + lane_off + (uint32_t)(sb * kTK) + col0;
       if (ok) ok = mbar_wait(&S.s_full[sb], (uint32_t)(j >> 1) & 1u, abort_flag, &g_attn_status);
       ok = __all_sync(0xffffffffu, ok);
-      const int64_t key0 = (int64_t)j * kTK + col0;
-      // positions of this part the row sees: key0 .. key0 + lim - 1
-      const int64_t vis = qpos - key0 + 1;
-      const int lim = vis >= kTCols ? kTCols : (vis <= 0 ? 0 : (int)vis);
+      const int64_t key0 = tile_pos(j) + col0;
+      // positions of this part the row sees: key0 + e for e < lim, and with
+      // kWin also e >= from or e < sk
+      const bool sink = kWin && j < sink_tiles;
+      auto clamp = [](int64_t x) { return x >= kTCols ? kTCols : (x <= 0 ? 0 : (int)x); };
+      const int lim = clamp((sink && W.sinks <= qpos ? W.sinks : qpos + 1) - key0);
+      const int from = kWin && !sink ? clamp(qpos - W.window + 1 - key0) : 0;
+      const int sk = kWin && !sink ? clamp(W.sinks - key0) : 0;
+      auto sees = [&](int e) { return e < lim && (!kWin || e >= from || e < sk); };
       uint32_t v[kTCols];
       float pmax = -INFINITY;
       // Every position of this part is visible to every row of the warp (a
       // tile below the diagonal): the loops below skip the per-position mask.
-      const bool full = __all_sync(0xffffffffu, lim == kTCols);
+      const bool full = __all_sync(0xffffffffu, lim == kTCols && (!kWin || from <= sk));
       if (ok) {
         tc_fence_after();
 #pragma unroll
@@ -569,13 +643,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
           } else {
 #pragma unroll
             for (int e = 16 * c; e < 16 * c + 16; ++e)
-              if (e < lim) pm[c] = neg ? fminf(pm[c], __uint_as_float(v[e])) : fmaxf(pm[c], __uint_as_float(v[e]));
+              if (sees(e)) pm[c] = neg ? fminf(pm[c], __uint_as_float(v[e])) : fmaxf(pm[c], __uint_as_float(v[e]));
           }
         }
         float ext = pm[0];
 #pragma unroll
         for (int c = 1; c < kTCols / 16; ++c) ext = neg ? fminf(ext, pm[c]) : fmaxf(ext, pm[c]);
-        pmax = lim > 0 ? ext * scale_log2e : -INFINITY;
+        pmax = lim > 0 && (!kWin || from < lim || sk > 0) ? ext * scale_log2e : -INFINITY;
       }
       // S_j is in registers: its buffer may take S_{j+2}
       tc_fence_before();
@@ -590,10 +664,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // the weights 2^(s - m) then stay below 256 (fp16 holds them) and O is
       // rescaled rarely; O and l use the same reference, so the result is the
       // same softmax.  All parts of a row take the same decision.
-      const bool upd = m == -INFINITY || tmax > m + 8.0f;
+      // kWin: a row may see nothing of the tiles so far; its max stays -inf and
+      // its weights (all masked) are taken relative to 0.
+      const bool upd = (m == -INFINITY && (!kWin || tmax != -INFINITY)) || tmax > m + 8.0f;
       const float mn = upd ? tmax : m;
       const float corr = upd ? exp2f(m - mn) : 1.0f;
       m = mn;
+      const float mref = kWin && m == -INFINITY ? 0.f : m;
       // P buffer j % 2 is free once P_{j-2}.V_{j-2} is done.
       if (ok && j >= 2) ok = mbar_wait(&S.pv_done[j & 1], (uint32_t)((j >> 1) - 1) & 1u, abort_flag, &g_attn_status);
       ok = __all_sync(0xffffffffu, ok);
@@ -628,11 +705,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const int e0 = 32 * c + e;
-            float p0 = ex2_approx(fmaf(__uint_as_float(v[e0]), scale_log2e, -m));
-            float p1 = ex2_approx(fmaf(__uint_as_float(v[e0 + 1]), scale_log2e, -m));
+            float p0 = ex2_approx(fmaf(__uint_as_float(v[e0]), scale_log2e, -mref));
+            float p1 = ex2_approx(fmaf(__uint_as_float(v[e0 + 1]), scale_log2e, -mref));
             if (!full) {
-              p0 = e0 < lim ? p0 : 0.f;
-              p1 = e0 + 1 < lim ? p1 : 0.f;
+              p0 = sees(e0) ? p0 : 0.f;
+              p1 = sees(e0 + 1) ? p1 : 0.f;
             }
             lp[(e >> 4) & 1] += p0 + p1;
             hp[e >> 1] = pack_h2(p0, p1);
@@ -663,7 +740,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t v[16];
         tmem_ld16(tmem + lane_off + 256u + col0 + (uint32_t)(16 * c), v);
         tmem_wait_ld();
-        if (row < M) {
+        if (kWin && row < M) {
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = pack_h2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+          uint4* dst = reinterpret_cast<uint4*>(W.out + (row * H + h) * kD + col0 + 16 * c);
+          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        } else if (row < M) {
           float4* dst = reinterpret_cast<float4*>(out + (row * H + h) * kD + col0 + 16 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -694,29 +779,58 @@ uint32_t attn_take_status() {
   return v;
 }
 
-cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
-                                 int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s) {
+namespace {
+
+// W == null: qk_gqa_attention (out fp32); else the window and sinks, out in W.
+template <bool kWin>
+cudaError_t launch(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M, int H, int Hkv,
+                   int64_t pos0, int64_t Lmax, float scale, WinArgs W, cudaStream_t s) {
   const int G = H / Hkv;
   const float sl2e = scale * 1.4426950408889634f;
   const __half* qh = reinterpret_cast<const __half*>(q);
-  // Tensor maps over [H_kv][visible positions][128] of each cache: positions
-  // past the last query read as zero.
-  const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)(pos0 + M), (uint64_t)Hkv};
   const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)Lmax * kRowBytes};
+  const int box_rows = M == 1 ? kPK : kTK;
+  // Tensor maps over [H_kv][rows positions from `from`][128] of a cache: other
+  // positions read as zero.
+  auto encode = [&](CUtensorMap* tk, CUtensorMap* tv, int64_t from, int64_t rows) {
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)(rows > 0 ? rows : 1), (uint64_t)Hkv};
+    const uint32_t box[3] = {64u, (uint32_t)box_rows, 1u};
+    return encode_tensor_map_f16(tk, kc + from * kD, 3, dims, strides, box, true) &&
+           encode_tensor_map_f16(tv, vc + from * kD, 3, dims, strides, box, true);
+  };
+  alignas(64) CUtensorMap tk, tv, tks, tvs;
+  const int64_t end = pos0 + M;  // positions past the last query
+  if (kWin && M == 1) {
+    // the one query's window; a window that reaches the sinks takes them in
+    int64_t first = end - W.window;
+    if (first <= W.sinks) {
+      first = 0;
+      W.sinks = 0;
+      if (W.window == 0) {  // the sinks alone, all of them visible positions
+        W.sinks = end;
+        first = end;
+      }
+    }
+    W.window = end - first;
+    if (!encode(&tk, &tv, first < end ? first : 0, W.window)) return cudaErrorInvalidValue;
+  } else if (!encode(&tk, &tv, 0, end)) {
+    return cudaErrorInvalidValue;
+  }
+  if (kWin && W.sinks > 0) {
+    if (!encode(&tks, &tvs, 0, W.sinks < end ? W.sinks : end)) return cudaErrorInvalidValue;
+  } else {
+    tks = tk;
+    tvs = tv;
+  }
+  const int dev = current_device();
   if (M == 1) {
-    const uint32_t box[3] = {64u, (uint32_t)kPK, 1u};
-    alignas(64) CUtensorMap tk, tv;
-    if (!encode_tensor_map_f16(&tk, kc, 3, dims, strides, box, true) ||
-        !encode_tensor_map_f16(&tv, vc, 3, dims, strides, box, true))
-      return cudaErrorInvalidValue;
     // Decode: a cluster of C CTAs per key/value head, at least 256 positions each.
-    const int64_t n = pos0 + 1;
+    const int64_t n = kWin ? W.window + W.sinks : end;
     int C = (int)((n + 255) / 256);
     C = C < 1 ? 1 : (C > kDecMaxCluster ? kDecMaxCluster : C);
     static PerDeviceFlag attr_set;
-    const int dev = current_device();
     if (!attr_set.done(dev)) {
-      const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)dec_smem());
       if (e != cudaSuccess) return e;
       attr_set.mark(dev);
@@ -734,33 +848,42 @@ cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const ui
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel, tk, tv, qh, out, G, n, sl2e, C);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<kWin>, tk, tv, tks, tvs, qh, out, G, n, sl2e, C, W);
   }
-  {
-    // Q: [M][H][128] as a 3-D map {128, H, M}; a box is 64 dims of one head for 128 queries.
-    const uint64_t qd[3] = {(uint64_t)kD, (uint64_t)H, (uint64_t)M};
-    const uint64_t qs[2] = {(uint64_t)kRowBytes, (uint64_t)H * kRowBytes};
-    const uint32_t qbox[3] = {64u, 1u, (uint32_t)kTQ};
-    const uint32_t kvbox[3] = {64u, (uint32_t)kTK, 1u};
-    alignas(64) CUtensorMap tq, tk, tv;
-    if (!encode_tensor_map_f16(&tq, q, 3, qd, qs, qbox, true) ||
-        !encode_tensor_map_f16(&tk, kc, 3, dims, strides, kvbox, true) ||
-        !encode_tensor_map_f16(&tv, vc, 3, dims, strides, kvbox, true))
-      return cudaErrorInvalidValue;
-    static PerDeviceFlag attr_set;
-    const int dev = current_device();
-    if (!attr_set.done(dev)) {
-      const cudaError_t e = cudaFuncSetAttribute(attn_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)tc_smem());
-      if (e != cudaSuccess) return e;
-      attr_set.mark(dev);
-    }
-    const int64_t nqb = (M + kTQ - 1) / kTQ;
-    if (nqb > 65535) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)H, (unsigned)nqb);
-    attn_prefill_tc_kernel<<<grid, kTThreads, tc_smem(), s>>>(tq, tk, tv, out, H, G, M, pos0, sl2e);
-    return cudaGetLastError();
+  // Q: [M][H][128] as a 3-D map {128, H, M}; a box is 64 dims of one head for 128 queries.
+  const uint64_t qd[3] = {(uint64_t)kD, (uint64_t)H, (uint64_t)M};
+  const uint64_t qs[2] = {(uint64_t)kRowBytes, (uint64_t)H * kRowBytes};
+  const uint32_t qbox[3] = {64u, 1u, (uint32_t)kTQ};
+  alignas(64) CUtensorMap tq;
+  if (!encode_tensor_map_f16(&tq, q, 3, qd, qs, qbox, true)) return cudaErrorInvalidValue;
+  static PerDeviceFlag attr_set;
+  if (!attr_set.done(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_prefill_tc_kernel<kWin>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem());
+    if (e != cudaSuccess) return e;
+    attr_set.mark(dev);
   }
+  const int64_t nqb = (M + kTQ - 1) / kTQ;
+  if (nqb > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)H, (unsigned)nqb);
+  attn_prefill_tc_kernel<kWin><<<grid, kTThreads, tc_smem(), s>>>(tq, tk, tv, tks, tvs, out, H, G, M, pos0, sl2e, W);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
+                                 int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s) {
+  return launch<false>(q, kc, vc, out, M, H, Hkv, pos0, Lmax, scale, WinArgs{0, 0, nullptr}, s);
+}
+
+cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out,
+                                        int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
+                                        int64_t window, int64_t sinks, cudaStream_t s) {
+  if (window == 0 && sinks == 0) return cudaMemsetAsync(out, 0, (size_t)M * H * kRowBytes, s);  // nothing is visible
+  const int64_t end = pos0 + M;
+  const WinArgs W{window < end ? window : end, sinks < end ? sinks : end, reinterpret_cast<__half*>(out)};
+  return launch<true>(q, kc, vc, nullptr, M, H, Hkv, pos0, Lmax, scale, W, s);
 }
 
 }  // namespace qk

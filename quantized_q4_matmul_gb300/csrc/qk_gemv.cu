@@ -550,6 +550,7 @@ struct GemvProb {
   int M;                // tokens (1 for the decode layout)
   const uint16_t* gamma;  // RMSNorm prologue: fp16 gamma[K], or null for none
   float eps;
+  const float* xd;      // int8 x given with its scales: x points at K int8 values, xd at K / 32 scales
   int N, K, qtype, kind;
   int pair;             // one tensor, whole rows: a stage holds two adjacent 16-row tiles
   int cb;               // K blocks per chunk (a stage holds 16 rows x cb blocks per weight tensor)
@@ -775,6 +776,21 @@ __device__ void build_x_table_q8(uint32_t xs, int K, uint32_t xq, uint32_t dt, i
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(dt + 16u * (uint32_t)b + 8u), "f"((float)s), "f"(0.0f)
                    : "memory");
     }
+  }
+}
+
+// The table's scales and sums for x that came in int8 (its values are in place
+// at xq, its K / 32 scales at xd): one thread per block of 32, two 16-byte
+// loads, the sums as dot products with ones.
+__device__ void build_x_sums_q8(uint32_t xd, int K, uint32_t xq, uint32_t dt, int tid) {
+  for (int b = tid; b < K / 32; b += kDCompute) {
+    const uint4 u = lds128(xq + 32u * (uint32_t)b), w = lds128(xq + 32u * (uint32_t)b + 16u);
+    uint32_t d;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(d) : "r"(xd + 4u * (uint32_t)b));
+    constexpr uint32_t kOnes = 0x01010101u;
+    const int s0 = dp4a_us(kOnes, u.x, dp4a_us(kOnes, u.y, dp4a_us(kOnes, u.z, dp4a_us(kOnes, u.w, 0))));
+    const int s1 = dp4a_us(kOnes, w.x, dp4a_us(kOnes, w.y, dp4a_us(kOnes, w.z, dp4a_us(kOnes, w.w, 0))));
+    sts128_u(dt + 16u * (uint32_t)b, d, __float_as_uint((float)s0), __float_as_uint((float)s1), 0u);
   }
 }
 
@@ -1018,10 +1034,18 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
     if (lane == 0) {
       // one token: x lands in its own buffer for the x-table build; several:
       // x lands in the table area and is rearranged in place
-      const uint32_t xbytes = (uint32_t)(2 * K) * (uint32_t)M, gbytes = P.gamma ? (uint32_t)(2 * K) : 0u;
-      mbar_arrive_expect_tx(&ctl->x_full, xbytes + gbytes);
-      bulk_copy_g2s(smem + P.rawx_off, P.x, xbytes, &ctl->x_full);
-      if (gbytes) bulk_copy_g2s(smem + P.gamma_off, P.gamma, gbytes, &ctl->x_full);
+      if (Q8X && P.xd) {
+        // x in int8: the values land where the x table wants them, the scales beside
+        const uint32_t qbytes = (uint32_t)K, dbytes = (uint32_t)(K / 8);
+        mbar_arrive_expect_tx(&ctl->x_full, qbytes + dbytes);
+        bulk_copy_g2s(smem, P.x, qbytes, &ctl->x_full);
+        bulk_copy_g2s(smem + P.rawx_off, P.xd, dbytes, &ctl->x_full);
+      } else {
+        const uint32_t xbytes = (uint32_t)(2 * K) * (uint32_t)M, gbytes = P.gamma ? (uint32_t)(2 * K) : 0u;
+        mbar_arrive_expect_tx(&ctl->x_full, xbytes + gbytes);
+        bulk_copy_g2s(smem + P.rawx_off, P.x, xbytes, &ctl->x_full);
+        if (gbytes) bulk_copy_g2s(smem + P.gamma_off, P.gamma, gbytes, &ctl->x_full);
+      }
     }
     for (int st = 0; st < steps; ++st) {
       const int s = st % S;
@@ -1071,9 +1095,12 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kDCompute) : "memory");
   }
-  if constexpr (Q8X)
-    build_x_table_q8(xs, K, base, base + (uint32_t)K, tid);
-  else if constexpr (MT == 1)
+  if constexpr (Q8X) {
+    if (P.xd)
+      build_x_sums_q8(xs, K, base, base + (uint32_t)K, tid);
+    else
+      build_x_table_q8(xs, K, base, base + (uint32_t)K, tid);
+  } else if constexpr (MT == 1)
     build_x_table<QT>(xs, gs, ctl->rnorm, K, base, sxt, zero, tid);
   else
     build_x_table_tn<QT, MT>(gs, ctl->rnorm, M, K, base, sxt, zero, tid);
@@ -1304,6 +1331,7 @@ bool plan_decode_problem(const GemvDesc& d, GemvProb& P, size_t* smem_out) {
   P.M = (int)d.M;
   P.gamma = d.gamma;
   P.eps = d.eps;
+  P.xd = d.xd;
   P.N = (int)d.N;
   P.K = (int)d.K;
   P.qtype = d.qtype;

@@ -71,6 +71,34 @@ bool gemm_plan(QType t, bool gateup, int64_t M, int64_t N, GemmPlanInfo* info);
 cudaError_t launch_rmsnorm_rows(const uint16_t* x, const uint16_t* gamma, float eps, uint16_t* out, int64_t M,
                                 int64_t K, cudaStream_t s);
 
+// Residual addition + RMSNorm (qk_add_rmsnorm: xhat set; qk_add_rmsnorm_q8: xq
+// and xd set); arguments validated.
+cudaError_t launch_add_rmsnorm(const void* residual, bool f32, const float* delta, const uint16_t* gamma, float eps,
+                               void* residual_out, uint16_t* xhat, int8_t* xq, float* xd, int64_t M, int64_t K,
+                               cudaStream_t s);
+
+// Rotary positions and the KV-cache rows (qk_rope_kv_append); arguments validated.
+struct RopeArgs {
+  const float *q, *k, *v;
+  const double* inv_freq;
+  uint16_t *q_out, *k_cache, *v_cache;
+  int64_t M, pos0, Lmax;
+  int H, Hkv, D, n_rot, half;
+  float magnitude;
+};
+cudaError_t launch_rope_kv(const RopeArgs& a, cudaStream_t s);
+
+// Log probabilities, entropy and top alternatives (qk_logprobs); arguments validated.
+struct LogprobArgs {
+  const float* logits;
+  const int32_t* tokens;
+  float *logprob, *entropy, *top_logprobs;
+  int32_t* top_ids;
+  int64_t M;
+  int V, top_n;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
+
 // The built-in scratch of qk_rmsnorm_matmul_batch_static (bytes) and its
 // device address on the current device (looked up once per device).
 constexpr size_t kStaticScratchBytes = size_t(8) << 20;
@@ -86,6 +114,10 @@ bool encode_tensor_map_f16(void* out, const void* base, int rank, const uint64_t
 // GQA attention (qk_gqa_attention); arguments validated.  Device status word.
 cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
                                  int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s);
+// The same with a window and sinks, fp16 out (qk_gqa_attention_window).
+cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out,
+                                        int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
+                                        int64_t window, int64_t sinks, cudaStream_t s);
 uint32_t attn_take_status();
 
 // A kernel whose single bounded wait can never complete (see qk_debug_wait_timeout).
@@ -113,6 +145,7 @@ struct GemvDesc {
   const uint16_t* gamma;  // RMSNorm prologue over x (fp16 gamma[K]), or null
   float eps;
   bool q8x = false;       // x quantized to int8 per block of 32 (one token, no gamma)
+  const float* xd = nullptr;  // q8x with x given in int8: x points at the values, xd at their K / 32 scales
 };
 cudaError_t launch_gemv_batch(const GemvDesc* d, int count, cudaStream_t s);
 

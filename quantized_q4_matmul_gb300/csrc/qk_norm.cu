@@ -97,7 +97,176 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_rows_kernel(const uint16
   for (int c = tid + kNormChunks * kNormThreads; c < nc; c += kNormThreads) emit(c, ldg_stream16(x + row + 8 * c));
 }
 
+// ---------------------------------------------------------------------------
+// Residual addition + RMSNorm
+// ---------------------------------------------------------------------------
+// h = residual + delta (fp32), residual_out = h in the residual's type, and
+// xhat = fp16(h * r * gamma), r = 1 / sqrt(mean h^2 + eps), taken from the
+// unrounded h; or xhat in int8 with a scale per 32 values.  One CTA per row: a
+// thread keeps 8-value chunks of h in registers, so each input is read once.
+struct AddNormArgs {
+  const void* res;
+  const float* delta;
+  const uint16_t* gamma;
+  void* res_out;
+  uint16_t* xhat;
+  int8_t* xq;
+  float* xd;
+  float eps;
+  int K;
+};
+
+// 16-byte load that may read what this kernel also writes (the residual in
+// place): not through the read-only path.
+__device__ __forceinline__ uint4 ldg16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_h(const AddNormArgs& A, size_t at, float (&h)[8]) {
+  if (F32) {
+    const float* p = static_cast<const float*>(A.res) + at;
+    const uint4 a = ldg16(p), b = ldg16(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __uint_as_float(w[i]);
+  } else {
+    const uint4 a = ldg16(static_cast<const uint16_t*>(A.res) + at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[2 * i] = hlo(w[i]);
+      h[2 * i + 1] = hlo(w[i] >> 16);
+    }
+  }
+  if (A.delta) {
+    const uint4 a = ldg_stream16(A.delta + at), b = ldg_stream16(A.delta + at + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += __uint_as_float(w[i]);
+  }
+}
+
+// Writes one chunk: the residual, and the normalized values in fp16 or int8.
+// Every lane of the warp calls this (the int8 scales are maxima over 4 lanes);
+// `on` is false for lanes past the row's end.
+template <bool F32, bool Q8>
+__device__ __forceinline__ void emit_h(const AddNormArgs& A, size_t row, int c, bool on, const float (&h)[8], float r) {
+  const size_t at = row + 8 * (size_t)c;
+  uint32_t x[4] = {0u, 0u, 0u, 0u};
+  if (on) {
+    if (A.res_out) {
+      if (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(A.res_out) + at);
+        o[0] = make_float4(h[0], h[1], h[2], h[3]);
+        o[1] = make_float4(h[4], h[5], h[6], h[7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.res_out) + at) =
+            make_uint4(h2pack(h[0], h[1]), h2pack(h[2], h[3]), h2pack(h[4], h[5]), h2pack(h[6], h[7]));
+      }
+    }
+    const uint4 g = ldg_stream16(A.gamma + 8 * c);
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = h2pack(h[2 * i] * r * hlo(gw[i]), h[2 * i + 1] * r * hlo(gw[i] >> 16));
+    if (!Q8) *reinterpret_cast<uint4*>(A.xhat + at) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  if (Q8) {
+    float v[8], a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = hlo(x[i]);
+      v[2 * i + 1] = hlo(x[i] >> 16);
+      a = fmaxf(a, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+    }
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const float d = __fdiv_rn(a, 127.0f);
+    if (on) {
+      uint32_t q[2] = {0u, 0u};
+      if (d != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int b = (int)fminf(fmaxf(roundf(__fdiv_rn(v[i], d)), -127.0f), 127.0f);
+          q[i >> 2] |= ((uint32_t)b & 0xFFu) << (8 * (i & 3));
+        }
+      }
+      *reinterpret_cast<uint2*>(A.xq + at) = make_uint2(q[0], q[1]);
+      if ((c & 3) == 0) A.xd[at / 32] = d;
+    }
+  }
+}
+
+template <bool F32, bool Q8>
+__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_kernel(const __grid_constant__ AddNormArgs A) {
+  __shared__ float wsum[kNormThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const size_t row = (size_t)blockIdx.x * (size_t)A.K;
+  const int nc = A.K / 8;
+  float h[kNormChunks][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNormChunks; ++i) {
+    const int c = tid + i * kNormThreads;
+    if (c < nc) {
+      load_h<F32>(A, row + 8 * (size_t)c, h[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    }
+  }
+  // longer rows: the remaining chunks, read again in the second pass (a thread
+  // writes only chunks that it alone reads, after reading them: in place is fine)
+  for (int c = tid + kNormChunks * kNormThreads; c < nc; c += kNormThreads) {
+    float t[8];
+    load_h<F32>(A, row + 8 * (size_t)c, t);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(t[e], t[e], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) wsum[warp] = ss;
+  __syncthreads();
+  float t = 0.f;
+  for (int w = 0; w < kNormThreads / 32; ++w) t += wsum[w];
+  const float r = 1.0f / sqrtf(t / (float)A.K + A.eps);
+#pragma unroll
+  for (int i = 0; i < kNormChunks; ++i) {
+    const int c0 = i * kNormThreads + 32 * warp;  // the warp's first chunk: the warp stays together
+    if (c0 < nc) emit_h<F32, Q8>(A, row, c0 + lane, c0 + lane < nc, h[i], r);
+  }
+  for (int c0 = kNormChunks * kNormThreads + 32 * warp; c0 < nc; c0 += kNormThreads) {
+    float u[8];
+    if (c0 + lane < nc) load_h<F32>(A, row + 8 * (size_t)(c0 + lane), u);
+    emit_h<F32, Q8>(A, row, c0 + lane, c0 + lane < nc, u, r);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_add_rmsnorm(const void* residual, bool f32, const float* delta, const uint16_t* gamma, float eps,
+                               void* residual_out, uint16_t* xhat, int8_t* xq, float* xd, int64_t M, int64_t K,
+                               cudaStream_t s) {
+  const AddNormArgs A{residual, delta, gamma, residual_out, xhat, xq, xd, eps, (int)K};
+  const dim3 grid((unsigned)M);
+  if (xq) {
+    if (f32)
+      add_rmsnorm_kernel<true, true><<<grid, kNormThreads, 0, s>>>(A);
+    else
+      add_rmsnorm_kernel<false, true><<<grid, kNormThreads, 0, s>>>(A);
+  } else {
+    if (f32)
+      add_rmsnorm_kernel<true, false><<<grid, kNormThreads, 0, s>>>(A);
+    else
+      add_rmsnorm_kernel<false, false><<<grid, kNormThreads, 0, s>>>(A);
+  }
+  return cudaGetLastError();
+}
 
 // Scratch of qk_rmsnorm_matmul_batch_static, the entry point that allocates
 // nothing: the normalized activations of the problems the tensor-core GEMM
