@@ -388,8 +388,8 @@ qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const
  * rows of the caches that some query of the call sees are used: rows between
  * the sinks and the first query's window, and rows past the last query, may
  * hold anything.  (A non-finite value in a row that only later queries of a
- * prefill see can still reach the outputs of earlier queries.)  Other
- * arguments, limits and errors as in qk_gqa_attention; out: [M][H][D] fp16,
+ * prefill see can still reach the outputs of earlier queries.)  scale is
+ * finite.  Other arguments, limits and errors as in qk_gqa_attention; out: [M][H][D] fp16,
  * within about 2^-10 * max|v| of the exact value plus its own rounding.
  */
 qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,

@@ -589,7 +589,8 @@ qk_status qk_gqa_attention_window(const uint16_t* q_f16, const uint16_t* k_cache
                                   uint16_t* out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,
                                   int64_t L_max, float scale, int64_t window, int64_t sinks, qk_stream_t stream) {
   if (M < 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || H / H_kv > 8 || D != 128 || pos0 < 0 || L_max <= 0 ||
-      M > L_max - pos0 || H > 1024 || L_max >= kMaxDim || window < 0 || sinks < 0 || M > kMaxM)
+      M > L_max - pos0 || H > 1024 || L_max >= kMaxDim || window < 0 || sinks < 0 || M > kMaxM ||
+      !std::isfinite(scale))
     return QK_ERR_SHAPE;
   if (M == 0) return QK_OK;
   const int64_t q_bytes = M * H * D * 2, c_bytes = H_kv * L_max * D * 2;  // below 2^53
@@ -695,7 +696,8 @@ qk_status qk_logprobs(const float* logits, const int32_t* tokens, float* logprob
 qk_status qk_get_device_status(qk_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QK_ERR_CUDA;
   const uint32_t v =
-      qk::dequant_take_status() | qk::gemv_take_status() | qk::gemm_take_status() | qk::attn_take_status();
+      qk::dequant_take_status() | qk::gemv_take_status() | qk::gemm_take_status() | qk::attn_take_status() |
+      qk::attn_win_take_status();
   if (v & QK_DEV_BAD_COPY) return QK_ERR_BAD_COPY;
   return v ? QK_ERR_TIMEOUT : QK_OK;
 }

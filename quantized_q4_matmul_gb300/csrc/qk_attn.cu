@@ -13,10 +13,10 @@
 // 0 .. pos0 + i); caches [H_kv][L_max][128] fp16, head-major, so one head's
 // positions are contiguous rows of 256 bytes; out [M][H][128] fp32.
 //
-// qk_gqa_attention_window: position j <= p is visible to position p when
-// j > p - window or j < sinks; out is fp16.  The same kernels with kWin: they
-// walk two runs of tiles, the sinks' and the window's, and never load a
-// position that no query of the CTA sees.
+// A decode step of qk_gqa_attention_window (position j <= p is visible to
+// position p when j > p - window or j < sinks; out fp16) is the decode kernel
+// with kWin: it walks two runs of tiles, the sinks' and the window's, and never
+// loads another position.  Its prefill is in qk_attn_win.cu.
 //
 // Decode (M = 1): a cluster of C CTAs per key/value head splits the visible
 // positions into C ranges.  The G query heads of the group are the rows of
@@ -43,6 +43,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "qk_attn.cuh"
 #include "qk_device.cuh"
 #include "qk_internal.h"
 
@@ -52,17 +53,8 @@ __device__ uint32_t g_attn_status = 0;
 
 namespace {
 
-constexpr int kD = 128;               // head dimension
-constexpr int kRowBytes = kD * 2;     // one position of one head, fp16
-constexpr int kMaxGroup = 8;          // query heads per key/value head
 
 
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 
 // ---------------------------------------------------------------------------
 // Tiles and warp-level MMA helpers (decode)
@@ -71,43 +63,10 @@ constexpr int kPK = 64;                                // positions per key / va
 constexpr int kPBox = kPK * 128;                       // one 64-dim box: 64 rows x 128 bytes
 constexpr int kPTile = 2 * kPBox;                      // 16 KB: a key or value tile
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
 // Shared address of 16-byte chunk c (dims 8c .. 8c+7) of row r of a tile
 // stored as two 128-byte-swizzled 64-dim boxes.
 __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c) {
   return base + (uint32_t)((c >> 3) * kPBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-// 2^x with the hardware approximation (relative error about 2^-22, far below
-// the fp16 rounding the weights get next; subnormal results flush to zero).
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // ---------------------------------------------------------------------------
@@ -131,11 +90,10 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// What qk_gqa_attention_window adds: the maps tm_k, tm_v start at the first
-// window position (decode) or at position 0 (prefill), tm_ks, tm_vs hold the
-// sinks alone, so that no other position can enter a tile.
+// What qk_gqa_attention_window adds: the maps tm_k, tm_v hold the positions of
+// the window, tm_ks, tm_vs the sinks, so that no other position can enter a tile.
 struct WinArgs {
-  int64_t window, sinks;  // prefill: as the call gives them; decode: positions in the window and sink maps
+  int64_t window, sinks;  // positions in the window's and the sinks' maps
   __half* out;
 };
 
@@ -370,8 +328,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kTQ = 128;                   // queries per CTA (UMMA M)
 constexpr int kTK = 128;                   // positions per key / value tile
-constexpr int kTBox = 128 * 128;           // one 64-wide box of 128 rows of 128 bytes: 16 KB
-constexpr int kTTile = 2 * kTBox;          // 32 KB: Q, one key or value tile, or P
 constexpr int kTStages = 2;
 constexpr int kTParts = 2;                 // softmax warps per TMEM lane quarter (each takes kTCols positions)
 constexpr int kTCols = kTK / kTParts;      // 32 positions of S (and columns of O) per softmax thread
@@ -398,27 +354,6 @@ struct TcShared {
   uint32_t abort_flag;
 };
 
-// UMMA shared-memory descriptor of 16-wide K slice kk (0..7) of a K-major tile
-// stored as two 64-wide boxes of 128 rows with the 128-byte swizzle.
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk) {
-  return umma_desc_sw128(tile + (uint32_t)((kk >> 2) * kTBox)) + (uint64_t)(2 * (kk & 3));
-}
-
-// The same for an MN-major operand (N contiguous): rows are K (positions) of
-// 128 bytes = 64 N; the two 64-wide N atoms are kTBox apart (leading byte
-// offset) and groups of 8 rows 1024 bytes apart (stride byte offset); slice kk
-// starts 16 rows further on.
-__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int kk) {
-  const uint32_t a = tile + (uint32_t)(kk * 16 * 128);
-  uint64_t d = 0;
-  d |= (uint64_t)((a & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kTBox >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 // One CTA: 128 queries of one head.  Warp 0 copies Q once and the key and
 // value tiles (two stages each, keys one tile ahead); warp 1 allocates tensor memory and issues the UMMAs:
 // S_j = Q K_j^T (128 x 128, fp32 in tensor memory, two buffers) and
@@ -427,14 +362,10 @@ __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int kk) {
 // shared memory), rescale of its part of O in tensor memory when the
 // max grew by more than 2^8, P = 2^(s - m) rounded to fp16 into tensor memory
 // (the A operand of P.V, two buffers), row sums.
-// kWin: the tiles are the sinks' and then those from the first position that
-// the block's first query sees; where sinks and window meet, one run from 0.
-template <bool kWin>
 __global__ void __launch_bounds__(kTThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
-                           const __grid_constant__ CUtensorMap tm_vs, float* __restrict__ out, int H, int G, int64_t M,
-                           int64_t pos0, float scale_log2e, const WinArgs W) {
+                           const __grid_constant__ CUtensorMap tm_v, float* __restrict__ out, int H, int G, int64_t M,
+                           int64_t pos0, float scale_log2e) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   TcShared& S = *reinterpret_cast<TcShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -445,29 +376,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int h = (int)blockIdx.x, g = h / G;
   const int64_t q0 = (int64_t)qb * kTQ;
   const int64_t last_q = q0 + kTQ - 1 < M - 1 ? q0 + kTQ - 1 : M - 1;
-  int nt, sink_tiles = 0;
-  int64_t first = 0;  // kWin: the first position of the window's run of tiles
-  if (kWin) {
-    const int64_t last = pos0 + last_q;
-    first = pos0 + q0 - W.window + 1;
-    if (W.window == 0) {  // the sinks alone
-      sink_tiles = (int)(((W.sinks <= last ? W.sinks : last + 1) + kTK - 1) / kTK);
-      nt = sink_tiles;
-    } else {
-      if (first <= W.sinks)
-        first = 0;
-      else
-        sink_tiles = (int)((W.sinks + kTK - 1) / kTK);
-      nt = sink_tiles + (int)((last - first + kTK) / kTK);
-    }
-  } else {
-    nt = (int)((pos0 + last_q) / kTK) + 1;
-  }
-  // Position of the first row of tile t: in the sinks' map, or in the cache.
-  auto tile_pos = [&](int t) -> int64_t {
-    if (!kWin) return (int64_t)t * kTK;
-    return t < sink_tiles ? (int64_t)t * kTK : first + (int64_t)(t - sink_tiles) * kTK;
-  };
+  const int nt = (int)((pos0 + last_q) / kTK) + 1;
 
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 1);
@@ -516,9 +425,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nk >= kTStages) ok = mbar_wait(&S.k_empty[st], (uint32_t)((nk >> 1) - 1) & 1u, abort_flag, &g_attn_status);
         if (!ok) return;
         mbar_arrive_expect_tx(&S.k_full[st], (uint32_t)kTTile);
-        const CUtensorMap* mk = kWin && nk < sink_tiles ? &tm_ks : &tm_k;
-        tma_load_3d(S.k[st], mk, 0, (int)tile_pos(nk), g, &S.k_full[st]);
-        tma_load_3d(S.k[st] + kTBox, mk, 64, (int)tile_pos(nk), g, &S.k_full[st]);
+        tma_load_3d(S.k[st], &tm_k, 0, nk * kTK, g, &S.k_full[st]);
+        tma_load_3d(S.k[st] + kTBox, &tm_k, 64, nk * kTK, g, &S.k_full[st]);
         ++nk;
       };
       auto issue_v = [&]() {
@@ -526,9 +434,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nv >= kTStages) ok = mbar_wait(&S.v_empty[st], (uint32_t)((nv >> 1) - 1) & 1u, abort_flag, &g_attn_status);
         if (!ok) return;
         mbar_arrive_expect_tx(&S.v_full[st], (uint32_t)kTTile);
-        const CUtensorMap* mv = kWin && nv < sink_tiles ? &tm_vs : &tm_v;
-        tma_load_3d(S.v[st], mv, 0, (int)tile_pos(nv), g, &S.v_full[st]);
-        tma_load_3d(S.v[st] + kTBox, mv, 64, (int)tile_pos(nv), g, &S.v_full[st]);
+        tma_load_3d(S.v[st], &tm_v, 0, nv * kTK, g, &S.v_full[st]);
+        tma_load_3d(S.v[st] + kTBox, &tm_v, 64, nv * kTK, g, &S.v_full[st]);
         ++nv;
       };
       issue_k();
@@ -603,20 +510,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint32_t t_s = tmem + lane_off + (uint32_t)(sb * kTK) + col0;
       if (ok) ok = mbar_wait(&S.s_full[sb], (uint32_t)(j >> 1) & 1u, abort_flag, &g_attn_status);
       ok = __all_sync(0xffffffffu, ok);
-      const int64_t key0 = tile_pos(j) + col0;
-      // positions of this part the row sees: key0 + e for e < lim, and with
-      // kWin also e >= from or e < sk
-      const bool sink = kWin && j < sink_tiles;
-      auto clamp = [](int64_t x) { return x >= kTCols ? kTCols : (x <= 0 ? 0 : (int)x); };
-      const int lim = clamp((sink && W.sinks <= qpos ? W.sinks : qpos + 1) - key0);
-      const int from = kWin && !sink ? clamp(qpos - W.window + 1 - key0) : 0;
-      const int sk = kWin && !sink ? clamp(W.sinks - key0) : 0;
-      auto sees = [&](int e) { return e < lim && (!kWin || e >= from || e < sk); };
+      const int64_t key0 = (int64_t)j * kTK + col0;
+      // positions of this part the row sees: key0 .. key0 + lim - 1
+      const int64_t vis = qpos - key0 + 1;
+      const int lim = vis >= kTCols ? kTCols : (vis <= 0 ? 0 : (int)vis);
       uint32_t v[kTCols];
       float pmax = -INFINITY;
       // Every position of this part is visible to every row of the warp (a
       // tile below the diagonal): the loops below skip the per-position mask.
-      const bool full = __all_sync(0xffffffffu, lim == kTCols && (!kWin || from <= sk));
+      const bool full = __all_sync(0xffffffffu, lim == kTCols);
       if (ok) {
         tc_fence_after();
 #pragma unroll
@@ -643,13 +545,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
           } else {
 #pragma unroll
             for (int e = 16 * c; e < 16 * c + 16; ++e)
-              if (sees(e)) pm[c] = neg ? fminf(pm[c], __uint_as_float(v[e])) : fmaxf(pm[c], __uint_as_float(v[e]));
+              if (e < lim) pm[c] = neg ? fminf(pm[c], __uint_as_float(v[e])) : fmaxf(pm[c], __uint_as_float(v[e]));
           }
         }
         float ext = pm[0];
 #pragma unroll
         for (int c = 1; c < kTCols / 16; ++c) ext = neg ? fminf(ext, pm[c]) : fmaxf(ext, pm[c]);
-        pmax = lim > 0 && (!kWin || from < lim || sk > 0) ? ext * scale_log2e : -INFINITY;
+        pmax = lim > 0 ? ext * scale_log2e : -INFINITY;
       }
       // S_j is in registers: its buffer may take S_{j+2}
       tc_fence_before();
@@ -664,13 +566,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // the weights 2^(s - m) then stay below 256 (fp16 holds them) and O is
       // rescaled rarely; O and l use the same reference, so the result is the
       // same softmax.  All parts of a row take the same decision.
-      // kWin: a row may see nothing of the tiles so far; its max stays -inf and
-      // its weights (all masked) are taken relative to 0.
-      const bool upd = (m == -INFINITY && (!kWin || tmax != -INFINITY)) || tmax > m + 8.0f;
+      const bool upd = m == -INFINITY || tmax > m + 8.0f;
       const float mn = upd ? tmax : m;
       const float corr = upd ? exp2f(m - mn) : 1.0f;
       m = mn;
-      const float mref = kWin && m == -INFINITY ? 0.f : m;
       // P buffer j % 2 is free once P_{j-2}.V_{j-2} is done.
       if (ok && j >= 2) ok = mbar_wait(&S.pv_done[j & 1], (uint32_t)((j >> 1) - 1) & 1u, abort_flag, &g_attn_status);
       ok = __all_sync(0xffffffffu, ok);
@@ -705,11 +604,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const int e0 = 32 * c + e;
-            float p0 = ex2_approx(fmaf(__uint_as_float(v[e0]), scale_log2e, -mref));
-            float p1 = ex2_approx(fmaf(__uint_as_float(v[e0 + 1]), scale_log2e, -mref));
+            float p0 = ex2_approx(fmaf(__uint_as_float(v[e0]), scale_log2e, -m));
+            float p1 = ex2_approx(fmaf(__uint_as_float(v[e0 + 1]), scale_log2e, -m));
             if (!full) {
-              p0 = sees(e0) ? p0 : 0.f;
-              p1 = sees(e0 + 1) ? p1 : 0.f;
+              p0 = e0 < lim ? p0 : 0.f;
+              p1 = e0 + 1 < lim ? p1 : 0.f;
             }
             lp[(e >> 4) & 1] += p0 + p1;
             hp[e >> 1] = pack_h2(p0, p1);
@@ -740,15 +639,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t v[16];
         tmem_ld16(tmem + lane_off + 256u + col0 + (uint32_t)(16 * c), v);
         tmem_wait_ld();
-        if (kWin && row < M) {
-          uint32_t o[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            o[e] = pack_h2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(W.out + (row * H + h) * kD + col0 + 16 * c);
-          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        } else if (row < M) {
+        if (row < M) {
           float4* dst = reinterpret_cast<float4*>(out + (row * H + h) * kD + col0 + 16 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -779,77 +670,80 @@ uint32_t attn_take_status() {
   return v;
 }
 
-namespace {
-
-// W == null: qk_gqa_attention (out fp32); else the window and sinks, out in W.
-template <bool kWin>
-cudaError_t launch(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M, int H, int Hkv,
-                   int64_t pos0, int64_t Lmax, float scale, WinArgs W, cudaStream_t s) {
-  const int G = H / Hkv;
-  const float sl2e = scale * 1.4426950408889634f;
-  const __half* qh = reinterpret_cast<const __half*>(q);
+// Tensor maps over [H_kv][`rows` positions from `from`][128] of each cache:
+// positions past them read as zero.
+static bool encode_caches(CUtensorMap* tk, CUtensorMap* tv, const uint16_t* kc, const uint16_t* vc, int Hkv,
+                          int64_t Lmax, int64_t from, int64_t rows, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)rows, (uint64_t)Hkv};
   const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)Lmax * kRowBytes};
-  const int box_rows = M == 1 ? kPK : kTK;
-  // Tensor maps over [H_kv][rows positions from `from`][128] of a cache: other
-  // positions read as zero.
-  auto encode = [&](CUtensorMap* tk, CUtensorMap* tv, int64_t from, int64_t rows) {
-    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)(rows > 0 ? rows : 1), (uint64_t)Hkv};
-    const uint32_t box[3] = {64u, (uint32_t)box_rows, 1u};
-    return encode_tensor_map_f16(tk, kc + from * kD, 3, dims, strides, box, true) &&
-           encode_tensor_map_f16(tv, vc + from * kD, 3, dims, strides, box, true);
-  };
-  alignas(64) CUtensorMap tk, tv, tks, tvs;
-  const int64_t end = pos0 + M;  // positions past the last query
-  if (kWin && M == 1) {
-    // the one query's window; a window that reaches the sinks takes them in
-    int64_t first = end - W.window;
-    if (first <= W.sinks) {
-      first = 0;
-      W.sinks = 0;
-      if (W.window == 0) {  // the sinks alone, all of them visible positions
-        W.sinks = end;
-        first = end;
-      }
-    }
-    W.window = end - first;
-    if (!encode(&tk, &tv, first < end ? first : 0, W.window)) return cudaErrorInvalidValue;
-  } else if (!encode(&tk, &tv, 0, end)) {
-    return cudaErrorInvalidValue;
+  const uint32_t box[3] = {64u, (uint32_t)box_rows, 1u};
+  return encode_tensor_map_f16(tk, kc + from * kD, 3, dims, strides, box, true) &&
+         encode_tensor_map_f16(tv, vc + from * kD, 3, dims, strides, box, true);
+}
+
+// Decode: a cluster of C CTAs per key/value head, at least 256 of the n visible positions each.
+template <bool kWin>
+static cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
+                                 const CUtensorMap& tvs, const uint16_t* q, float* out, int H, int Hkv, int64_t n,
+                                 float scale, const WinArgs& W, cudaStream_t s) {
+  int C = (int)((n + 255) / 256);
+  C = C < 1 ? 1 : (C > kDecMaxCluster ? kDecMaxCluster : C);
+  static PerDeviceFlag attr_set;
+  const int dev = current_device();
+  if (!attr_set.done(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)dec_smem());
+    if (e != cudaSuccess) return e;
+    attr_set.mark(dev);
   }
-  if (kWin && W.sinks > 0) {
-    if (!encode(&tks, &tvs, 0, W.sinks < end ? W.sinks : end)) return cudaErrorInvalidValue;
-  } else {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)C, (unsigned)Hkv, 1);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = dec_smem();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<kWin>, tk, tv, tks, tvs, reinterpret_cast<const __half*>(q), out,
+                            H / Hkv, n, scale * 1.4426950408889634f, C, W);
+}
+
+cudaError_t launch_attn_window_decode(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out, int H,
+                                      int Hkv, int64_t pos0, int64_t Lmax, float scale, int64_t window, int64_t sinks,
+                                      cudaStream_t s) {
+  const int64_t end = pos0 + 1;
+  int64_t first = end - window;
+  if (first <= sinks) {  // a window that reaches the sinks takes them in
+    first = window > 0 ? 0 : end;
+    if (window > 0) sinks = 0;
+  }
+  window = end - first;
+  alignas(64) CUtensorMap tk, tv, tks, tvs;
+  if (window > 0 && !encode_caches(&tk, &tv, kc, vc, Hkv, Lmax, first, window, kPK)) return cudaErrorInvalidValue;
+  if (sinks > 0 && !encode_caches(&tks, &tvs, kc, vc, Hkv, Lmax, 0, sinks, kPK)) return cudaErrorInvalidValue;
+  if (window == 0) {
+    tk = tks;
+    tv = tvs;
+  } else if (sinks == 0) {
     tks = tk;
     tvs = tv;
   }
-  const int dev = current_device();
-  if (M == 1) {
-    // Decode: a cluster of C CTAs per key/value head, at least 256 positions each.
-    const int64_t n = kWin ? W.window + W.sinks : end;
-    int C = (int)((n + 255) / 256);
-    C = C < 1 ? 1 : (C > kDecMaxCluster ? kDecMaxCluster : C);
-    static PerDeviceFlag attr_set;
-    if (!attr_set.done(dev)) {
-      const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)dec_smem());
-      if (e != cudaSuccess) return e;
-      attr_set.mark(dev);
-    }
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)C, (unsigned)Hkv, 1);
-    cfg.blockDim = dim3(kDecThreads);
-    cfg.dynamicSmemBytes = dec_smem();
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<kWin>, tk, tv, tks, tvs, qh, out, G, n, sl2e, C, W);
-  }
+  const WinArgs W{window, sinks, reinterpret_cast<__half*>(out)};
+  return launch_decode<true>(tk, tv, tks, tvs, q, nullptr, H, Hkv, window + sinks, scale, W, s);
+}
+
+cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
+                                 int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s) {
+  alignas(64) CUtensorMap tk, tv;
+  if (!encode_caches(&tk, &tv, kc, vc, Hkv, Lmax, 0, pos0 + M, M == 1 ? kPK : kTK)) return cudaErrorInvalidValue;
+  if (M == 1) return launch_decode<false>(tk, tv, tk, tv, q, out, H, Hkv, pos0 + 1, scale, WinArgs{0, 0, nullptr}, s);
+  const int G = H / Hkv;
+  const float sl2e = scale * 1.4426950408889634f;
   // Q: [M][H][128] as a 3-D map {128, H, M}; a box is 64 dims of one head for 128 queries.
   const uint64_t qd[3] = {(uint64_t)kD, (uint64_t)H, (uint64_t)M};
   const uint64_t qs[2] = {(uint64_t)kRowBytes, (uint64_t)H * kRowBytes};
@@ -857,33 +751,18 @@ cudaError_t launch(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, fl
   alignas(64) CUtensorMap tq;
   if (!encode_tensor_map_f16(&tq, q, 3, qd, qs, qbox, true)) return cudaErrorInvalidValue;
   static PerDeviceFlag attr_set;
+  const int dev = current_device();
   if (!attr_set.done(dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_prefill_tc_kernel<kWin>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem());
+    const cudaError_t e = cudaFuncSetAttribute(attn_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)tc_smem());
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
   const int64_t nqb = (M + kTQ - 1) / kTQ;
   if (nqb > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)H, (unsigned)nqb);
-  attn_prefill_tc_kernel<kWin><<<grid, kTThreads, tc_smem(), s>>>(tq, tk, tv, tks, tvs, out, H, G, M, pos0, sl2e, W);
+  attn_prefill_tc_kernel<<<grid, kTThreads, tc_smem(), s>>>(tq, tk, tv, out, H, G, M, pos0, sl2e);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
-                                 int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s) {
-  return launch<false>(q, kc, vc, out, M, H, Hkv, pos0, Lmax, scale, WinArgs{0, 0, nullptr}, s);
-}
-
-cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out,
-                                        int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
-                                        int64_t window, int64_t sinks, cudaStream_t s) {
-  if (window == 0 && sinks == 0) return cudaMemsetAsync(out, 0, (size_t)M * H * kRowBytes, s);  // nothing is visible
-  const int64_t end = pos0 + M;
-  const WinArgs W{window < end ? window : end, sinks < end ? sinks : end, reinterpret_cast<__half*>(out)};
-  return launch<true>(q, kc, vc, nullptr, M, H, Hkv, pos0, Lmax, scale, W, s);
 }
 
 }  // namespace qk

@@ -1,0 +1,461 @@
+// qk_attn_win.cu -- grouped-query attention with a sliding window and sinks
+// over the KV cache: position j <= p is visible to the query at position p when
+// j > p - window or j < sinks.
+//
+// Source: DAMASCUS project overview, "[02] the pipeline" (a decoder layer is GQA
+// with a KV cache) and "[04] one decode step"; the window and the sinks bound
+// the cache that one step reads.
+//
+// Layouts: q [M][H][128] fp16 (query i at position pos0 + i), caches
+// [H_kv][L_max][128] fp16, out [M][H][128] fp16 (the O projection's x).
+//
+// Prefill (M >= 2) on the 5th-generation tensor cores.  A query tile is 128
+// rows: the G heads of one key/value head for floor(128 / G) consecutive
+// queries, so that a key or value tile is read once for all of them and a
+// tile's queries span few positions (a window of 512 over 42 queries touches 5
+// tiles of keys, over 128 queries 6).  A CTA has two query tiles and one stream
+// of key and value tiles (128 positions, TMA, a ring of five): while one tile's
+// four softmax warps work, the tensor core runs the other tile's S = Q K^T and
+// O += P V.  P (fp16) takes the place of its S in tensor memory, O stays there.
+// One thread owns one row: no exchange between threads, and the running maximum
+// moves only when it grows by more than 2^8, so O is rarely rescaled.
+//
+// The tiles of a CTA are the sinks' (from maps that hold the sinks alone) and
+// then those from the first position that its first query sees; where the two
+// meet, one run from position 0.  A position that no query of the CTA sees is
+// never loaded.
+//
+// Decode (M = 1) runs in qk_attn.cu.
+//
+// All waits are bounded; a timeout raises the device status word.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "qk_attn.cuh"
+#include "qk_device.cuh"
+#include "qk_internal.h"
+
+namespace qk {
+
+__device__ uint32_t g_attn_win_status = 0;
+
+namespace {
+
+constexpr int kWK = 128;         // positions per key / value tile
+constexpr int kWRing = 5;        // key and value tiles in flight, in the order of their use: K0 V0 K1 V1 ...
+constexpr int kWWarps = 12;      // copy, UMMA issue, 2 idle, 4 softmax warps for each query tile
+constexpr int kWThreads = 32 * kWWarps;
+
+struct WpShared {
+  uint8_t q[2][kTTile];
+  uint8_t kv[kWRing][kTTile];
+  uint64_t q_full;
+  uint64_t full[kWRing];
+  uint64_t empty[kWRing];
+  uint64_t s_full[2];     // [query tile] S is in tensor memory
+  uint64_t p_full[2][2];  // [query tile][half]: 64 positions of P are in tensor memory
+  uint64_t pv_done[2];    // O holds the tile's product, P's columns are free for the next S
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+
+struct WpArgs {
+  __half* out;
+  int H, Hkv, G, queries;  // query heads, key/value heads, heads per key/value head, queries per tile
+  int64_t M, pos0, window, sinks;
+  float scale_log2e;
+};
+
+// Packed pairs of fp32 (one instruction for two values).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Bits e of 0 .. 31 with lo <= e < hi.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  lo = max(0, min(32, lo));
+  hi = max(0, min(32, hi));
+  const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+
+__global__ void __launch_bounds__(kWThreads, 1)
+    attn_win_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
+                            const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ WpArgs A) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  WpShared& S = *reinterpret_cast<WpShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // every head's latest queries, which see the most, first
+  const int g = (int)(blockIdx.x % (unsigned)A.Hkv), G = A.G;
+  const int64_t q0 = (int64_t)((gridDim.x - 1 - blockIdx.x) / (unsigned)A.Hkv) * 2 * A.queries;
+  const bool two = q0 + A.queries < A.M;
+  // positions of each query tile's first and last query
+  const int64_t pf0 = A.pos0 + q0, pf1 = pf0 + A.queries, end = A.pos0 + A.M - 1;
+  const int64_t pl0 = min(pf1 - 1, end), pl1 = min(pf1 + A.queries - 1, end);
+  const int64_t last = two ? pl1 : pl0;
+  int64_t first = pf0 - A.window + 1;  // first position of the window's run of tiles
+  int nt, sink_tiles = 0;
+  if (A.window == 0) {  // the sinks alone
+    sink_tiles = (int)(((A.sinks <= last ? A.sinks : last + 1) + kWK - 1) / kWK);
+    nt = sink_tiles;
+  } else {
+    if (first <= A.sinks)
+      first = 0;
+    else
+      sink_tiles = (int)((A.sinks + kWK - 1) / kWK);
+    nt = sink_tiles + (int)((last - first + kWK) / kWK);
+  }
+  // Position of the first row of tile j: in the sinks' map, or in the cache.
+  auto tile_pos = [&](int j) -> int64_t {
+    return j < sink_tiles ? (int64_t)j * kWK : first + (int64_t)(j - sink_tiles) * kWK;
+  };
+  // Whether some row of query tile t sees some position of tile j.
+  auto active = [&](int t, int j) -> bool {
+    if (j >= nt || (t == 1 && !two)) return false;
+    const int64_t k0 = tile_pos(j);
+    if (k0 > (t ? pl1 : pl0)) return false;
+    return j < sink_tiles || k0 + kWK - 1 > (t ? pf1 : pf0) - A.window || k0 < A.sinks;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&S.q_full, 1);
+    for (int s = 0; s < kWRing; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&S.s_full[t], 1);
+      mbar_init(&S.p_full[t][0], 4);
+      mbar_init(&S.p_full[t][1], 4);
+      mbar_init(&S.pv_done[t], 1);
+    }
+    mbar_init(&S.mma_done, 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&S.tmem_base, 512);  // S (then P) of the tiles at columns 0 and 128, O at 256 and 384
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  volatile uint32_t* abort_flag = &S.abort_flag;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copy warp
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      const uint32_t qbytes = (uint32_t)(kRowBytes * G * A.queries);
+      mbar_arrive_expect_tx(&S.q_full, qbytes * (two ? 2u : 1u));
+      for (int t = 0; t < (two ? 2 : 1); ++t)
+        for (int b = 0; b < 2; ++b)
+          tma_load_3d(S.q[t] + b * kTBox, &tm_q, 64 * b, g * G, (int)(q0 + t * A.queries), &S.q_full);
+      bool ok = true;
+      int n = 0;  // tiles issued: K0 V0 K1 V1 ...
+      for (; n < 2 * nt && ok; ++n) {
+        const int s = n % kWRing;
+        if (n >= kWRing)
+          ok = mbar_wait(&S.empty[s], (uint32_t)(n / kWRing - 1) & 1u, abort_flag, &g_attn_win_status);
+        if (!ok) break;
+        const int j = n >> 1;
+        const bool sink = j < sink_tiles;
+        const CUtensorMap* m = n & 1 ? (sink ? &tm_vs : &tm_v) : (sink ? &tm_ks : &tm_k);
+        mbar_arrive_expect_tx(&S.full[s], (uint32_t)kTTile);
+        tma_load_3d(S.kv[s], m, 0, (int)tile_pos(j), g, &S.full[s]);
+        tma_load_3d(S.kv[s] + kTBox, m, 64, (int)tile_pos(j), g, &S.full[s]);
+      }
+      // Drain: every copy issued has landed before the CTA exits.
+      mbar_wait(&S.q_full, 0u, abort_flag, &g_attn_win_status, true);
+      for (int u = (n > kWRing ? n - kWRing : 0); u < n; ++u)
+        mbar_wait(&S.full[u % kWRing], (uint32_t)(u / kWRing) & 1u, abort_flag, &g_attn_win_status, true);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- UMMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = umma_idesc_f16(128, kWK);
+      constexpr uint32_t idesc_pv = umma_idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
+      bool ok = mbar_wait(&S.q_full, 0u, abort_flag, &g_attn_win_status);
+      int done[2] = {0, 0};  // tiles of each query tile whose P V is issued
+      // S of query tile t and key tile j; `free_k`: no later use of the key tile
+      auto qk = [&](int t, int j, bool free_k) {
+        const int n = 2 * j;
+        ok = ok && mbar_wait(&S.full[n % kWRing], (uint32_t)(n / kWRing) & 1u, abort_flag, &g_attn_win_status);
+        if (ok && done[t] > 0)
+          ok = mbar_wait(&S.pv_done[t], (uint32_t)(done[t] - 1) & 1u, abort_flag, &g_attn_win_status);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(S.q[t]), ka = smem_u32(S.kv[n % kWRing]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_ss(tmem + (uint32_t)(128 * t), kmajor_desc(qa, kk), kmajor_desc(ka, kk), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(&S.s_full[t]);
+        if (free_k) umma_commit(&S.empty[n % kWRing]);
+      };
+      auto pv = [&](int t, int j, bool free_v) {
+        const int n = 2 * j + 1;
+        ok = ok && mbar_wait(&S.full[n % kWRing], (uint32_t)(n / kWRing) & 1u, abort_flag, &g_attn_win_status);
+        const uint32_t va = smem_u32(S.kv[n % kWRing]), t_o = tmem + 256u + (uint32_t)(128 * t);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && mbar_wait(&S.p_full[t][half], (uint32_t)done[t] & 1u, abort_flag, &g_attn_win_status);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            umma_f16_ts(t_o, tmem + (uint32_t)(128 * t + 8 * kk), mnmajor_desc(va, kk), idesc_pv,
+                        (done[t] > 0 || kk > 0) ? 1u : 0u);
+        }
+        ++done[t];
+        umma_commit(&S.pv_done[t]);
+        if (free_v) umma_commit(&S.empty[n % kWRing]);
+      };
+      if (active(0, 0)) qk(0, 0, !active(1, 0));
+      if (active(1, 0)) qk(1, 0, true);
+      for (int j = 0; j < nt && ok; ++j)
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (active(t, j)) pv(t, j, t == 1 || !active(1, j));
+          if (ok && active(t, j + 1)) qk(t, j + 1, t == 1 || !active(1, j + 1));
+        }
+      // every UMMA issued has completed before tensor memory is freed
+      umma_commit(&S.mma_done);
+      mbar_wait(&S.mma_done, 0u, abort_flag, &g_attn_win_status, true);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- softmax warps
+    const int t = (warp - 4) >> 2;
+    const int r = 32 * (warp & 3) + lane;  // row of the query tile = tensor-memory lane
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + lane_off + (uint32_t)(128 * t), t_o = tmem + lane_off + 256u + (uint32_t)(128 * t);
+    const int64_t row = q0 + t * A.queries + r / G;  // this row's query
+    const int64_t p = A.pos0 + row;
+    const float scale = A.scale_log2e;
+    const bool neg = scale < 0.f;
+    float m = -INFINITY;
+    uint64_t l2 = 0;  // the row's sum, as two partial sums
+    bool ok = true;
+    int n = 0;  // active tiles so far
+    for (int j = 0; j < nt && ok; ++j) {
+      if (!active(t, j)) continue;
+      // row p sees positions k0 + e of the tile with e < lim and (e >= from or e < sk)
+      const int64_t k0 = tile_pos(j);
+      const bool sink = j < sink_tiles;
+      auto clamp = [](int64_t x) { return x >= kWK ? kWK : (x <= 0 ? 0 : (int)x); };
+      const int lim = clamp((sink && A.sinks <= p ? A.sinks : p + 1) - k0);
+      const int from = sink ? 0 : clamp(p - A.window + 1 - k0);
+      const int sk = sink ? 0 : clamp(A.sinks - k0);
+      const bool full = __all_sync(0xffffffffu, lim == kWK && from <= sk);
+      ok = mbar_wait(&S.s_full[t], (uint32_t)n & 1u, abort_flag, &g_attn_win_status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[kWK];
+#pragma unroll
+      for (int c = 0; c < kWK / 16; ++c)
+        tmem_ld16(t_s + (uint32_t)(16 * c), *reinterpret_cast<uint32_t(*)[16]>(v + 16 * c));
+      tmem_wait_ld();
+      if (!full) {  // hidden positions get the score that has weight 0 (and whatever was there is dropped)
+        const uint32_t hidden = neg ? 0x7F800000u : 0xFF800000u;
+#pragma unroll
+        for (int c = 0; c < kWK / 32; ++c) {
+          const uint32_t sees = bits_between(0, lim - 32 * c) &
+                                (bits_between(from - 32 * c, 32) | bits_between(0, sk - 32 * c));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[32 * c + e] = (sees >> e) & 1u ? v[32 * c + e] : hidden;
+        }
+      }
+      // max_e(s_e * c) is c * max_e(s_e) for c >= 0 (rounding is monotonic) and c * min_e(s_e) for c < 0
+      float ext[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ext[c] = __uint_as_float(v[c]);
+      if (!neg) {
+#pragma unroll
+        for (int e = 4; e < kWK; ++e) ext[e & 3] = fmaxf(ext[e & 3], __uint_as_float(v[e]));
+        ext[0] = fmaxf(fmaxf(ext[0], ext[1]), fmaxf(ext[2], ext[3]));
+      } else {
+#pragma unroll
+        for (int e = 4; e < kWK; ++e) ext[e & 3] = fminf(ext[e & 3], __uint_as_float(v[e]));
+        ext[0] = fminf(fminf(ext[0], ext[1]), fminf(ext[2], ext[3]));
+      }
+      const float tmax = ext[0] * scale;
+      // The reference max moves only when the row max grows by more than 2^8:
+      // the weights 2^(s - m) then stay below 256 (fp16 holds them) and O is
+      // rescaled rarely; O and l use the same reference, so the result is the
+      // same softmax.  A row that has seen nothing yet keeps m = -inf, and its
+      // weights, all 0, are taken relative to 0.
+      const bool upd = (m == -INFINITY && tmax != -INFINITY) || tmax > m + 8.0f;
+      const float mn = upd ? tmax : m;
+      const float corr = upd ? exp2f(m - mn) : 1.0f;
+      m = mn;
+      const float mref = m == -INFINITY ? 0.f : m;
+      if (__any_sync(0xffffffffu, upd)) {
+        float a, b;
+        unpack2(l2, a, b);
+        l2 = pack2(a * corr, b * corr);
+        if (n > 0) {  // S was issued after the tile before was added to O
+#pragma unroll 1
+          for (int c = 0; c < kD / 16; ++c) {
+            uint32_t w[16];
+            tmem_ld16(t_o + (uint32_t)(16 * c), w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * corr);
+            tmem_st16(t_o + (uint32_t)(16 * c), w);
+          }
+        }
+      }
+      const uint64_t sc2 = pack2(scale, scale), mm2 = pack2(-mref, -mref);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int e0 = 64 * half + 32 * c;
+          uint32_t hp[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(v[e0 + e]), __uint_as_float(v[e0 + e + 1])), sc2, mm2), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            l2 = add2(l2, pack2(a, b));
+            hp[e >> 1] = pack_h2(a, b);
+          }
+          tmem_st16(t_s + (uint32_t)(e0 / 2), hp);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[t][half]);
+      }
+      ++n;
+    }
+    if (ok && n > 0) {
+      ok = mbar_wait(&S.pv_done[t], (uint32_t)(n - 1) & 1u, abort_flag, &g_attn_win_status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        float a, b;
+        unpack2(l2, a, b);
+        const float inv = 1.0f / (a + b);
+        const bool on = r < G * A.queries && row < A.M;
+        __half* dst = A.out + (row * A.H + g * G + r % G) * kD;
+#pragma unroll 1
+        for (int c = 0; c < kD / 16; ++c) {
+          uint32_t w[16], o[8];
+          tmem_ld16(t_o + (uint32_t)(16 * c), w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = pack_h2(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+          if (on) {
+            uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
+            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr size_t kWpSmem = sizeof(WpShared) + 1024;  // + alignment slack
+static_assert(kWpSmem <= 227 * 1024, "shared memory of a CTA");
+
+cudaError_t launch_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out, int64_t M, int H,
+                           int Hkv, int64_t pos0, int64_t Lmax, float scale, int64_t window, int64_t sinks,
+                           cudaStream_t s) {
+  const int G = H / Hkv;
+  const int queries = 128 / G;
+  const uint64_t qd[3] = {(uint64_t)kD, (uint64_t)H, (uint64_t)M};
+  const uint64_t qs[2] = {(uint64_t)kRowBytes, (uint64_t)H * kRowBytes};
+  const uint32_t qbox[3] = {64u, (uint32_t)G, (uint32_t)queries};
+  const uint64_t strides[2] = {(uint64_t)kRowBytes, (uint64_t)Lmax * kRowBytes};
+  const uint32_t box[3] = {64u, (uint32_t)kWK, 1u};
+  // Maps over the caches' first rows: positions past them read as zero.
+  auto encode = [&](CUtensorMap* tk, CUtensorMap* tv, int64_t rows) {
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)rows, (uint64_t)Hkv};
+    return encode_tensor_map_f16(tk, kc, 3, dims, strides, box, true) &&
+           encode_tensor_map_f16(tv, vc, 3, dims, strides, box, true);
+  };
+  alignas(64) CUtensorMap tq, tk, tv, tks, tvs;
+  if (!encode_tensor_map_f16(&tq, q, 3, qd, qs, qbox, true) || !encode(&tk, &tv, pos0 + M)) return cudaErrorInvalidValue;
+  if (sinks > 0) {
+    if (!encode(&tks, &tvs, sinks)) return cudaErrorInvalidValue;
+  } else {
+    tks = tk;
+    tvs = tv;
+  }
+  static PerDeviceFlag attr_set;
+  const int dev = current_device();
+  if (!attr_set.done(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_win_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWpSmem);
+    if (e != cudaSuccess) return e;
+    attr_set.mark(dev);
+  }
+  // A scale of 0 (every visible position alike) must still tell hidden
+  // positions, whose score is infinite, from visible ones.
+  float sl2e = scale * 1.4426950408889634f;
+  if (sl2e == 0.f) sl2e = 1e-37f;
+  const int64_t nqb = (M + 2 * queries - 1) / (2 * queries);
+  if (nqb * Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const WpArgs A{reinterpret_cast<__half*>(out), H, Hkv, G, queries, M, pos0, window, sinks, sl2e};
+  attn_win_prefill_kernel<<<(unsigned)(nqb * Hkv), kWThreads, kWpSmem, s>>>(tq, tk, tv, tks, tvs, A);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+uint32_t attn_win_take_status() {
+  uint32_t v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_attn_win_status, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_attn_win_status, &zero, sizeof(zero));
+  v |= take_debug_status();
+  return v;
+}
+
+cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out,
+                                        int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
+                                        int64_t window, int64_t sinks, cudaStream_t s) {
+  if (window == 0 && sinks == 0) return cudaMemsetAsync(out, 0, (size_t)M * H * kRowBytes, s);  // nothing is visible
+  const int64_t end = pos0 + M;
+  if (window > end) window = end;
+  if (sinks > end) sinks = end;
+  if (M == 1) return launch_attn_window_decode(q, kc, vc, out, H, Hkv, pos0, Lmax, scale, window, sinks, s);
+  return launch_prefill(q, kc, vc, out, M, H, Hkv, pos0, Lmax, scale, window, sinks, s);
+}
+
+}  // namespace qk

@@ -114,11 +114,16 @@ bool encode_tensor_map_f16(void* out, const void* base, int rank, const uint64_t
 // GQA attention (qk_gqa_attention); arguments validated.  Device status word.
 cudaError_t launch_gqa_attention(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, float* out, int64_t M,
                                  int H, int Hkv, int64_t pos0, int64_t Lmax, float scale, cudaStream_t s);
-// The same with a window and sinks, fp16 out (qk_gqa_attention_window).
+// The same with a window and sinks, fp16 out (qk_gqa_attention_window), and its
+// decode step (window and sinks at most pos0 + 1, not both 0).
+cudaError_t launch_attn_window_decode(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out, int H,
+                                      int Hkv, int64_t pos0, int64_t Lmax, float scale, int64_t window, int64_t sinks,
+                                      cudaStream_t s);
 cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out,
                                         int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
                                         int64_t window, int64_t sinks, cudaStream_t s);
 uint32_t attn_take_status();
+uint32_t attn_win_take_status();
 
 // A kernel whose single bounded wait can never complete (see qk_debug_wait_timeout).
 cudaError_t launch_wait_probe(uint64_t limit_ns, cudaStream_t s);
