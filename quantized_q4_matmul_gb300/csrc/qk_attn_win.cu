@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kWK = 128;         // positions per key / value tile
 constexpr int kWRing = 5;        // key and value tiles in flight, in the order of their use: K0 V0 K1 V1 ...
-constexpr int kWWarps = 12;      // copy, UMMA issue, 2 idle, 4 softmax warps for each query tile
+constexpr int kWWarps = 12;      // copy, 2 UMMA issuers, 1 idle, 4 softmax warps for each query tile
 constexpr int kWThreads = 32 * kWWarps;
 
 struct WpShared {
@@ -59,7 +59,8 @@ struct WpShared {
   uint64_t s_full[2];     // [query tile] S is in tensor memory
   uint64_t p_full[2][2];  // [query tile][half]: 64 positions of P are in tensor memory
   uint64_t pv_done[2];    // O holds the tile's product, P's columns are free for the next S
-  uint64_t mma_done;
+  uint64_t mma_done[2];
+  uint64_t turn[2];       // whose turn on the tensor core
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
@@ -131,27 +132,42 @@ __global__ void __launch_bounds__(kWThreads, 1)
   auto tile_pos = [&](int j) -> int64_t {
     return j < sink_tiles ? (int64_t)j * kWK : first + (int64_t)(j - sink_tiles) * kWK;
   };
-  // Whether some row of query tile t sees some position of tile j.
-  auto active = [&](int t, int j) -> bool {
-    if (j >= nt || (t == 1 && !two)) return false;
-    const int64_t k0 = tile_pos(j);
-    if (k0 > (t ? pl1 : pl0)) return false;
-    return j < sink_tiles || k0 + kWK - 1 > (t ? pf1 : pf0) - A.window || k0 < A.sinks;
+  // Query tile u has rows that see something of tile j: those up to its last
+  // query, but for a gap between the sinks and its first query's window.
+  struct Active {
+    int end, gap0, gap1;
+    __device__ __forceinline__ bool operator()(int j) const { return j < end && (j < gap0 || j >= gap1); }
+  };
+  auto actives = [&](int u) {
+    Active r{0, 0, 0};
+    if (u == 1 && !two) return r;
+    const int64_t pf = u ? pf1 : pf0, pl = u ? pl1 : pl0;
+    if (A.window == 0) {
+      r.end = min(nt, (int)(pl / kWK) + 1);
+      return r;
+    }
+    r.end = sink_tiles + (int)((pl - first) / kWK) + 1;
+    const int64_t hidden = pf - A.window - first + 1;  // positions of the run before the window
+    const int64_t kept = A.sinks - first;              // those of them that are sinks
+    r.gap0 = sink_tiles + (int)(kept > 0 ? (kept + kWK - 1) / kWK : 0);
+    r.gap1 = sink_tiles + (int)(hidden > 0 ? hidden / kWK : 0);
+    return r;
   };
 
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 1);
     for (int s = 0; s < kWRing; ++s) {
       mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
+      mbar_init(&S.empty[s], two ? 2 : 1);  // released by each query tile's issuer
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&S.s_full[t], 1);
       mbar_init(&S.p_full[t][0], 4);
       mbar_init(&S.p_full[t][1], 4);
       mbar_init(&S.pv_done[t], 1);
+      mbar_init(&S.mma_done[t], 1);
+      mbar_init(&S.turn[t], 1);
     }
-    mbar_init(&S.mma_done, 1);
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -196,56 +212,95 @@ __global__ void __launch_bounds__(kWThreads, 1)
         mbar_wait(&S.full[u % kWRing], (uint32_t)(u / kWRing) & 1u, abort_flag, &g_attn_win_status, true);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- UMMA issuer
-    if (lane == 0) {
+  } else if (warp <= 2) {
+    // ---------------------------------------------------------------- UMMA issuers
+    // One warp for each query tile.  The whole warp runs this code and an
+    // elected lane issues.  The tiles take turns, each with its P V and its next
+    // S, so that the tensor core works for one while the other's softmax runs:
+    // left alone, the two fall into step, share the tensor core and then leave
+    // it idle together (3650 clocks for a key tile of both, in turns TURNCLK).
+    const int u = warp - 1;
+    if (u == 0 || two) {
       constexpr uint32_t idesc_s = umma_idesc_f16(128, kWK);
       constexpr uint32_t idesc_pv = umma_idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
-      bool ok = mbar_wait(&S.q_full, 0u, abort_flag, &g_attn_win_status);
-      int done[2] = {0, 0};  // tiles of each query tile whose P V is issued
-      // S of query tile t and key tile j; `free_k`: no later use of the key tile
-      auto qk = [&](int t, int j, bool free_k) {
-        const int n = 2 * j;
-        ok = ok && mbar_wait(&S.full[n % kWRing], (uint32_t)(n / kWRing) & 1u, abort_flag, &g_attn_win_status);
-        if (ok && done[t] > 0)
-          ok = mbar_wait(&S.pv_done[t], (uint32_t)(done[t] - 1) & 1u, abort_flag, &g_attn_win_status);
-        if (!ok) return;
+      const uint32_t t_s = __shfl_sync(0xffffffffu, tmem, 0) + (uint32_t)(128 * u), t_o = t_s + 256u;
+      const uint32_t qa = smem_u32(S.q[u]), kv_s = smem_u32(S.kv[0]);
+      const Active act = actives(u);
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, &g_attn_win_status));
+      };
+      struct Slot {  // ring position of the key (or value) tiles: every second slot
+        int s;
+        uint32_t phase;
+        __device__ __forceinline__ void next() {
+          s += 2;
+          if (s >= kWRing) {
+            s -= kWRing;
+            phase ^= 1u;
+          }
+        }
+      } ks{0, 0u}, vs{1, 0u};
+      uint32_t done = 0;  // tiles whose P V is issued
+      bool ok = wait(&S.q_full, 0u);
+      // What a turn needs is waited for before it: on the way through a turn
+      // only the end of P V holds the next S up (they share columns).
+      auto qk = [&]() {
         tc_fence_after();
-        const uint32_t qa = smem_u32(S.q[t]), ka = smem_u32(S.kv[n % kWRing]);
+        const uint32_t ka = kv_s + (uint32_t)(ks.s * kTTile);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ss(tmem + (uint32_t)(128 * t), kmajor_desc(qa, kk), kmajor_desc(ka, kk), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(&S.s_full[t]);
-        if (free_k) umma_commit(&S.empty[n % kWRing]);
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_f16_ss_warp(t_s, kmajor_desc(qa, kk), kmajor_desc(ka, kk), idesc_s, kk > 0 ? 1u : 0u);
+          if (kk == 3 && two && lane == 0) mbar_arrive(&S.turn[1 - u]);  // the hand-over takes as long as the rest
+        }
+        umma_commit_warp(&S.s_full[u]);
       };
-      auto pv = [&](int t, int j, bool free_v) {
-        const int n = 2 * j + 1;
-        ok = ok && mbar_wait(&S.full[n % kWRing], (uint32_t)(n / kWRing) & 1u, abort_flag, &g_attn_win_status);
-        const uint32_t va = smem_u32(S.kv[n % kWRing]), t_o = tmem + 256u + (uint32_t)(128 * t);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && mbar_wait(&S.p_full[t][half], (uint32_t)done[t] & 1u, abort_flag, &g_attn_win_status);
-          if (!ok) return;
+      auto release = [&](int slot, bool used) {
+        if (used)
+          umma_commit_warp(&S.empty[slot]);
+        else if (lane == 0)
+          mbar_arrive(&S.empty[slot]);
+        __syncwarp();
+      };
+      if (ok) ok = wait(&S.full[ks.s], ks.phase);
+      if (u == 1 && ok) ok = wait(&S.turn[1], 0u);
+      if (ok && act(0))
+        qk();
+      else if (two && lane == 0)
+        mbar_arrive(&S.turn[1 - u]);
+      if (ok) release(ks.s, act(0));
+      for (int j = 0; j < nt && ok; ++j) {
+        const bool now = act(j), next = act(j + 1);
+        ks.next();
+        ok = wait(&S.full[vs.s], vs.phase);
+        if (ok && j + 1 < nt) ok = wait(&S.full[ks.s], ks.phase);
+        if (ok && now) ok = wait(&S.p_full[u][0], done & 1u) && wait(&S.p_full[u][1], done & 1u);
+        if (two && ok) ok = wait(&S.turn[u], (uint32_t)(u == 0 ? j : j + 1) & 1u);
+        if (!ok) break;
+        if (now) {
           tc_fence_after();
+          const uint32_t va = kv_s + (uint32_t)(vs.s * kTTile);
 #pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            umma_f16_ts(t_o, tmem + (uint32_t)(128 * t + 8 * kk), mnmajor_desc(va, kk), idesc_pv,
-                        (done[t] > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ts_warp(t_o, t_s + (uint32_t)(8 * kk), mnmajor_desc(va, kk), idesc_pv,
+                             (done > 0 || kk > 0) ? 1u : 0u);
+          ++done;
+          umma_commit_warp(&S.pv_done[u]);
         }
-        ++done[t];
-        umma_commit(&S.pv_done[t]);
-        if (free_v) umma_commit(&S.empty[n % kWRing]);
-      };
-      if (active(0, 0)) qk(0, 0, !active(1, 0));
-      if (active(1, 0)) qk(1, 0, true);
-      for (int j = 0; j < nt && ok; ++j)
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (active(t, j)) pv(t, j, t == 1 || !active(1, j));
-          if (ok && active(t, j + 1)) qk(t, j + 1, t == 1 || !active(1, j + 1));
+        if (next) {
+          if (done > 0) ok = wait(&S.pv_done[u], (done - 1u) & 1u);  // P is read, its columns free
+          if (!ok) break;
+          qk();
+        } else {
+          __syncwarp();
+          if (two && lane == 0) mbar_arrive(&S.turn[1 - u]);
         }
+        release(vs.s, now);
+        if (j + 1 < nt) release(ks.s, next);
+        vs.next();
+      }
       // every UMMA issued has completed before tensor memory is freed
-      umma_commit(&S.mma_done);
-      mbar_wait(&S.mma_done, 0u, abort_flag, &g_attn_win_status, true);
+      umma_commit_warp(&S.mma_done[u]);
+      mbar_wait(&S.mma_done[u], 0u, abort_flag, &g_attn_win_status, true);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -262,8 +317,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     uint64_t l2 = 0;  // the row's sum, as two partial sums
     bool ok = true;
     int n = 0;  // active tiles so far
-    for (int j = 0; j < nt && ok; ++j) {
-      if (!active(t, j)) continue;
+    const Active act = actives(t);
+    for (int j = 0; j < act.end && ok; ++j) {
+      if (!act(j)) continue;
       // row p sees positions k0 + e of the tile with e < lim and (e >= from or e < sk)
       const int64_t k0 = tile_pos(j);
       const bool sink = j < sink_tiles;
