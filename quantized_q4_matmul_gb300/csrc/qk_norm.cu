@@ -14,10 +14,15 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
+
+#ifndef QK_NORM_PER
+#define QK_NORM_PER 2
+#endif
 
 namespace qk {
 
@@ -203,26 +208,31 @@ __device__ __forceinline__ void emit_h(const AddNormArgs& A, size_t row, int c, 
   }
 }
 
+constexpr int kAddNormThreads = 1024;  // at most
+
 template <bool F32, bool Q8>
-__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_kernel(const __grid_constant__ AddNormArgs A) {
-  __shared__ float wsum[kNormThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(kAddNormThreads) add_rmsnorm_kernel(const __grid_constant__ AddNormArgs A) {
+  __shared__ float wsum[kAddNormThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
   const size_t row = (size_t)blockIdx.x * (size_t)A.K;
   const int nc = A.K / 8;
   float h[kNormChunks][8];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kNormChunks; ++i) {
-    const int c = tid + i * kNormThreads;
-    if (c < nc) {
-      load_h<F32>(A, row + 8 * (size_t)c, h[i]);
+    const int c = tid + i * T;
+    if (c < nc) load_h<F32>(A, row + 8 * (size_t)c, h[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kNormChunks; ++i) {
+    if (tid + i * T < nc) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
     }
   }
   // longer rows: the remaining chunks, read again in the second pass (a thread
   // writes only chunks that it alone reads, after reading them: in place is fine)
-  for (int c = tid + kNormChunks * kNormThreads; c < nc; c += kNormThreads) {
+  for (int c = tid + kNormChunks * T; c < nc; c += T) {
     float t[8];
     load_h<F32>(A, row + 8 * (size_t)c, t);
 #pragma unroll
@@ -232,15 +242,17 @@ __global__ void __launch_bounds__(kNormThreads) add_rmsnorm_kernel(const __grid_
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (lane == 0) wsum[warp] = ss;
   __syncthreads();
-  float t = 0.f;
-  for (int w = 0; w < kNormThreads / 32; ++w) t += wsum[w];
+  // every warp adds the warps' sums in the same tree
+  float t = lane < T / 32 ? wsum[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   const float r = 1.0f / sqrtf(t / (float)A.K + A.eps);
 #pragma unroll
   for (int i = 0; i < kNormChunks; ++i) {
-    const int c0 = i * kNormThreads + 32 * warp;  // the warp's first chunk: the warp stays together
+    const int c0 = i * T + 32 * warp;  // the warp's first chunk: the warp stays together
     if (c0 < nc) emit_h<F32, Q8>(A, row, c0 + lane, c0 + lane < nc, h[i], r);
   }
-  for (int c0 = kNormChunks * kNormThreads + 32 * warp; c0 < nc; c0 += kNormThreads) {
+  for (int c0 = kNormChunks * T + 32 * warp; c0 < nc; c0 += T) {
     float u[8];
     if (c0 + lane < nc) load_h<F32>(A, row + 8 * (size_t)(c0 + lane), u);
     emit_h<F32, Q8>(A, row, c0 + lane, c0 + lane < nc, u, r);
@@ -253,18 +265,13 @@ cudaError_t launch_add_rmsnorm(const void* residual, bool f32, const float* delt
                                void* residual_out, uint16_t* xhat, int8_t* xq, float* xd, int64_t M, int64_t K,
                                cudaStream_t s) {
   const AddNormArgs A{residual, delta, gamma, residual_out, xhat, xq, xd, eps, (int)K};
-  const dim3 grid((unsigned)M);
-  if (xq) {
-    if (f32)
-      add_rmsnorm_kernel<true, true><<<grid, kNormThreads, 0, s>>>(A);
-    else
-      add_rmsnorm_kernel<false, true><<<grid, kNormThreads, 0, s>>>(A);
-  } else {
-    if (f32)
-      add_rmsnorm_kernel<true, false><<<grid, kNormThreads, 0, s>>>(A);
-    else
-      add_rmsnorm_kernel<false, false><<<grid, kNormThreads, 0, s>>>(A);
-  }
+  // Threads of a row: one 8-value chunk each where the rows are few (latency),
+  // else QK_NORM_PER.
+  const int64_t per = M <= device_sms() ? 1 : QK_NORM_PER;
+  const int T = (int)std::min<int64_t>(kAddNormThreads, (K / 8 + 32 * per - 1) / (32 * per) * 32);
+  auto kernel = xq ? (f32 ? add_rmsnorm_kernel<true, true> : add_rmsnorm_kernel<false, true>)
+                   : (f32 ? add_rmsnorm_kernel<true, false> : add_rmsnorm_kernel<false, false>);
+  kernel<<<(unsigned)M, T, 0, s>>>(A);
   return cudaGetLastError();
 }
 
