@@ -41,6 +41,7 @@ SYMBOLS = ("qk_dequant_q4k", "qk_dequant_q6k", "qk_matmul_q4k", "qk_matmul_q6k",
            "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_logprobs")
 
 QK_Q4_K, QK_Q6_K = 0, 1
+_QTYPES = {"q4k": QK_Q4_K, "q6k": QK_Q6_K}
 QK_F16, QK_F32 = 0, 1
 QK_ROPE_INTERLEAVED, QK_ROPE_HALF = 0, 1
 QK_ROPE_SCALE_NONE, QK_ROPE_SCALE_LINEAR, QK_ROPE_SCALE_BANDED = 0, 1, 2
@@ -160,36 +161,46 @@ _I32 = ("torch.int32",)
 _dtype_names = {}  # torch dtype -> its name: str() of a dtype takes longer than the lookup
 
 
-def _buf(t, nbytes: int, what: str, dtypes=None) -> int:
+def _buf(t, nbytes: int, what, dtypes=None) -> int:
     """The address of a buffer argument.  A raw integer address (or None) is
     passed through unchecked.  A tensor must be contiguous, of one of `dtypes`
     (any dtype if None), and hold at least `nbytes` bytes: the C ABI takes
-    plain pointers and cannot see how large a buffer is."""
+    plain pointers and cannot see how large a buffer is.  `what` names the
+    argument in the error: a string, or a format and its arguments in a tuple
+    (formatted only then)."""
     if t is None:
         return 0
     if isinstance(t, int):
         return t
-    dtype = t.dtype
-    name = _dtype_names.get(dtype)
-    if name is None:
-        name = _dtype_names[dtype] = str(dtype)
-    if dtypes is not None and name not in dtypes:
-        raise ValueError("%s: dtype %s, expected one of %s" % (what, dtype, ", ".join(dtypes)))
+    if dtypes is not None:
+        dtype = t.dtype
+        name = _dtype_names.get(dtype)
+        if name is None:
+            name = _dtype_names[dtype] = str(dtype)
+        if name not in dtypes:
+            raise ValueError("%s: dtype %s, expected one of %s" % (_what(what), dtype, ", ".join(dtypes)))
     if not t.is_contiguous():
-        raise ValueError("%s: the tensor is not contiguous" % what)
+        raise ValueError("%s: the tensor is not contiguous" % _what(what))
     if t.nbytes < nbytes:
-        raise ValueError("%s: holds %d bytes, the call needs %d" % (what, t.nbytes, nbytes))
+        raise ValueError("%s: holds %d bytes, the call needs %d" % (_what(what), t.nbytes, nbytes))
     return t.data_ptr()
 
 
+def _what(what) -> str:
+    return what if isinstance(what, str) else what[0] % what[1:]
+
+
 def _n(v) -> int:
-    return max(int(v), 0)
+    v = int(v)
+    return v if v > 0 else 0
+
+
+_BLOCK_BYTES = {QK_Q4_K: 144, QK_Q6_K: 210}
 
 
 def _weight_bytes(qtype, N, K) -> int:
     """Bytes of N rows of K/256 super-blocks (0 for shapes the library rejects)."""
-    bb = {QK_Q4_K: 144, QK_Q6_K: 210}.get(qtype, 0)
-    return _n(N) * (_n(K) // 256) * bb
+    return _n(N) * (_n(K) // 256) * _BLOCK_BYTES.get(qtype, 0)
 
 
 _raw_stream = None  # device index -> the address of torch's current stream on it
@@ -267,16 +278,16 @@ def _descs(problems):
     arr = (qk_matmul_desc * max(1, len(problems)))()
     for i, p in enumerate(problems):
         qt = p["qtype"]
-        qt = int({"q4k": QK_Q4_K, "q6k": QK_Q6_K}.get(qt, qt))
+        qt = int(_QTYPES.get(qt, qt))
         M, N, K = int(p["M"]), int(p["N"]), int(p["K"])
-        what = "qk_matmul_batch[%d]" % i
-        gu = p.get("up_blocks") is not None
+        up = p.get("up_blocks")
+        gu = up is not None
         wb = _weight_bytes(qt, N, K)
-        arr[i] = qk_matmul_desc(qt, _buf(p["blocks"], wb, what + ": blocks"),
-                                _buf(p.get("up_blocks"), wb, what + ": up_blocks"),
-                                _buf(p["x_f16"], _n(M) * _n(K) * 2, what + ": x_f16", _F16),
-                                _buf(p["y"], _n(M) * _n(N) * (2 if gu else 4), what + ": y", _F16 if gu else _F32),
-                                M, N, K)
+        arr[i] = qk_matmul_desc(qt, _buf(p["blocks"], wb, ("qk_matmul_batch[%d]: blocks", i)),
+                                _buf(up, wb, ("qk_matmul_batch[%d]: up_blocks", i)),
+                                _buf(p["x_f16"], _n(M) * _n(K) * 2, ("qk_matmul_batch[%d]: x_f16", i), _F16),
+                                _buf(p["y"], _n(M) * _n(N) * (2 if gu else 4), ("qk_matmul_batch[%d]: y", i),
+                                     _F16 if gu else _F32), M, N, K)
     return arr
 
 
@@ -311,30 +322,35 @@ def qk_matmul_batch_q8(problems, stream=None) -> None:
     arr = (qk_matmul_q8_desc * max(1, len(problems)))()
     for i, p in enumerate(problems):
         qt = p["qtype"]
-        qt = int({"q4k": QK_Q4_K, "q6k": QK_Q6_K}.get(qt, qt))
+        qt = int(_QTYPES.get(qt, qt))
         M, N, K = int(p["M"]), int(p["N"]), int(p["K"])
-        what = "qk_matmul_batch_q8[%d]" % i
         up = p.get("up_blocks")
+        gu = up is not None
         wb = _weight_bytes(qt, N, K)
-        arr[i] = qk_matmul_q8_desc(qt, _buf(p["blocks"], wb, what + ": blocks"), _buf(up, wb, what + ": up_blocks"),
-                                   _buf(p["x_q8"], _n(M) * _n(K), what + ": x_q8", _I8),
-                                   _buf(p["x_d"], _n(M) * (_n(K) // 32) * 4, what + ": x_d", _F32),
-                                   _buf(p["y"], _n(M) * _n(N) * (2 if up is not None else 4), what + ": y",
-                                        _F16 if up is not None else _F32), M, N, K)
+        n = _n(M) * _n(K)
+        arr[i] = qk_matmul_q8_desc(qt, _buf(p["blocks"], wb, ("qk_matmul_batch_q8[%d]: blocks", i)),
+                                   _buf(up, wb, ("qk_matmul_batch_q8[%d]: up_blocks", i)),
+                                   _buf(p["x_q8"], n, ("qk_matmul_batch_q8[%d]: x_q8", i), _I8),
+                                   _buf(p["x_d"], n // 8, ("qk_matmul_batch_q8[%d]: x_d", i), _F32),
+                                   _buf(p["y"], _n(M) * _n(N) * (2 if gu else 4), ("qk_matmul_batch_q8[%d]: y", i),
+                                        _F16 if gu else _F32), M, N, K)
     _check(lib().qk_matmul_batch_q8(arr, len(problems), _stream(stream)), "qk_matmul_batch_q8")
 
 
-def _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K):
+def _residual(names, residual, delta, gamma_f16, residual_out, residual_type, n, K):
     """Addresses and element type of an add_rmsnorm call's inputs and residual output."""
     if residual_type is None:
         if isinstance(residual, int) or residual is None:
-            raise ValueError("%s: residual_type is needed for a raw address" % what)
-        residual_type = QK_F32 if str(residual.dtype) in _F32 else QK_F16
-    n = _n(M) * _n(K)
-    types, size = (_F32, 4) if residual_type == QK_F32 else (_F16, 2)
-    return (_buf(residual, n * size, what + ": residual", types), int(residual_type),
-            _buf(delta, 4 * n, what + ": delta", _F32), _buf(gamma_f16, 2 * _n(K), what + ": gamma_f16", _F16),
-            _buf(residual_out, n * size, what + ": residual_out", types))
+            raise ValueError("%s: residual_type is needed for a raw address" % names[0])
+        dtype = residual.dtype
+        residual_type = QK_F32 if (_dtype_names.get(dtype) or str(dtype)) in _F32 else QK_F16
+    types, size = (_F32, 4 * n) if residual_type == QK_F32 else (_F16, 2 * n)
+    return (_buf(residual, size, names[0], types), int(residual_type), _buf(delta, 4 * n, names[1], _F32),
+            _buf(gamma_f16, 2 * K, names[2], _F16), _buf(residual_out, size, names[3], types))
+
+
+_ADD_RMSNORM = tuple("qk_add_rmsnorm: " + n for n in ("residual", "delta", "gamma_f16", "residual_out"))
+_ADD_RMSNORM_Q8 = tuple("qk_add_rmsnorm_q8: " + n for n in ("residual", "delta", "gamma_f16", "residual_out"))
 
 
 def qk_add_rmsnorm(residual, delta, gamma_f16, eps: float, residual_out, xhat_f16, M: int, K: int,
@@ -342,9 +358,10 @@ def qk_add_rmsnorm(residual, delta, gamma_f16, eps: float, residual_out, xhat_f1
     """h = residual + delta, residual_out = h, xhat = fp16(RMSNorm(h) * gamma) (see
     include/qk.h).  residual is fp16 or fp32 (residual_type QK_F16 / QK_F32, by
     default the tensor's own); delta and residual_out may be None."""
-    what = "qk_add_rmsnorm"
-    r, t, d, g, o = _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K)
-    x = _buf(xhat_f16, 2 * _n(M) * _n(K), "qk_add_rmsnorm: xhat_f16", _F16)
+    k = _n(K)
+    n = _n(M) * k
+    r, t, d, g, o = _residual(_ADD_RMSNORM, residual, delta, gamma_f16, residual_out, residual_type, n, k)
+    x = _buf(xhat_f16, 2 * n, "qk_add_rmsnorm: xhat_f16", _F16)
     _check(lib().qk_add_rmsnorm(r, t, d, g, float(eps), o, x, int(M), int(K), _stream(stream)), "qk_add_rmsnorm")
 
 
@@ -352,11 +369,13 @@ def qk_add_rmsnorm_q8(residual, delta, gamma_f16, eps: float, residual_out, xq, 
                       residual_type=None, stream=None) -> None:
     """qk_add_rmsnorm with the activations in int8 (xq [M][K], xd fp32 [M][K / 32]):
     the x of qk_matmul_batch_q8."""
-    what = "qk_add_rmsnorm_q8"
-    r, t, d, g, o = _residual(what, residual, delta, gamma_f16, residual_out, residual_type, M, K)
-    q = _buf(xq, _n(M) * _n(K), "qk_add_rmsnorm_q8: xq", _I8)
-    s = _buf(xd, _n(M) * (_n(K) // 32) * 4, "qk_add_rmsnorm_q8: xd", _F32)
-    _check(lib().qk_add_rmsnorm_q8(r, t, d, g, float(eps), o, q, s, int(M), int(K), _stream(stream)), "qk_add_rmsnorm_q8")
+    k = _n(K)
+    n = _n(M) * k
+    r, t, d, g, o = _residual(_ADD_RMSNORM_Q8, residual, delta, gamma_f16, residual_out, residual_type, n, k)
+    q = _buf(xq, n, "qk_add_rmsnorm_q8: xq", _I8)
+    s = _buf(xd, n // 8, "qk_add_rmsnorm_q8: xd", _F32)
+    _check(lib().qk_add_rmsnorm_q8(r, t, d, g, float(eps), o, q, s, int(M), int(K), _stream(stream)),
+           "qk_add_rmsnorm_q8")
 
 
 def qk_rope_inv_freq(n_rot: int, theta: float, scaling: int = QK_ROPE_SCALE_NONE, factor: float = 1.0,

@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     fence_mbar_init();
   }
   cluster_sync_all();  // barriers initialised; every CTA of the cluster is running (DSMEM below)
+  if (kWin) dependent_wait();
 
   float (*part)[kMaxGroup][kD + 2] = reinterpret_cast<float (*)[kMaxGroup][kD + 2]>(S.k[0]);
   bool ok = true;
@@ -696,9 +697,15 @@ static cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, c
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
+  const dim3 grid((unsigned)C, (unsigned)Hkv, 1);
+  const __half* qh = reinterpret_cast<const __half*>(q);
+  const float sl2e = scale * 1.4426950408889634f;
+  if (kWin)
+    return launch_dependent(attn_decode_kernel<kWin>, grid, kDecThreads, dec_smem(), (unsigned)C, s, tk, tv, tks, tvs, qh,
+                            out, H / Hkv, n, sl2e, C, W);
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)C, (unsigned)Hkv, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kDecThreads);
   cfg.dynamicSmemBytes = dec_smem();
   cfg.stream = s;
@@ -709,8 +716,7 @@ static cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<kWin>, tk, tv, tks, tvs, reinterpret_cast<const __half*>(q), out,
-                            H / Hkv, n, scale * 1.4426950408889634f, C, W);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<kWin>, tk, tv, tks, tvs, qh, out, H / Hkv, n, sl2e, C, W);
 }
 
 cudaError_t launch_attn_window_decode(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out, int H,

@@ -145,6 +145,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch (launch_dependent in qk_internal.h)
+// ---------------------------------------------------------------------------
+// The next kernel may be scheduled now (it waits in turn); nothing before the
+// wait touches what an earlier kernel reads or writes.
+__device__ __forceinline__ void dependent_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // TMA (bulk tensor copies) and proxy fences
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_1d(void* dst, const void* tmap, int32_t x, uint64_t* bar) {

@@ -1413,20 +1413,25 @@ bool plan_gemv(const GemvDesc* d, int count, int sms, GemvBatch* out, size_t* sm
     B.p[i].ctas = 1;
   }
   *smem_out = smem;
+  if (sms == 0) return true;  // the fit alone is asked for
+  // CTAs one by one to the problem whose busiest CTA has the most to do
   const int budget = std::max(count, sms);
+  double load[kMaxGemvProbs];
+  for (int i = 0; i < count; ++i)
+    load[i] = B.p[i].tiles > 1 ? (double)B.p[i].tiles * tile_cost[i] : 0.0;  // 0: no further CTA helps
   for (int used = count; used < budget; ++used) {
     int best = -1;
     double best_load = 0.0;
     for (int i = 0; i < count; ++i) {
-      if (B.p[i].ctas >= B.p[i].tiles) continue;
-      const double load = (double)((B.p[i].tiles + B.p[i].ctas - 1) / B.p[i].ctas) * tile_cost[i];
-      if (load > best_load) {
-        best_load = load;
+      if (load[i] > best_load) {
+        best_load = load[i];
         best = i;
       }
     }
     if (best < 0) break;
-    ++B.p[best].ctas;
+    GemvProb& p = B.p[best];
+    ++p.ctas;
+    load[best] = p.ctas < p.tiles ? (double)((p.tiles + p.ctas - 1) / p.ctas) * tile_cost[best] : 0.0;
   }
   int begin = 0;
   for (int i = 0; i < count; ++i) {
@@ -1476,7 +1481,7 @@ cudaError_t launch_decode(const GemvBatch& B, size_t smem, cudaStream_t s) {
 bool gemv_plan_fits(const GemvDesc* d, int count) {
   GemvBatch B;
   size_t smem = 0;
-  return plan_gemv(d, count, 152, &B, &smem);  // the SM count splits CTAs; it does not decide the fit
+  return plan_gemv(d, count, 0, &B, &smem);  // the SM count splits CTAs; it does not decide the fit
 }
 
 int gemv_slots(int64_t M) { return slots_for(M); }

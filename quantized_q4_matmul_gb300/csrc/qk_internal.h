@@ -42,6 +42,29 @@ class PerDeviceFlag {
   std::atomic<uint64_t> bits_{0};
 };
 
+// Launch a kernel whose CTAs may be scheduled while the kernel before it on the
+// stream finishes (they call dependent_wait before touching memory), in
+// clusters of `cluster` CTAs along x.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                             cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Each translation unit with kernels that can time out owns one device status
 // word; these read it (after the stream has been synchronised) and clear it.
 // Status bit of a copy that a debug build (QK_DEBUG) skipped (qk_device.cuh).

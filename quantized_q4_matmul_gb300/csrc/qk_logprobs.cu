@@ -29,7 +29,6 @@
 
 #include <cfloat>
 #include <cmath>
-#include <cstring>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
@@ -194,6 +193,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   const int64_t v0 = nv * rank / C, v1 = nv * (rank + 1) / C;
   const int batches = (int)((v1 - v0 + kLpBatch - 1) / kLpBatch);
   const int per_seg = (batches + kLpSegs - 1) / kLpSegs;  // batches per segment (1 up to 131072 logits)
+  dependent_wait();
   float given = NAN;
   if (rank == 0 && tid == 0 && A.logprob) {
     const int t = A.tokens[row];
@@ -357,19 +357,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
 
 template <int C>
 cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(a.M * C));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<C>, a);
+  return launch_dependent(logprobs_kernel<C>, dim3((unsigned)(a.M * C)), kLpThreads, 0, C, s, a);
 }
 
 }  // namespace

@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kAddNormThreads) add_rmsnorm_kernel(const __gr
   const int nc = A.K / 8;
   float h[kNormChunks][8];
   float ss = 0.f;
+  dependent_wait();
 #pragma unroll
   for (int i = 0; i < kNormChunks; ++i) {
     const int c = tid + i * T;
@@ -271,8 +272,7 @@ cudaError_t launch_add_rmsnorm(const void* residual, bool f32, const float* delt
   const int T = (int)std::min<int64_t>(kAddNormThreads, (K / 8 + 32 * per - 1) / (32 * per) * 32);
   auto kernel = xq ? (f32 ? add_rmsnorm_kernel<true, true> : add_rmsnorm_kernel<false, true>)
                    : (f32 ? add_rmsnorm_kernel<true, false> : add_rmsnorm_kernel<false, false>);
-  kernel<<<(unsigned)M, T, 0, s>>>(A);
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3((unsigned)M), (unsigned)T, 0, 1, s, A);
 }
 
 // Scratch of qk_rmsnorm_matmul_batch_static, the entry point that allocates

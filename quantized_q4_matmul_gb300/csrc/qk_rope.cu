@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
   const int per_head = A.D / 8, items = (A.H + 2 * A.Hkv) * per_head, step = gridDim.y * kRopeThreads;
   const int apart = A.half ? A.n_rot / 2 : 4;  // from a turning item's first run to its second
   bool ready = false;
+  dependent_wait();
   for (int w0 = blockIdx.y * kRopeThreads + threadIdx.x; w0 - (int)threadIdx.x < items; w0 += kRopeItems * step) {
     uint4 x[kRopeItems], y[kRopeItems];
 #pragma unroll
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
 __global__ void __launch_bounds__(kRopeThreads) rope_kv_any_kernel(const __grid_constant__ RopeArgs A) {
   __shared__ float2 cs[kRopeMaxPairs];
   const int64_t i = blockIdx.x, p = A.pos0 + i;
+  dependent_wait();
   fill_table(A, p, cs);
   __syncthreads();
   const int n4 = A.D / 4, items = (A.H + 2 * A.Hkv) * n4, h = A.n_rot / 2;
@@ -171,11 +173,7 @@ cudaError_t launch_rope_kv(const RopeArgs& a, cudaStream_t s) {
   // Few tokens: a CTA per 256 items, so that the heads' loads are all in flight.
   const int split = a.M < 64 ? (items + kRopeThreads - 1) / kRopeThreads : 1;
   const dim3 grid((unsigned)a.M, (unsigned)split);
-  if (vec)
-    rope_kv_kernel<<<grid, kRopeThreads, 0, s>>>(a);
-  else
-    rope_kv_any_kernel<<<grid, kRopeThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(vec ? rope_kv_kernel : rope_kv_any_kernel, grid, kRopeThreads, 0, 1, s, a);
 }
 
 }  // namespace qk
