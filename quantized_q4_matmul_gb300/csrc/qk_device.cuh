@@ -223,6 +223,10 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Its two halves: everything before the arrival is visible after the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // The shared::cluster address of shared-memory address `a` (of this CTA's
 // window) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t a, uint32_t rank) {

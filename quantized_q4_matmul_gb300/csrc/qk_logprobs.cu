@@ -13,10 +13,10 @@
 // HBM-bound for many rows: the row is read once, 8 independent 16-byte loads
 // per thread and batch.  The alternatives cost almost nothing on the way: a
 // thread notes the maximum of every batch of 32 logits (a segment) that it
-// needs for the rescaling anyway.  Afterwards t0, the n-th largest of the 512
-// threads' maxima, is a lower bound of the n-th largest logit, so the
+// needs for the rescaling anyway.  Afterwards t0, the n-th largest of the maxima
+// of 64 groups of threads, is a lower bound of the n-th largest logit, so the
 // alternatives lie in the few segments whose maximum reaches it; only those
-// (about n of 4008) are read again.
+// (about 1.2 n of 4008) are read again.
 //
 // The order of the alternatives is that of a 64-bit key, the logit's bits in
 // sortable form above the complement of the token: larger logits first, equal
@@ -43,9 +43,13 @@ constexpr int kLpVecs = 8;                           // 16-byte loads per thread
 constexpr int kLpBatch = kLpThreads * kLpVecs;       // vectors per batch
 constexpr int kLpSegs = 8;                           // segments per thread (of one batch each up to 131072 logits)
 constexpr int kLpTop = 32;                           // largest top_n
+constexpr int kLpGroups = 64;                        // groups of 8 threads
 constexpr int kLpTies = 64;                          // segments whose maximum is t0 itself, at most, before the scan
-constexpr int kLpList = kLpTop * kLpSegs + kLpTies;  // segments read again
-constexpr int kLpCand = 1024;                        // candidate keys: 512 kept, 512 of a round
+// Segments above t0: those of the threads of at most top_n - 1 groups.
+constexpr int kLpList = (kLpTop - 1) * (kLpThreads / kLpGroups) * kLpSegs + kLpTies;
+constexpr int kLpUnits = 3;                          // segments of a warp and round
+constexpr int kLpRound = kLpUnits * kLpThreads;      // candidate keys of a round, at most
+constexpr int kLpKeep = 512;                         // and between rounds
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -88,70 +92,107 @@ __device__ __forceinline__ void rescale(Stat& a, float m) {  // to a reference m
   a.m = m;
 }
 
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
+// The lanes' sets in one, in every lane.
+__device__ __forceinline__ void warp_join(Stat& a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   rescale(a, m);
-  rescale(b, m);
-  return Stat{m, a.S + b.S, a.T + b.T};
-}
-
-__device__ __forceinline__ Stat shfl_xor(const Stat& a, int o) {
-  return Stat{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
-              __shfl_xor_sync(0xffffffffu, a.T, o)};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.S += __shfl_xor_sync(0xffffffffu, a.S, o);
+    a.T += __shfl_xor_sync(0xffffffffu, a.T, o);
+  }
 }
 
 struct LpShared {
   float seg[kLpSegs][kLpThreads];  // each thread's segment maxima
-  float top[kLpWarps][kLpTop];     // warps' sorted maxima
-  uint64_t cand[kLpCand];
+  float top[kLpGroups];            // the groups' maxima
+  uint64_t cand[kLpKeep + kLpRound];
   uint64_t best[kLpTop];           // this CTA's top n, sorted
   uint64_t all[kLpMaxCluster * kLpTop];  // rank 0: every CTA's
   Stat wstat[kLpWarps];
   Stat cstat[kLpMaxCluster];       // rank 0: every CTA's
-  int list[kLpList];               // segments to read again: 512 * segment + thread
+  uint16_t list[kLpList];          // segments to read again: 512 * segment + thread
   int n_above, n_equal, n_cand;
 };
+static_assert(sizeof(LpShared) <= 48 * 1024 && kLpSegs * kLpThreads <= 65536, "static shared memory; segment numbers");
 
-// One step of a bitonic sort across the warp: lanes o apart, the larger value
-// to the lower lane where `down`.
+// One step of a bitonic sort of 64 values, two per lane (a: 0 .. 31, b: 32 ..
+// 63): values o apart, the larger to the lower place where `down`.
 __device__ __forceinline__ float exchange(float v, int o, bool down, int lane) {
   const float w = __shfl_xor_sync(0xffffffffu, v, o);
   const bool low = (lane & o) == 0;
   return (low == down) ? fmaxf(v, w) : fminf(v, w);
 }
 
-// The n-th largest (1-based) of one value per thread, to every thread.
-__device__ float nth_of_threads(LpShared& S, float v, int n, int warp, int lane) {
+// A lower bound of the n-th largest of one value per thread that n of them
+// reach: the n-th largest (1-based) of the groups' maxima.  Every warp sorts
+// the 64 maxima for itself.
+__device__ __forceinline__ float bound_of_threads(LpShared& S, float v, int n, int warp, int lane) {
+#pragma unroll
+  for (int o = 1; o < kLpThreads / kLpGroups; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (lane % (kLpThreads / kLpGroups) == 0) S.top[(32 * warp + lane) / (kLpThreads / kLpGroups)] = v;
+  __syncthreads();
+  float a = S.top[lane], b = S.top[lane + 32];
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-    for (int o = k >> 1; o > 0; o >>= 1) v = exchange(v, o, (lane & k) == 0 || k == 32, lane);
-  S.top[warp][lane] = v;
-  // the 32 largest of two descending lists a, b are max(a_i, b_(31 - i)), a bitonic sequence
-  for (int half = kLpWarps / 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if (warp < half) {
-      v = fmaxf(v, S.top[warp + half][31 - lane]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v = exchange(v, o, true, lane);
+    for (int o = k >> 1; o > 0; o >>= 1) {
+      const bool down = (lane & k) == 0 || k == 32;
+      a = exchange(a, o, down, lane);
+      b = exchange(b, o, k == 32 ? false : down, lane);  // ascending in the end: a, b bitonic
     }
-    __syncthreads();
-    if (warp < half) S.top[warp][lane] = v;
-  }
-  __syncthreads();
-  return S.top[0][n - 1];
+  const float hi = fmaxf(a, b), lo = fminf(a, b);
+  a = hi;
+  b = lo;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = exchange(a, o, true, lane);
+  return __shfl_sync(0xffffffffu, a, n - 1);  // n <= 32: among the upper half
 }
 
 // Keep the n largest of cand[0 .. count): sorted into best[], the rest of
-// best[0 .. n) zero.  A key's place is the number of larger keys.
+// best[0 .. n) zero.  A key's place is the number of larger keys, which eight
+// threads count together.
 __device__ void select_n(uint64_t* best, const uint64_t* cand, int count, int n, int tid) {
   if (tid < n) best[tid] = 0;
   __syncthreads();
-  for (int i = tid; i < count; i += kLpThreads) {
-    const uint64_t k = cand[i];
+  for (int i0 = 0; i0 < count; i0 += kLpThreads / 8) {
+    const int i = i0 + tid / 8;
+    const uint64_t k = i < count ? cand[i] : 0;
     int place = 0;
-    for (int j = 0; j < count; ++j) place += cand[j] > k;
-    if (place < n && k != 0) best[place] = k;
+#pragma unroll 4
+    for (int j = tid % 8; j < count; j += 8) place += cand[j] > k;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (tid % 8 == 0 && place < n && k != 0) best[place] = k;
+  }
+  __syncthreads();
+}
+
+// The same for `lists` (at most 8) lists of n keys, each in order: one thread
+// for each list finds by halving how many of its keys are larger.
+__device__ void select_n_sorted(uint64_t* best, const uint64_t* keys, int lists, int n, int tid) {
+  if (tid < n) best[tid] = 0;
+  __syncthreads();
+  for (int i0 = 0; i0 < lists * n; i0 += kLpThreads / 8) {
+    const int i = i0 + tid / 8, q = tid % 8;
+    const uint64_t k = i < lists * n ? keys[i] : 0;
+    int place = 0;
+    if (q < lists) {
+      int hi = n;
+      while (place < hi) {
+        const int mid = (place + hi) / 2;
+        if (keys[q * n + mid] > k)
+          place = mid + 1;
+        else
+          hi = mid;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (q == 0 && place < n && k != 0) best[place] = k;
   }
   __syncthreads();
 }
@@ -166,12 +207,12 @@ __device__ __forceinline__ void append(LpShared& S, uint64_t key, bool on, int l
   if (on) S.cand[at + __popc(b & ((1u << lane) - 1u))] = key;
 }
 
-// After a round of at most 512 appended keys: keep n if there is no room for another.
+// After a round of at most kLpRound appended keys: keep n if there is no room for another.
 __device__ __forceinline__ void make_room(LpShared& S, int n, int tid) {
   __syncthreads();
   const int count = S.n_cand;
   __syncthreads();  // read by every thread before the next round adds to it
-  if (count <= kLpCand - kLpThreads) return;
+  if (count <= kLpKeep) return;
   select_n(S.best, S.cand, count, n, tid);
   if (tid < n) S.cand[tid] = S.best[tid];
   if (tid == 0) S.n_cand = n;
@@ -193,12 +234,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   const int64_t v0 = nv * rank / C, v1 = nv * (rank + 1) / C;
   const int batches = (int)((v1 - v0 + kLpBatch - 1) / kLpBatch);
   const int per_seg = (batches + kLpSegs - 1) / kLpSegs;  // batches per segment (1 up to 131072 logits)
+  if (C > 1) cluster_arrive();
   dependent_wait();
-  float given = NAN;
-  if (rank == 0 && tid == 0 && A.logprob) {
-    const int t = A.tokens[row];
-    if (t >= 0 && t < V) given = x[t];
-  }
+  const int token = rank == 0 && tid == 0 && A.logprob ? A.tokens[row] : -1;
   if (tid == 0) S.n_above = S.n_equal = S.n_cand = 0;
 
   // ------------------------------------------------------------ the one pass
@@ -249,47 +287,54 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     if (n > 0) S.seg[s][tid] = smax;
     most = fmaxf(most, smax);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) st = join(st, shfl_xor(st, o));
+  const float given = token >= 0 && token < V ? x[token] : NAN;
+  warp_join(st);
   if (lane == 0) S.wstat[warp] = st;
 
   // -------------------------------------------------------- the alternatives
   if (n > 0) {
-    const float t0 = nth_of_threads(S, most, n, warp, lane);
+    const float t0 = bound_of_threads(S, most, n, warp, lane);
     const uint32_t b0 = order_bits(t0);
     const int segs = batches > 0 ? (batches + per_seg - 1) / per_seg : 0;
-    for (int s = 0; s < segs; ++s) {
-      const bool filled = v0 + (int64_t)s * per_seg * kLpBatch + tid < v1;
-      const float smax = S.seg[s][tid];
-      if (filled && smax > t0) S.list[atomicAdd(&S.n_above, 1)] = s * kLpThreads + tid;  // at most n - 1 threads
+    if (most >= t0) {
+      for (int s = 0; s < segs; ++s) {
+        if (v0 + (int64_t)s * per_seg * kLpBatch + tid >= v1) break;  // nothing of the slice is in it
+        const float smax = S.seg[s][tid];
+        if (smax > t0) {
+          S.list[atomicAdd(&S.n_above, 1)] = (uint16_t)(s * kLpThreads + tid);
+        } else if (smax >= t0) {  // from the list's end
+          const int i = atomicAdd(&S.n_equal, 1);
+          if (i < kLpTies) S.list[kLpList - 1 - i] = (uint16_t)(s * kLpThreads + tid);
+        }
+      }
     }
     __syncthreads();
     const int above = S.n_above;
-    for (int s = 0; s < segs; ++s) {
-      const bool filled = v0 + (int64_t)s * per_seg * kLpBatch + tid < v1;
-      if (filled && !(S.seg[s][tid] > t0) && S.seg[s][tid] >= t0) {
-        const int i = atomicAdd(&S.n_equal, 1);
-        if (i < kLpTies) S.list[above + i] = s * kLpThreads + tid;
-      }
-    }
-    __syncthreads();
     const bool scan = S.n_equal > kLpTies;  // many logits equal to t0: found by the scan below instead
     const int units = (above + (scan ? 0 : S.n_equal)) * per_seg;
-    for (int u0 = 0; u0 < units; u0 += kLpWarps) {
-      const int u = u0 + warp;
-      bool on = false;
-      uint64_t key = 0;
-      if (u < units) {
-        const int seg = S.list[u / per_seg], b = (seg / kLpThreads) * per_seg + u % per_seg;
-        const int64_t v = v0 + (int64_t)b * kLpBatch + (lane >> 2) * kLpThreads + seg % kLpThreads;
-        const int64_t at = 4 * v - shift + (lane & 3);
-        if (v < v1 && at >= 0 && at < V) {
-          const uint32_t bits = order_bits(x[at]);
-          on = scan ? bits > b0 : bits >= b0;
-          key = key_of(bits, (int)at);
+    for (int u0 = 0; u0 < units; u0 += kLpUnits * kLpWarps) {
+      float f[kLpUnits];
+      int token[kLpUnits];
+#pragma unroll
+      for (int i = 0; i < kLpUnits; ++i) {
+        const int u = u0 + i * kLpWarps + warp;
+        token[i] = -1;
+        if (u < units) {
+          const int q = u / per_seg, seg = S.list[q < above ? q : kLpList - 1 - (q - above)];
+          const int b = (seg / kLpThreads) * per_seg + u % per_seg;
+          const int64_t v = v0 + (int64_t)b * kLpBatch + (lane >> 2) * kLpThreads + seg % kLpThreads;
+          const int64_t at = 4 * v - shift + (lane & 3);
+          if (v < v1 && at >= 0 && at < V) {
+            token[i] = (int)at;
+            f[i] = x[at];
+          }
         }
       }
-      append(S, key, on, lane);
+#pragma unroll
+      for (int i = 0; i < kLpUnits; ++i) {
+        const uint32_t bits = token[i] >= 0 ? order_bits(f[i]) : 0u;
+        append(S, key_of(bits, token[i]), token[i] >= 0 && (scan ? bits > b0 : bits >= b0), lane);
+      }
       make_room(S, n, tid);
     }
     // Ties at t0, and, where logits are NaN, those: in token order until n are found.
@@ -316,13 +361,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
 
   // ---------------------------------------------------------------- the join
   if (warp == 0) {
-    st = S.wstat[lane % kLpWarps];
-#pragma unroll
-    for (int o = kLpWarps / 2; o > 0; o >>= 1) st = join(st, shfl_xor(st, o));
+    st = lane < kLpWarps ? S.wstat[lane] : Stat{-FLT_MAX, 0.f, 0.f};
+    warp_join(st);
   }
   const uint64_t* best = S.best;
   if (C > 1) {
-    cluster_sync_all();  // every CTA of the cluster is running
+    cluster_wait();  // every CTA of the cluster is running
     if (warp == 0) {
       const uint32_t to = mapa_shared(smem_u32(&S.cstat[rank]), 0);
       const float part[3] = {st.m, st.S, st.T};
@@ -336,10 +380,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     }
     cluster_sync_all();
     if (rank != 0) return;
-    if (n > 0) select_n(S.best, S.all, C * n, n, tid);
+    if (n > 0) select_n_sorted(S.best, S.all, C, n, tid);
     if (warp == 0) {
-      st = S.cstat[0];
-      for (int r = 1; r < C; ++r) st = join(st, S.cstat[r]);
+      st = lane < C ? S.cstat[lane] : Stat{-FLT_MAX, 0.f, 0.f};
+      warp_join(st);
     }
   }
   if (warp != 0) return;
