@@ -25,6 +25,10 @@
 // meet, one run from position 0.  A position that no query of the CTA sees is
 // never loaded.
 //
+// Few queries (a short chunk after a long context) make few CTAs, so a cluster of
+// up to eight shares a CTA's work: each takes a run of its key tiles, and they
+// join their (maximum, sum, O) through distributed shared memory, in rank order.
+//
 // Decode (M = 1) runs in qk_attn.cu.
 //
 // All waits are bounded; a timeout raises the device status word.
@@ -32,8 +36,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <cstring>
 
 #include "qk_attn.cuh"
 #include "qk_device.cuh"
@@ -49,6 +54,7 @@ constexpr int kWK = 128;         // positions per key / value tile
 constexpr int kWRing = 5;        // key and value tiles in flight, in the order of their use: K0 V0 K1 V1 ...
 constexpr int kWWarps = 12;      // copy, 2 UMMA issuers, 1 idle, 4 softmax warps for each query tile
 constexpr int kWThreads = 32 * kWWarps;
+constexpr int kWMaxSplit = 8;    // CTAs that share the key tiles of a pair of query tiles
 
 struct WpShared {
   uint8_t q[2][kTTile];
@@ -70,7 +76,32 @@ struct WpArgs {
   int H, Hkv, G, queries;  // query heads, key/value heads, heads per key/value head, queries per tile
   int64_t M, pos0, window, sinks;
   float scale_log2e;
+  int split;  // CTAs (of a cluster) that share a pair of query tiles
 };
+
+// What a CTA of a cluster leaves for the others, where its key and value tiles
+// were: O of its query tiles, rows of 512 bytes whose 16-byte chunks are
+// permuted by the row (a warp writes one chunk of 32 rows at a time), and each
+// row's reference and sum.
+__device__ __forceinline__ uint32_t part_chunk(const WpShared& S, int t, int r, int c) {
+  return smem_u32(S.kv[2 * t]) + (uint32_t)(r * 512 + ((c ^ (r & 31)) << 4));
+}
+__device__ __forceinline__ uint32_t part_stat(const WpShared& S, int t, int r) {
+  return smem_u32(S.kv[4]) + (uint32_t)(8 * (128 * t + r));
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
 
 // Packed pairs of fp32 (one instruction for two values).
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -109,8 +140,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
   WpShared& S = *reinterpret_cast<WpShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // every head's latest queries, which see the most, first
-  const int g = (int)(blockIdx.x % (unsigned)A.Hkv), G = A.G;
-  const int64_t q0 = (int64_t)((gridDim.x - 1 - blockIdx.x) / (unsigned)A.Hkv) * 2 * A.queries;
+  const unsigned unit = blockIdx.x / (unsigned)A.split, units = gridDim.x / (unsigned)A.split;
+  const int rank = (int)(blockIdx.x - unit * (unsigned)A.split);
+  const int g = (int)(unit % (unsigned)A.Hkv), G = A.G;
+  const int64_t q0 = (int64_t)((units - 1 - unit) / (unsigned)A.Hkv) * 2 * A.queries;
   const bool two = q0 + A.queries < A.M;
   // positions of each query tile's first and last query
   const int64_t pf0 = A.pos0 + q0, pf1 = pf0 + A.queries, end = A.pos0 + A.M - 1;
@@ -128,9 +161,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
       sink_tiles = (int)((A.sinks + kWK - 1) / kWK);
     nt = sink_tiles + (int)((last - first + kWK) / kWK);
   }
+  // This CTA's run of them, numbered from 0 from here on.
+  const int j0 = (int)((int64_t)rank * nt / A.split);
+  nt = (int)((int64_t)(rank + 1) * nt / A.split) - j0;
+  sink_tiles -= j0;
   // Position of the first row of tile j: in the sinks' map, or in the cache.
   auto tile_pos = [&](int j) -> int64_t {
-    return j < sink_tiles ? (int64_t)j * kWK : first + (int64_t)(j - sink_tiles) * kWK;
+    return j < sink_tiles ? (int64_t)(j + j0) * kWK : first + (int64_t)(j - sink_tiles) * kWK;
   };
   // Query tile u has rows that see something of tile j: those up to its last
   // query, but for a gap between the sinks and its first query's window.
@@ -143,10 +180,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (u == 1 && !two) return r;
     const int64_t pf = u ? pf1 : pf0, pl = u ? pl1 : pl0;
     if (A.window == 0) {
-      r.end = min(nt, (int)(pl / kWK) + 1);
+      r.end = min(nt, (int)(pl / kWK) + 1 - j0);
       return r;
     }
-    r.end = sink_tiles + (int)((pl - first) / kWK) + 1;
+    r.end = min(nt, sink_tiles + (int)((pl - first) / kWK) + 1);
     const int64_t hidden = pf - A.window - first + 1;  // positions of the run before the window
     const int64_t kept = A.sinks - first;              // those of them that are sinks
     r.gap0 = sink_tiles + (int)(kept > 0 ? (kept + kWK - 1) / kWK : 0);
@@ -180,10 +217,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   volatile uint32_t* abort_flag = &S.abort_flag;
+  dependent_wait();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copy warp
-    if (lane == 0) {
+    if (lane == 0 && nt > 0) {
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
@@ -218,9 +256,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // elected lane issues.  The tiles take turns, each with its P V and its next
     // S, so that the tensor core works for one while the other's softmax runs:
     // left alone, the two fall into step, share the tensor core and then leave
-    // it idle together (3650 clocks for a key tile of both, in turns TURNCLK).
+    // it idle together (3650 clocks for a key tile of both, in turns 3380).
     const int u = warp - 1;
-    if (u == 0 || two) {
+    if (nt > 0 && (u == 0 || two)) {
       constexpr uint32_t idesc_s = umma_idesc_f16(128, kWK);
       constexpr uint32_t idesc_pv = umma_idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
       const uint32_t t_s = __shfl_sync(0xffffffffu, tmem, 0) + (uint32_t)(128 * u), t_o = t_s + 256u;
@@ -412,32 +450,83 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       ++n;
     }
-    if (ok && n > 0) {
-      ok = mbar_wait(&S.pv_done[t], (uint32_t)(n - 1) & 1u, abort_flag, &g_attn_win_status);
-      ok = __all_sync(0xffffffffu, ok);
+    if (ok && n > 0) ok = mbar_wait(&S.pv_done[t], (uint32_t)(n - 1) & 1u, abort_flag, &g_attn_win_status);
+    ok = __all_sync(0xffffffffu, ok) && n > 0;
+    float a, b;
+    unpack2(l2, a, b);
+    if (A.split > 1) {
+      // Every UMMA of both query tiles is done: their key and value tiles may go.
+      named_bar_sync(1, 256u);
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_stat(S, t, r)), "f"(ok ? m : -INFINITY), "f"(a + b)
+                   : "memory");
       if (ok) {
         tc_fence_after();
-        float a, b;
-        unpack2(l2, a, b);
-        const float inv = 1.0f / (a + b);
-        const bool on = r < G * A.queries && row < A.M;
-        __half* dst = A.out + (row * A.H + g * G + r % G) * kD;
 #pragma unroll 1
         for (int c = 0; c < kD / 16; ++c) {
-          uint32_t w[16], o[8];
+          uint32_t w[16];
           tmem_ld16(t_o + (uint32_t)(16 * c), w);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            o[e] = pack_h2(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
-          if (on) {
-            uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-          }
+          for (int e = 0; e < 4; ++e)
+            sts128_u(part_chunk(S, t, r, 4 * c + e), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        }
+      }
+    } else if (ok) {
+      tc_fence_after();
+      const float inv = 1.0f / (a + b);
+      const bool on = r < G * A.queries && row < A.M;
+      __half* dst = A.out + (row * A.H + g * G + r % G) * kD;
+#pragma unroll 1
+      for (int c = 0; c < kD / 16; ++c) {
+        uint32_t w[16], o[8];
+        tmem_ld16(t_o + (uint32_t)(16 * c), w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          o[e] = pack_h2(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+        if (on) {
+          uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
+          d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          d[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
     }
+    __syncwarp();
+  }
+  if (A.split > 1) {
+    cluster_sync_all();  // every CTA's part is in its shared memory
+    // A warp joins one row at a time, a lane four of its columns.
+    for (int i = warp * A.split + rank; i < 256; i += kWWarps * A.split) {
+      const int t = i >> 7, r = i & 127;
+      const int64_t row = q0 + t * A.queries + r / G;
+      if (r >= G * A.queries || row >= A.M) continue;
+      float2 st[kWMaxSplit];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kWMaxSplit; ++c) {
+        st[c] = make_float2(-INFINITY, 0.f);
+        if (c < A.split) st[c] = ld_cluster2(mapa_shared(part_stat(S, t, r), (uint32_t)c));
+        mx = fmaxf(mx, st[c].x);
+      }
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kWMaxSplit; ++c) {
+        if (st[c].x == -INFINITY) continue;  // it saw nothing of this row
+        const float w = exp2f(st[c].x - mx);
+        const float4 v = ld_cluster4(mapa_shared(part_chunk(S, t, r, lane), (uint32_t)c));
+        l = fmaf(w, st[c].y, l);
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+      }
+      const float inv = 1.0f / l;
+      *reinterpret_cast<uint2*>(A.out + (row * A.H + g * G + r % G) * kD + 4 * lane) =
+          make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while its part is read
   }
   tc_fence_before();
   __syncthreads();
@@ -449,6 +538,36 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
 constexpr size_t kWpSmem = sizeof(WpShared) + 1024;  // + alignment slack
 static_assert(kWpSmem <= 227 * 1024, "shared memory of a CTA");
+
+// How many clusters of `split` CTAs of the prefill kernel the device runs at
+// once: a cluster lies within one GPC, so fewer than SMs / split.  Asked once per
+// device and size; the kernel's attributes are set before.
+int max_clusters(int split) {
+  static std::atomic<int> known[kMaxDevices][kWMaxSplit + 1];
+  const int dev = current_device();
+  if (dev < 0) return 0;
+  int n = known[dev][split].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = kWpSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, attn_win_prefill_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    n = n > 0 ? n : -1;  // -1: none
+    known[dev][split].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 cudaError_t launch_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t* vc, uint16_t* out, int64_t M, int H,
                            int Hkv, int64_t pos0, int64_t Lmax, float scale, int64_t window, int64_t sinks,
@@ -488,9 +607,18 @@ cudaError_t launch_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t
   if (sl2e == 0.f) sl2e = 1e-37f;
   const int64_t nqb = (M + 2 * queries - 1) / (2 * queries);
   if (nqb * Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const WpArgs A{reinterpret_cast<__half*>(out), H, Hkv, G, queries, M, pos0, window, sinks, sl2e};
-  attn_win_prefill_kernel<<<(unsigned)(nqb * Hkv), kWThreads, kWpSmem, s>>>(tq, tk, tv, tks, tvs, A);
-  return cudaGetLastError();
+  // A cluster shares the work while all clusters run at once and each CTA has
+  // two key tiles of the longest query tiles at least (the joining costs about
+  // as much as one).  8 key/value heads, us with 1, 2, 4, 8 CTAs: 10 queries
+  // after 15000 positions, window 2500: 36, 22, 14, 10; 128 after 8000, window
+  // 2048: 39, 28, 19, 30 (16 clusters of 8 take two turns).
+  const int64_t units = nqb * Hkv, span = std::min(window + 2 * queries, pos0 + M);
+  const int64_t tiles = (std::min(sinks, pos0 + M - span) + kWK - 1) / kWK + (span + kWK - 1) / kWK;
+  int split = 1;
+  while (split < kWMaxSplit && tiles >= 4 * split && units <= max_clusters(2 * split)) split *= 2;
+  const WpArgs A{reinterpret_cast<__half*>(out), H, Hkv, G, queries, M, pos0, window, sinks, sl2e, split};
+  return launch_dependent(attn_win_prefill_kernel, dim3((unsigned)(units * split)), kWThreads, kWpSmem, (unsigned)split,
+                          s, tq, tk, tv, tks, tvs, A);
 }
 
 }  // namespace

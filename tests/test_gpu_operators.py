@@ -359,6 +359,25 @@ def test_window_prefill(qk_lib, cuda, M, pos0, window, sinks):
     _attn_check(got, _attn_reference(q, k, v, H, Hkv, pos0, window, sinks), v, "prefill")
 
 
+@pytest.mark.parametrize("M,pos0,window,sinks,H,Hkv", [
+    (2, 6000, 4096, 4, 24, 8), (5, 3000, 10 ** 6, 0, 8, 8), (43, 2500, 2048, 300, 6, 2), (85, 1500, 1200, 16, 24, 8),
+    (9, 4000, 0, 4000, 4, 1), (130, 3000, 2900, 7, 7, 1), (16, 2000, 1, 1500, 32, 4), (300, 100, 150, 100, 8, 8),
+    (257, 0, 10 ** 6, 0, 2, 2), (24, 1023, 1024, 1, 16, 2)])
+def test_window_short_chunks(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
+    """Few queries after a long context: a cluster shares their key tiles.  The
+    joining is fp32, a few steps of 2^-24: the same tolerance."""
+    q, k, v = _attn_inputs(220, M, H, Hkv, pos0, pos0 + M + 1, window, sinks)
+    got = _attn(qk_lib, cuda, q, k, v, H, Hkv, pos0, window, sinks)
+    _attn_check(got, _attn_reference(q, k, v, H, Hkv, pos0, window, sinks), v, "short chunk")
+
+
+def test_window_is_deterministic(qk_lib, cuda):
+    for M, pos0, window, sinks in ((1, 5000, 3000, 4), (7, 5000, 3000, 4), (300, 50, 100, 4), (1300, 0, 700, 0)):
+        q, k, v = _attn_inputs(221, M, 24, 8, pos0, pos0 + M, window, sinks)
+        a, b = (_attn(qk_lib, cuda, q, k, v, 24, 8, pos0, window, sinks) for _ in range(2))
+        assert np.array_equal(a, b)
+
+
 def test_window_large_prefill_sampled(qk_lib, cuda):
     H, Hkv, M, pos0, window, sinks = 24, 8, 1500, 700, 512, 4
     q, k, v = _attn_inputs(210, M, H, Hkv, pos0, pos0 + M, window, sinks)
