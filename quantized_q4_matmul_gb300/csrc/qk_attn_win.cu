@@ -256,7 +256,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // elected lane issues.  The tiles take turns, each with its P V and its next
     // S, so that the tensor core works for one while the other's softmax runs:
     // left alone, the two fall into step, share the tensor core and then leave
-    // it idle together (3650 clocks for a key tile of both, in turns 3380).
+    // it idle together.  Within a turn P is taken in halves, as the softmax makes
+    // it; the turn ends when the next S is issued, not when it is done.  4095
+    // queries after 4001, 24 heads over 8, window 2048: 149 us with one issuing
+    // thread for both, 121 with turns, 114 with the halves, 109 with the softmax's
+    // sums in four chains.
     const int u = warp - 1;
     if (nt > 0 && (u == 0 || two)) {
       constexpr uint32_t idesc_s = umma_idesc_f16(128, kWK);
@@ -280,16 +284,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
       } ks{0, 0u}, vs{1, 0u};
       uint32_t done = 0;  // tiles whose P V is issued
       bool ok = wait(&S.q_full, 0u);
-      // What a turn needs is waited for before it: on the way through a turn
-      // only the end of P V holds the next S up (they share columns).
+      // The end of P V holds the next S up (they share columns).
       auto qk = [&]() {
         tc_fence_after();
         const uint32_t ka = kv_s + (uint32_t)(ks.s * kTTile);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
+        for (int kk = 0; kk < 8; ++kk)
           umma_f16_ss_warp(t_s, kmajor_desc(qa, kk), kmajor_desc(ka, kk), idesc_s, kk > 0 ? 1u : 0u);
-          if (kk == 3 && two && lane == 0) mbar_arrive(&S.turn[1 - u]);  // the hand-over takes as long as the rest
-        }
+        if (two && lane == 0) mbar_arrive(&S.turn[1 - u]);
         umma_commit_warp(&S.s_full[u]);
       };
       auto release = [&](int slot, bool used) {
@@ -311,16 +313,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ks.next();
         ok = wait(&S.full[vs.s], vs.phase);
         if (ok && j + 1 < nt) ok = wait(&S.full[ks.s], ks.phase);
-        if (ok && now) ok = wait(&S.p_full[u][0], done & 1u) && wait(&S.p_full[u][1], done & 1u);
         if (two && ok) ok = wait(&S.turn[u], (uint32_t)(u == 0 ? j : j + 1) & 1u);
+        if (ok && now) ok = wait(&S.p_full[u][0], done & 1u);
         if (!ok) break;
         if (now) {
           tc_fence_after();
           const uint32_t va = kv_s + (uint32_t)(vs.s * kTTile);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < 4; ++kk)
             umma_f16_ts_warp(t_o, t_s + (uint32_t)(8 * kk), mnmajor_desc(va, kk), idesc_pv,
                              (done > 0 || kk > 0) ? 1u : 0u);
+          ok = wait(&S.p_full[u][1], done & 1u);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            umma_f16_ts_warp(t_o, t_s + (uint32_t)(8 * kk), mnmajor_desc(va, kk), idesc_pv, 1u);
           ++done;
           umma_commit_warp(&S.pv_done[u]);
         }
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const float scale = A.scale_log2e;
     const bool neg = scale < 0.f;
     float m = -INFINITY;
-    uint64_t l2 = 0;  // the row's sum, as two partial sums
+    uint64_t l2 = 0, l3 = 0;  // the row's sum, as four partial sums (short chains)
     bool ok = true;
     int n = 0;  // active tiles so far
     const Active act = actives(t);
@@ -411,6 +419,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const float mref = m == -INFINITY ? 0.f : m;
       if (__any_sync(0xffffffffu, upd)) {
         float a, b;
+        l2 = add2(l2, l3);
+        l3 = 0;
         unpack2(l2, a, b);
         l2 = pack2(a * corr, b * corr);
         if (n > 0) {  // S was issued after the tile before was added to O
@@ -438,7 +448,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
             unpack2(fma2(pack2(__uint_as_float(v[e0 + e]), __uint_as_float(v[e0 + e + 1])), sc2, mm2), a, b);
             a = ex2_approx(a);
             b = ex2_approx(b);
-            l2 = add2(l2, pack2(a, b));
+            if (e & 2)
+              l3 = add2(l3, pack2(a, b));
+            else
+              l2 = add2(l2, pack2(a, b));
             hp[e >> 1] = pack_h2(a, b);
           }
           tmem_st16(t_s + (uint32_t)(e0 / 2), hp);
@@ -453,6 +466,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (ok && n > 0) ok = mbar_wait(&S.pv_done[t], (uint32_t)(n - 1) & 1u, abort_flag, &g_attn_win_status);
     ok = __all_sync(0xffffffffu, ok) && n > 0;
     float a, b;
+    l2 = add2(l2, l3);
     unpack2(l2, a, b);
     if (A.split > 1) {
       // Every UMMA of both query tiles is done: their key and value tiles may go.
