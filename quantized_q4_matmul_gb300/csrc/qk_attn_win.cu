@@ -28,6 +28,8 @@
 // Few queries (a short chunk after a long context) make few CTAs, so a cluster of
 // up to eight shares a CTA's work: each takes a run of its key tiles, and they
 // join their (maximum, sum, O) through distributed shared memory, in rank order.
+// Pairs of query tiles that would leave most of a last round of SMs idle are
+// taken apart: a CTA for each tile.
 //
 // Decode (M = 1) runs in qk_attn.cu.
 //
@@ -76,7 +78,8 @@ struct WpArgs {
   int H, Hkv, G, queries;  // query heads, key/value heads, heads per key/value head, queries per tile
   int64_t M, pos0, window, sinks;
   float scale_log2e;
-  int split;  // CTAs (of a cluster) that share a pair of query tiles
+  unsigned units, pairs;  // pairs of query tiles of all key/value heads; those of them that are one CTA's
+  int split;              // CTAs (of a cluster) that share a pair of query tiles
 };
 
 // What a CTA of a cluster leaves for the others, where its key and value tiles
@@ -139,12 +142,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   WpShared& S = *reinterpret_cast<WpShared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // every head's latest queries, which see the most, first
-  const unsigned unit = blockIdx.x / (unsigned)A.split, units = gridDim.x / (unsigned)A.split;
+  // every head's latest queries, which see the most, first; after A.pairs pairs
+  // of query tiles a CTA has one tile
+  unsigned unit = blockIdx.x / (unsigned)A.split;
   const int rank = (int)(blockIdx.x - unit * (unsigned)A.split);
+  const unsigned single = unit < A.pairs ? 0u : unit - A.pairs;
+  if (unit >= A.pairs) unit = A.pairs + single / 2u;
   const int g = (int)(unit % (unsigned)A.Hkv), G = A.G;
-  const int64_t q0 = (int64_t)((units - 1 - unit) / (unsigned)A.Hkv) * 2 * A.queries;
-  const bool two = q0 + A.queries < A.M;
+  const int64_t q0 = ((int64_t)((A.units - 1u - unit) / (unsigned)A.Hkv) * 2 + (single & 1u)) * A.queries;
+  const bool two = unit < A.pairs && q0 + A.queries < A.M;
   // positions of each query tile's first and last query
   const int64_t pf0 = A.pos0 + q0, pf1 = pf0 + A.queries, end = A.pos0 + A.M - 1;
   const int64_t pl0 = min(pf1 - 1, end), pl1 = min(pf1 + A.queries - 1, end);
@@ -161,6 +167,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       sink_tiles = (int)((A.sinks + kWK - 1) / kWK);
     nt = sink_tiles + (int)((last - first + kWK) / kWK);
   }
+  if (q0 >= A.M) nt = 0;  // the second tile of a pair that has one
   // This CTA's run of them, numbered from 0 from here on.
   const int j0 = (int)((int64_t)rank * nt / A.split);
   nt = (int)((int64_t)(rank + 1) * nt / A.split) - j0;
@@ -630,8 +637,26 @@ cudaError_t launch_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t
   const int64_t tiles = (std::min(sinks, pos0 + M - span) + kWK - 1) / kWK + (span + kWK - 1) / kWK;
   int split = 1;
   while (split < kWMaxSplit && tiles >= 4 * split && units <= max_clusters(2 * split)) split *= 2;
-  const WpArgs A{reinterpret_cast<__half*>(out), H, Hkv, G, queries, M, pos0, window, sinks, sl2e, split};
-  return launch_dependent(attn_win_prefill_kernel, dim3((unsigned)(units * split)), kWThreads, kWpSmem, (unsigned)split,
+  // Pairs beyond whole rounds of the SMs that would fill at most half of another
+  // go to a CTA for each query tile.  24 heads over 8, us with one CTA for a pair
+  // and with one for each: 600 queries after 300, window 128 (64 pairs): 11.8,
+  // 9.6; 2048 after 8000, window 2048 (200): 70.0, 64.8.
+  const int64_t sms = device_sms(), over = units % sms;
+  const int64_t singles = split == 1 && M > queries && 2 * over <= sms ? over : 0;
+  const WpArgs A{reinterpret_cast<__half*>(out),
+                 H,
+                 Hkv,
+                 G,
+                 queries,
+                 M,
+                 pos0,
+                 window,
+                 sinks,
+                 sl2e,
+                 (unsigned)units,
+                 (unsigned)(units - singles),
+                 split};
+  return launch_dependent(attn_win_prefill_kernel, dim3((unsigned)((units + singles) * split)), kWThreads, kWpSmem, (unsigned)split,
                           s, tq, tk, tv, tks, tvs, A);
 }
 

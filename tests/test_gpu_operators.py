@@ -378,6 +378,17 @@ def test_window_is_deterministic(qk_lib, cuda):
         assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("M,pos0,window,sinks,H,Hkv", [
+    (900, 30, 60, 3, 40, 40), (1150, 0, 33, 0, 40, 40), (150, 7, 50, 4, 40, 20), (300, 400, 20, 200, 8, 8)])
+def test_window_pairs_and_single_tiles(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
+    """More query tiles than SMs take, few more, or an odd number of them."""
+    q, k, v = _attn_inputs(224, M, H, Hkv, pos0, pos0 + M, window, sinks)
+    rows = np.unique(np.concatenate([[0, 63, 64, 127, 128, M - 1], synth.rng_for(225, M).choice(M, 60)]))
+    got = _attn(qk_lib, cuda, q, k, v, H, Hkv, pos0, window, sinks)
+    assert np.isfinite(got).all()
+    _attn_check(got[rows], _attn_reference(q, k, v, H, Hkv, pos0, window, sinks, rows), v, "pairs and tiles")
+
+
 def test_window_large_prefill_sampled(qk_lib, cuda):
     H, Hkv, M, pos0, window, sinks = 24, 8, 1500, 700, 512, 4
     q, k, v = _attn_inputs(210, M, H, Hkv, pos0, pos0 + M, window, sinks)
