@@ -31,11 +31,12 @@
 //   * Per sub-block, with Sx the sum of x over the lane's k-slots of it:
 //       Q4_K: sum(w*x) = (d*sc/F) * (D - 1024*Sx) - (dmin*m) * Sx
 //       Q6_K: sum(w*x) = (d*sc/F) * (D - (1024 + 32F)*Sx)
-//   * Reduction: compute warp w takes the blocks j = w mod kDW of every tile
-//     and leaves its sums of a finished tile in the stage's partials slot;
-//     the producer adds the kDW warps' sums in warp order before it refills
-//     the stage and writes y.  The order of every addition depends on the
-//     problem's shape only (deterministic, and the same alone or grouped).
+//   * Reduction: a compute warp takes the blocks j = c mod kDW of a tile, with
+//     a class c that moves from tile to tile, and leaves its sums of a finished
+//     tile in slot c of the stage's partials; the producer adds the kDW classes'
+//     sums in their order before it refills the stage and writes y.  The order
+//     of every addition depends on the problem's shape only (deterministic, and
+//     the same alone or grouped).
 // Q6_K blocks are 210 bytes, so a block can start 2 mod 4 bytes into shared
 // memory; its words then come from aligned loads and funnel shifts.  Problem
 // kind 1 is the fused gate/up + SwiGLU: a stage holds the gate tile and the up
@@ -1118,6 +1119,15 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
   asm volatile("mov.b32 %0, %1;" : "=r"(fmagic) : "n"(kFMagic));
   const uint32_t ring_s = base + P.ring_off + (uint32_t)L.g * pitch;
 
+  // A tile's blocks j = cls mod kDW are this warp's, and its partials go to slot
+  // cls, whose order the sums follow.  The classes move on by nb from tile to
+  // tile, so that a warp with a block less in one tile has one more in another,
+  // in the stages ahead.  131072 x 3072 Q4_K (12 blocks for 8 warps): fp16 x
+  // 48.8 -> 47.0 us, int8 x 54.7 -> 48.0.
+  int cls = warp;
+  const int nb_mod = nb % kDW;
+  auto next_class = [&](int c) { return c < nb_mod ? c - nb_mod + kDW : c - nb_mod; };
+
   if constexpr (Q8X) {
     // lane (r, s): row r of the 16, weights 128s .. 128s+127 of every block
     const int r = lane & 15, hs = lane >> 4;
@@ -1128,7 +1138,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
       const int j0 = chunk * cb;
-      int b = warp - j0 % kDW;
+      int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_r + (uint32_t)s * SB;
       for (; ok && b < cb; b += kDW) {
@@ -1146,11 +1156,12 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
       if (chunk == nchunks - 1) {
         const float p0 = a0 + __shfl_xor_sync(0xffffffffu, a0, 16), p1 = a1 + __shfl_xor_sync(0xffffffffu, a1, 16);
         if (lane < 16) {
-          float* q = red + ((size_t)s * kDW + warp) * redw;
+          float* q = red + ((size_t)s * kDW + cls) * redw;
           q[r] = p0;
           if (ncomb == 2) q[16 + r] = p1;
         }
         a0 = a1 = 0.f;
+        cls = next_class(cls);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[s]);
@@ -1173,9 +1184,9 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
     for (int st = 0; st < steps; ++st) {
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
-      // this warp's blocks of the chunk: j = chunk * cb + b with j mod kDW = warp
+      // this warp's blocks of the chunk: j = chunk * cb + b with j mod kDW = cls
       const int j0 = chunk * cb;
-      int b = warp - j0 % kDW;
+      int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_s + (uint32_t)s * SB;
       for (; ok && b < cb; b += kDW) {
@@ -1195,7 +1206,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
         // tile(s) done: this warp's row sums to the stage's partials slot
         const float p0 = quad_sum(a0), p1 = quad_sum(a1), p2 = quad_sum(a2), p3 = quad_sum(a3);
         if (L.tig == 0) {
-          float* q = red + ((size_t)s * kDW + warp) * redw;
+          float* q = red + ((size_t)s * kDW + cls) * redw;
           q[L.g] = p0;
           q[L.g + 8] = p1;
           if (ncomb == 2) {
@@ -1204,6 +1215,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
           }
         }
         a0 = a1 = a2 = a3 = 0.f;
+        cls = next_class(cls);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[s]);
@@ -1230,7 +1242,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
       const int j0 = chunk * cb;
-      int b = warp - j0 % kDW;
+      int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_s + (uint32_t)s * SB;
       for (; ok && b < cb; b += kDW) {
@@ -1250,7 +1262,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
         }
       }
       if (chunk == nchunks - 1) {
-        float* q = red + ((size_t)s * kDW + warp) * redw;
+        float* q = red + ((size_t)s * kDW + cls) * redw;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1260,6 +1272,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
             if (ncomb == 2) q[16 * MT + row * MT + tok] = yb[nt][i];
             ya[nt][i] = yb[nt][i] = 0.f;
           }
+        cls = next_class(cls);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[s]);
