@@ -47,6 +47,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
@@ -745,7 +746,9 @@ struct DecodeCtl {
 // away from zero, clamped to +-127; d = 0 gives q = 0), and the products run
 // as integer dot products (dp4a: four int8 x times four quant bytes, int32
 // sum).  Per sub-block (Q4_K) or scale group (Q6_K) the integer sum is scaled
-// once in fp32.  x table: the int8 x in k order (K bytes), then per 32-block
+// once in fp32.  x table: the int8 x in k order (K bytes; for Q4_K with the
+// 32-blocks of every second 128 values swapped in pairs, so that the lanes of
+// both halves of a block read different banks), then per 32-block
 // {d, sum of q over its first 16 k, over its last 16, 0} (16 bytes).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {
@@ -754,6 +757,12 @@ __device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {
   return d;
 }
 
+template <int QT>
+__device__ __forceinline__ int x_pos_q8(int b) {
+  return QT == kQ4K ? b ^ ((b >> 2) & 1) : b;
+}
+
+template <int QT>
 __device__ void build_x_table_q8(uint32_t xs, int K, uint32_t xq, uint32_t dt, int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   for (int b = warp; b < K / 32; b += kDW) {
@@ -766,7 +775,7 @@ __device__ void build_x_table_q8(uint32_t xs, int K, uint32_t xq, uint32_t dt, i
     const float d = __fdiv_rn(a, 127.0f);
     int q = 0;
     if (d != 0.0f) q = (int)fminf(fmaxf(roundf(__fdiv_rn(v, d)), -127.0f), 127.0f);
-    asm volatile("st.shared.s8 [%0], %1;" ::"r"(xq + (uint32_t)(32 * b + lane)), "r"(q) : "memory");
+    asm volatile("st.shared.s8 [%0], %1;" ::"r"(xq + (uint32_t)(32 * x_pos_q8<QT>(b) + lane)), "r"(q) : "memory");
     int s = q;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);  // within each half of the warp
@@ -781,54 +790,107 @@ __device__ void build_x_table_q8(uint32_t xs, int K, uint32_t xq, uint32_t dt, i
 }
 
 // The table's scales and sums for x that came in int8 (its values are in place
-// at xq, its K / 32 scales at xd): one thread per block of 32, two 16-byte
-// loads, the sums as dot products with ones.
+// at xq in k order, its K / 32 scales at xd): one thread per two blocks of 32,
+// the sums as dot products with ones.
+template <int QT>
 __device__ void build_x_sums_q8(uint32_t xd, int K, uint32_t xq, uint32_t dt, int tid) {
-  for (int b = tid; b < K / 32; b += kDCompute) {
-    const uint4 u = lds128(xq + 32u * (uint32_t)b), w = lds128(xq + 32u * (uint32_t)b + 16u);
-    uint32_t d;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(d) : "r"(xd + 4u * (uint32_t)b));
+  for (int b = 2 * tid; b < K / 32; b += 2 * kDCompute) {
+    const uint32_t a = xq + 32u * (uint32_t)b;
+    const uint4 v[4] = {lds128(a), lds128(a + 16u), lds128(a + 32u), lds128(a + 48u)};
+    uint32_t d[2];
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(d[0]), "=r"(d[1]) : "r"(xd + 4u * (uint32_t)b));
     constexpr uint32_t kOnes = 0x01010101u;
-    const int s0 = dp4a_us(kOnes, u.x, dp4a_us(kOnes, u.y, dp4a_us(kOnes, u.z, dp4a_us(kOnes, u.w, 0))));
-    const int s1 = dp4a_us(kOnes, w.x, dp4a_us(kOnes, w.y, dp4a_us(kOnes, w.z, dp4a_us(kOnes, w.w, 0))));
-    sts128_u(dt + 16u * (uint32_t)b, d, __float_as_uint((float)s0), __float_as_uint((float)s1), 0u);
+    float sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum[i] = (float)dp4a_us(kOnes, v[i].x, dp4a_us(kOnes, v[i].y, dp4a_us(kOnes, v[i].z, dp4a_us(kOnes, v[i].w, 0))));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      sts128_u(dt + 16u * (uint32_t)(b + i), d[i], __float_as_uint(sum[2 * i]), __float_as_uint(sum[2 * i + 1]), 0u);
+    if (x_pos_q8<QT>(b) != b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sts128_u(a + 16u * (uint32_t)(i ^ 2), v[i].x, v[i].y, v[i].z, v[i].w);
+    }
   }
 }
 
-// One Q4_K block of row r (address rb), lane half s (sub-blocks 4s .. 4s+3):
+// The lanes of a warp in a block: 16 rows, two halves of 128 weights.  Q6_K: 8
+// rows of one half read together.  Q4_K: 4 rows of both halves, and where rows
+// are an even number of 16 bytes apart a lane takes the 16-byte pieces of its
+// 64 in the order i ^ mask, so that 8 lanes always read 8 different groups of
+// four banks.  (4096 x 8192, int8 x: 20.0 us without the order.)
+template <int QT>
+struct Q8Lane {
+  int r, half, mask;
+  uint32_t x_off[4];  // Q4_K: where x of the low nibbles of piece i ^ mask is (the high nibbles' at ^ 32)
+  __device__ __forceinline__ Q8Lane(int lane, uint32_t pitch) {
+    if (QT == kQ4K) {
+      r = (lane & 3) | ((lane >> 3) << 2);
+      half = (lane >> 2) & 1;
+      mask = pitch % 32 == 0 ? r & 3 : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x_off[i] = (uint32_t)(128 * half + ((64 * ((i ^ mask) >> 1) + 16 * ((i ^ mask) & 1)) ^ (32 * half)));
+    } else {
+      r = lane & 15;
+      half = lane >> 4;
+      mask = 0;
+    }
+  }
+  // The sum over both halves of a row.
+  __device__ __forceinline__ float both(float a) const {
+    return a + __shfl_xor_sync(0xffffffffu, a, QT == kQ4K ? 4 : 16);
+  }
+};
+
+// x of one lane's half of a block (128 values, their four scales and sums), for
+// every row set that the lane takes the block of.  Q4_K: in the order of its
+// pieces, the low nibbles' four words and the high nibbles'.
+struct XHalf {
+  uint32_t X[32];
+  float4 D[4];
+  template <int QT>
+  __device__ __forceinline__ XHalf(uint32_t xa, uint32_t da, const Q8Lane<QT>& L) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = lds128(QT == kQ4K ? xa + (L.x_off[i >> 1] ^ (32u * (uint32_t)(i & 1)))
+                                        : xa + 128u * (uint32_t)L.half + 16u * (uint32_t)i);
+      X[4 * i] = v.x;
+      X[4 * i + 1] = v.y;
+      X[4 * i + 2] = v.z;
+      X[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) D[i] = ldsf4(da + 64u * (uint32_t)L.half + 16u * (uint32_t)i);
+  }
+};
+
+// One Q4_K block of the lane's row (address rb), half s (sub-blocks 4s .. 4s+3):
 // y += sum over those sub-blocks of d_x * (d*sc*IDOT - dmin*m*ISUM).
-__device__ __forceinline__ void q4_block_q8(uint32_t rb, uint32_t xa, uint32_t da, int s, float& y) {
+__device__ __forceinline__ void q4_block_q8(uint32_t rb, const XHalf& x, const Q8Lane<kQ4K>& L, float& y) {
   const uint4 h = lds128(rb);
   uint4 w4[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w4[i] = lds128(rb + 16u + 64u * (uint32_t)s + 16u * (uint32_t)i);
-  uint4 x4[8];
+  for (int i = 0; i < 4; ++i) w4[i] = lds128(rb + 16u + 64u * (uint32_t)L.half + 16u * (uint32_t)(i ^ L.mask));
+  int a[4] = {0, 0, 0, 0};  // pieces 0, 1: low and high nibbles; pieces 2, 3
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x4[i] = lds128(xa + 16u * (uint32_t)i);
-  float4 D[4];
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) D[i] = ldsf4(da + 16u * (uint32_t)i);
-  const uint32_t w[16] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w, w4[1].x, w4[1].y, w4[1].z, w4[1].w,
-                          w4[2].x, w4[2].y, w4[2].z, w4[2].w, w4[3].x, w4[3].y, w4[3].z, w4[3].w};
-  const uint32_t X[32] = {x4[0].x, x4[0].y, x4[0].z, x4[0].w, x4[1].x, x4[1].y, x4[1].z, x4[1].w,
-                          x4[2].x, x4[2].y, x4[2].z, x4[2].w, x4[3].x, x4[3].y, x4[3].z, x4[3].w,
-                          x4[4].x, x4[4].y, x4[4].z, x4[4].w, x4[5].x, x4[5].y, x4[5].z, x4[5].w,
-                          x4[6].x, x4[6].y, x4[6].z, x4[6].w, x4[7].x, x4[7].y, x4[7].z, x4[7].w};
-  int acc[4] = {0, 0, 0, 0};  // sub-blocks 4s + t
-#pragma unroll
-  for (int v = 0; v < 8; ++v) {
-    const uint32_t a = w[v], b = w[8 + v];  // groups 2s and 2s+1, bytes 4v .. 4v+3
-    acc[0] = dp4a_us(a & 0x0F0F0F0Fu, X[v], acc[0]);
-    acc[1] = dp4a_us((a >> 4) & 0x0F0F0F0Fu, X[8 + v], acc[1]);
-    acc[2] = dp4a_us(b & 0x0F0F0F0Fu, X[16 + v], acc[2]);
-    acc[3] = dp4a_us((b >> 4) & 0x0F0F0F0Fu, X[24 + v], acc[3]);
+    for (int v = 0; v < 4; ++v) {
+      a[2 * (i >> 1)] = dp4a_us(w[v] & 0x0F0F0F0Fu, x.X[8 * i + v], a[2 * (i >> 1)]);
+      a[2 * (i >> 1) + 1] = dp4a_us((w[v] >> 4) & 0x0F0F0F0Fu, x.X[8 * i + 4 + v], a[2 * (i >> 1) + 1]);
+    }
   }
+  // sub-blocks 4s + t: the first two are the lane's first or last two pieces
+  const bool swapped = L.mask & 2;
+  const int acc[4] = {swapped ? a[2] : a[0], swapped ? a[3] : a[1], swapped ? a[0] : a[2], swapped ? a[1] : a[3]};
   const float d = half_lo(h.x), dmin = half_lo(h.x >> 16);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     // sub-block j = 4s + t: bytes s[0..3] = h.y, s[4..7] = h.z, s[8..11] = h.w
     uint32_t sc, m;
-    if (s == 0) {
+    if (L.half == 0) {
       sc = (h.y >> (8 * t)) & 63u;
       m = (h.z >> (8 * t)) & 63u;
     } else {
@@ -836,7 +898,7 @@ __device__ __forceinline__ void q4_block_q8(uint32_t rb, uint32_t xa, uint32_t d
       m = ((h.w >> (8 * t + 4)) & 15u) | (((h.z >> (8 * t + 6)) & 3u) << 4);
     }
     const float dsc = d * (float)sc, dmn = dmin * (float)m;
-    y = fmaf(D[t].x, fmaf(dsc, (float)acc[t], -dmn * (D[t].y + D[t].z)), y);
+    y = fmaf(x.D[t].x, fmaf(dsc, (float)acc[t], -dmn * (x.D[t].y + x.D[t].z)), y);
   }
 }
 
@@ -852,31 +914,78 @@ __device__ __forceinline__ void lds_pair(uint32_t a, bool a2, uint32_t& w0, uint
   }
 }
 
+// Word i of the bytes that start kOff past words w[0].
+template <int kOff>
+__device__ __forceinline__ uint32_t word_at(const uint32_t* w, int i) {
+  return kOff & 2 ? __funnelshift_r(w[i + kOff / 4], w[i + kOff / 4 + 1], 16) : w[i + kOff / 4];
+}
+
+// The words of a Q6_K block half (address rb, half h) from 16-byte loads.  Rows
+// are 16-byte aligned here, so a block's offset from such a boundary (2 b mod
+// 16) is the same for the whole warp, and the shift to it a uniform branch.
+// Ten loads of 4 wavefronts each where rows are an odd number of 16 bytes
+// apart; word by word they are up to 42 loads of 4 or more.
+__device__ __forceinline__ void q6_words_wide(uint32_t rb, int h, uint32_t (&A)[8], uint32_t (&B)[8], uint32_t (&H)[8],
+                                              uint32_t (&S)[2], uint32_t& dw) {
+  const uint32_t off = rb & 15u, a = rb - off;
+  uint32_t L[20], Q[12], T[8];  // low nibbles (64 bytes), high bits (32), scales and d (18)
+  auto load = [](uint32_t* w, uint32_t at) {
+    const uint4 v = lds128(at);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  };
+#pragma unroll
+  for (int i = 0; i < 5; ++i) load(L + 4 * i, a + 64u * (uint32_t)h + 16u * (uint32_t)i);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) load(Q + 4 * i, a + 128u + 32u * (uint32_t)h + 16u * (uint32_t)i);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load(T + 4 * i, a + 192u + 16u * (uint32_t)i);
+  auto shift = [&](auto k) {
+    constexpr int kOff = decltype(k)::value;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      A[v] = word_at<kOff>(L, v);
+      B[v] = word_at<kOff>(L, 8 + v);
+      H[v] = word_at<kOff>(Q, v);
+    }
+    S[0] = h ? word_at<kOff>(T, 2) : word_at<kOff>(T, 0);
+    S[1] = h ? word_at<kOff>(T, 3) : word_at<kOff>(T, 1);
+    dw = T[4 + kOff / 4] >> (kOff & 2 ? 16 : 0);
+  };
+  switch (off) {
+    case 0: shift(std::integral_constant<int, 0>{}); break;
+    case 2: shift(std::integral_constant<int, 2>{}); break;
+    case 4: shift(std::integral_constant<int, 4>{}); break;
+    case 6: shift(std::integral_constant<int, 6>{}); break;
+    case 8: shift(std::integral_constant<int, 8>{}); break;
+    case 10: shift(std::integral_constant<int, 10>{}); break;
+    case 12: shift(std::integral_constant<int, 12>{}); break;
+    default: shift(std::integral_constant<int, 14>{}); break;
+  }
+}
+
 // One Q6_K block of row r (address rb), lane half h (weights 128h .. 128h+127,
 // scale groups 8h .. 8h+7): y += sum over the 8 groups of
 // d_x * d * sc * (IDOT(q6 + 32) - 32 * ISUM).
-__device__ __forceinline__ void q6_block_q8(uint32_t rb, uint32_t xa, uint32_t da, int h, float& y) {
-  const bool a2 = (rb & 3u) != 0;
-  uint32_t A[8], B[8], H[8];
+template <bool kWide>
+__device__ __forceinline__ void q6_block_q8(uint32_t rb, const XHalf& x, int h, float& y) {
+  uint32_t A[8], B[8], H[8], S[2], dw;  // dw: d is its low half
+  if constexpr (kWide) {
+    q6_words_wide(rb, h, A, B, H, S, dw);
+  } else {
+    const bool a2 = (rb & 3u) != 0;
 #pragma unroll
-  for (int v = 0; v < 8; v += 2) {
-    lds_pair(rb + 64u * (uint32_t)h + 4u * (uint32_t)v, a2, A[v], A[v + 1]);
-    lds_pair(rb + 64u * (uint32_t)h + 32u + 4u * (uint32_t)v, a2, B[v], B[v + 1]);
-    lds_pair(rb + 128u + 32u * (uint32_t)h + 4u * (uint32_t)v, a2, H[v], H[v + 1]);
+    for (int v = 0; v < 8; v += 2) {
+      lds_pair(rb + 64u * (uint32_t)h + 4u * (uint32_t)v, a2, A[v], A[v + 1]);
+      lds_pair(rb + 64u * (uint32_t)h + 32u + 4u * (uint32_t)v, a2, B[v], B[v + 1]);
+      lds_pair(rb + 128u + 32u * (uint32_t)h + 4u * (uint32_t)v, a2, H[v], H[v + 1]);
+    }
+    uint32_t before;
+    lds_pair(rb + 192u + 8u * (uint32_t)h, a2, S[0], S[1]);
+    lds_pair(rb + 204u, a2, before, dw);  // bytes 204..211: d is bytes 208..209
   }
-  uint32_t S[2], dw0, dw1;
-  lds_pair(rb + 192u + 8u * (uint32_t)h, a2, S[0], S[1]);
-  lds_pair(rb + 204u, a2, dw0, dw1);  // bytes 204..211: d is bytes 208..209
-  uint4 x4[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x4[i] = lds128(xa + 16u * (uint32_t)i);
-  float4 D[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) D[i] = ldsf4(da + 16u * (uint32_t)i);
-  const uint32_t X[32] = {x4[0].x, x4[0].y, x4[0].z, x4[0].w, x4[1].x, x4[1].y, x4[1].z, x4[1].w,
-                          x4[2].x, x4[2].y, x4[2].z, x4[2].w, x4[3].x, x4[3].y, x4[3].z, x4[3].w,
-                          x4[4].x, x4[4].y, x4[4].z, x4[4].w, x4[5].x, x4[5].y, x4[5].z, x4[5].w,
-                          x4[6].x, x4[6].y, x4[6].z, x4[6].w, x4[7].x, x4[7].y, x4[7].z, x4[7].w};
   int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // [field g6][half of l]
 #pragma unroll
   for (int v = 0; v < 8; ++v) {
@@ -887,20 +996,20 @@ __device__ __forceinline__ void q6_block_q8(uint32_t rb, uint32_t xa, uint32_t d
     const uint32_t q1 = (b & 0x0F0F0F0Fu) | ((q << 2) & 0x30303030u);
     const uint32_t q2 = ((a >> 4) & 0x0F0F0F0Fu) | (q & 0x30303030u);
     const uint32_t q3 = ((b >> 4) & 0x0F0F0F0Fu) | ((q >> 2) & 0x30303030u);
-    acc[0 + hl] = dp4a_us(q0, X[v], acc[0 + hl]);
-    acc[2 + hl] = dp4a_us(q1, X[8 + v], acc[2 + hl]);
-    acc[4 + hl] = dp4a_us(q2, X[16 + v], acc[4 + hl]);
-    acc[6 + hl] = dp4a_us(q3, X[24 + v], acc[6 + hl]);
+    acc[0 + hl] = dp4a_us(q0, x.X[v], acc[0 + hl]);
+    acc[2 + hl] = dp4a_us(q1, x.X[8 + v], acc[2 + hl]);
+    acc[4 + hl] = dp4a_us(q2, x.X[16 + v], acc[4 + hl]);
+    acc[6 + hl] = dp4a_us(q3, x.X[24 + v], acc[6 + hl]);
   }
-  const float d = half_lo(dw1);  // bytes 208..209 are the low half of the second word
+  const float d = half_lo(dw);
 #pragma unroll
   for (int g6 = 0; g6 < 4; ++g6) {
 #pragma unroll
     for (int hl = 0; hl < 2; ++hl) {
       const int gi = 2 * g6 + hl;  // scale group 8h + gi
       const int sc = (int)(int8_t)((S[gi >> 2] >> (8 * (gi & 3))) & 0xFFu);
-      const float isum = hl ? D[g6].z : D[g6].y;
-      y = fmaf(D[g6].x * (d * (float)sc), fmaf(-32.0f, isum, (float)acc[2 * g6 + hl]), y);
+      const float isum = hl ? x.D[g6].z : x.D[g6].y;
+      y = fmaf(x.D[g6].x * (d * (float)sc), fmaf(-32.0f, isum, (float)acc[2 * g6 + hl]), y);
     }
   }
 }
@@ -1098,9 +1207,9 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
   }
   if constexpr (Q8X) {
     if (P.xd)
-      build_x_sums_q8(xs, K, base, base + (uint32_t)K, tid);
+      build_x_sums_q8<QT>(xs, K, base, base + (uint32_t)K, tid);
     else
-      build_x_table_q8(xs, K, base, base + (uint32_t)K, tid);
+      build_x_table_q8<QT>(xs, K, base, base + (uint32_t)K, tid);
   } else if constexpr (MT == 1)
     build_x_table<QT>(xs, gs, ctl->rnorm, K, base, sxt, zero, tid);
   else
@@ -1125,14 +1234,13 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
   // in the stages ahead.  131072 x 3072 Q4_K (12 blocks for 8 warps): fp16 x
   // 48.8 -> 47.0 us, int8 x 54.7 -> 48.0.
   int cls = warp;
-  const int nb_mod = nb % kDW;
-  auto next_class = [&](int c) { return c < nb_mod ? c - nb_mod + kDW : c - nb_mod; };
+  const unsigned class_step = (unsigned)(kDW - nb % kDW);
+  auto next_class = [&](int c) { return (int)(((unsigned)c + class_step) % kDW); };
 
   if constexpr (Q8X) {
-    // lane (r, s): row r of the 16, weights 128s .. 128s+127 of every block
-    const int r = lane & 15, hs = lane >> 4;
-    const uint32_t ring_r = base + P.ring_off + (uint32_t)r * pitch;
-    const uint32_t xq = base + 128u * (uint32_t)hs, dq = base + (uint32_t)K + 64u * (uint32_t)hs;
+    const Q8Lane<QT> Q(lane, pitch);
+    const uint32_t ring_r = base + P.ring_off + (uint32_t)Q.r * pitch;
+    const uint32_t xq = base, dq = base + (uint32_t)K;
     float a0 = 0.f, a1 = 0.f;  // row r of row set 0, of row set 1 (this half)
     for (int st = 0; st < steps; ++st) {
       const int s = st % S, chunk = st % nchunks;
@@ -1145,20 +1253,24 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
         const int j = j0 + b;
         const uint32_t rb = stg + (uint32_t)(b * kBB);
         const uint32_t xa = xq + 256u * (uint32_t)j, da = dq + 128u * (uint32_t)j;
+        const XHalf x(xa, da, Q);
         if constexpr (QT == kQ4K) {
-          q4_block_q8(rb, xa, da, hs, a0);
-          if (ncomb == 2) q4_block_q8(rb + comb_bytes, xa, da, hs, a1);
+          q4_block_q8(rb, x, Q, a0);
+          if (ncomb == 2) q4_block_q8(rb + comb_bytes, x, Q, a1);
+        } else if (pitch % 16 == 0) {
+          q6_block_q8<true>(rb, x, Q.half, a0);
+          if (ncomb == 2) q6_block_q8<true>(rb + comb_bytes, x, Q.half, a1);
         } else {
-          q6_block_q8(rb, xa, da, hs, a0);
-          if (ncomb == 2) q6_block_q8(rb + comb_bytes, xa, da, hs, a1);
+          q6_block_q8<false>(rb, x, Q.half, a0);
+          if (ncomb == 2) q6_block_q8<false>(rb + comb_bytes, x, Q.half, a1);
         }
       }
       if (chunk == nchunks - 1) {
-        const float p0 = a0 + __shfl_xor_sync(0xffffffffu, a0, 16), p1 = a1 + __shfl_xor_sync(0xffffffffu, a1, 16);
-        if (lane < 16) {
+        const float p0 = Q.both(a0), p1 = Q.both(a1);
+        if (Q.half == 0) {
           float* q = red + ((size_t)s * kDW + cls) * redw;
-          q[r] = p0;
-          if (ncomb == 2) q[16 + r] = p1;
+          q[Q.r] = p0;
+          if (ncomb == 2) q[16 + Q.r] = p1;
         }
         a0 = a1 = 0.f;
         cls = next_class(cls);
