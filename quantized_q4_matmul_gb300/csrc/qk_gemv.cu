@@ -712,12 +712,12 @@ __device__ void build_x_table_tn(uint32_t gs, const float* rnorm, int M, int K, 
 // 16-row tiles (two adjacent tiles of one tensor, or the gate and the up tile,
 // per stage), or of 16-row x cb-block chunks with one copy per row: a few
 // large copies per stage keep the copy engine and DRAM efficient.  A unit is
-// 16 rows x one 256-weight block of one tensor; compute warp w takes the
-// units of block j = w, w + kDW, ... of every tile, so each warp's share of a
-// tile is fixed by j alone.  A warp adds its units in j order, leaves its row
-// (x token) sums of a finished tile in the stage's partials slot, and
-// releases the stage.  Before refilling a stage the producer adds the kDW warps' sums of
-// the tile(s) it held, in warp order, and writes y (fp32, or fp16
+// 16 rows x one 256-weight block of one tensor; a compute warp takes the
+// units of block j = c, c + kDW, ... of a tile, a class c that moves on from
+// tile to tile.  A warp adds its units in j order, leaves its row (x token) sums
+// of a finished tile in slot c of the stage's partials, and releases the stage.
+// Before refilling a stage the producer adds the kDW classes' sums of the
+// tile(s) it held, in their order, and writes y (fp32, or fp16
 // silu(gate) * up).  No atomic and no barrier among compute warps: each only
 // waits for its stage to land.  The order of every addition depends on the
 // problem's shape only, so a problem launched alone or grouped gives the same
@@ -818,7 +818,8 @@ __device__ void build_x_sums_q8(uint32_t xd, int K, uint32_t xq, uint32_t dt, in
 // rows of one half read together.  Q4_K: 4 rows of both halves, and where rows
 // are an even number of 16 bytes apart a lane takes the 16-byte pieces of its
 // 64 in the order i ^ mask, so that 8 lanes always read 8 different groups of
-// four banks.  (4096 x 8192, int8 x: 20.0 us without the order.)
+// four banks.  (65536 x 4096, int8 x: 39.7 us; with 8 rows of one half together
+// in one order 58.3.)
 template <int QT>
 struct Q8Lane {
   int r, half, mask;
@@ -902,90 +903,79 @@ __device__ __forceinline__ void q4_block_q8(uint32_t rb, const XHalf& x, const Q
   }
 }
 
-// Two consecutive words at shared address a (4-byte aligned, or 2 mod 4).
-__device__ __forceinline__ void lds_pair(uint32_t a, bool a2, uint32_t& w0, uint32_t& w1) {
-  if (!a2) {
-    w0 = lds32(a);
-    w1 = lds32(a + 4);
-  } else {
-    const uint32_t t0 = lds32(a - 2), t1 = lds32(a + 2), t2 = lds32(a + 6);
-    w0 = __funnelshift_r(t0, t1, 16);
-    w1 = __funnelshift_r(t1, t2, 16);
+// n words from shared address a, kBytes at a time.
+template <int kBytes>
+__device__ __forceinline__ void lds_words(uint32_t* w, uint32_t a, int n) {
+#pragma unroll
+  for (int i = 0; i < n; i += kBytes / 4) {
+    if constexpr (kBytes == 16) {
+      const uint4 v = lds128(a + 4u * (uint32_t)i);
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    } else {
+      w[i] = lds32(a + 4u * (uint32_t)i);
+    }
   }
 }
 
-// Word i of the bytes that start kOff past words w[0].
-template <int kOff>
-__device__ __forceinline__ uint32_t word_at(const uint32_t* w, int i) {
-  return kOff & 2 ? __funnelshift_r(w[i + kOff / 4], w[i + kOff / 4 + 1], 16) : w[i + kOff / 4];
-}
-
-// The words of a Q6_K block half (address rb, half h) from 16-byte loads.  Rows
-// are 16-byte aligned here, so a block's offset from such a boundary (2 b mod
-// 16) is the same for the whole warp, and the shift to it a uniform branch.
-// Ten loads of 4 wavefronts each where rows are an odd number of 16 bytes
-// apart; word by word they are up to 42 loads of 4 or more.
-__device__ __forceinline__ void q6_words_wide(uint32_t rb, int h, uint32_t (&A)[8], uint32_t (&B)[8], uint32_t (&H)[8],
-                                              uint32_t (&S)[2], uint32_t& dw) {
-  const uint32_t off = rb & 15u, a = rb - off;
-  uint32_t L[20], Q[12], T[8];  // low nibbles (64 bytes), high bits (32), scales and d (18)
-  auto load = [](uint32_t* w, uint32_t at) {
-    const uint4 v = lds128(at);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  };
-#pragma unroll
-  for (int i = 0; i < 5; ++i) load(L + 4 * i, a + 64u * (uint32_t)h + 16u * (uint32_t)i);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) load(Q + 4 * i, a + 128u + 32u * (uint32_t)h + 16u * (uint32_t)i);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load(T + 4 * i, a + 192u + 16u * (uint32_t)i);
-  auto shift = [&](auto k) {
-    constexpr int kOff = decltype(k)::value;
+// The words of a Q6_K block half (address rb, half h; dw: d is its low half)
+// from loads of kBytes and a shift to the block's offset from such a boundary.
+// kBytes = 16 where rows are aligned to it: the offset (2 b mod 16 for block b)
+// is then the same for the whole warp, the shift to its word a uniform branch,
+// and rows an odd number of 16 bytes apart share no bank (10 loads of 4
+// wavefronts; word by word each of 32 would take 4 or more).  128256 x 4096,
+// int8 x: 84 us, with words 142.  Rows that are not: kBytes = 4 (loads of 8 where
+// rows allow those were slower).
+template <int kBytes>
+__device__ __forceinline__ void q6_words(uint32_t rb, int h, uint32_t (&A)[8], uint32_t (&B)[8], uint32_t (&H)[8],
+                                         uint32_t (&S)[2], uint32_t& dw) {
+  constexpr int kPast = kBytes / 4;  // words read past a run for the shift
+  const uint32_t off = rb & (uint32_t)(kBytes - 1), a = rb - off;
+  uint32_t L[16 + kPast], Q[8 + kPast], T[8];  // low nibbles (64 bytes), high bits (32), scales and d (18)
+  lds_words<kBytes>(L, a + 64u * (uint32_t)h, 16 + kPast);
+  lds_words<kBytes>(Q, a + 128u + 32u * (uint32_t)h, 8 + kPast);
+  lds_words<kBytes>(T, a + 192u, kBytes == 16 ? 8 : 5);
+  // words from word f on, shifted down by bits
+  auto shift = [&](auto from, uint32_t bits) {
+    constexpr int f = decltype(from)::value;
+    auto at = [&](const uint32_t* w, int i) {
+      return kBytes == 16 && bits == 0 ? w[i + f] : __funnelshift_r(w[i + f], w[i + f + 1], bits);
+    };
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      A[v] = word_at<kOff>(L, v);
-      B[v] = word_at<kOff>(L, 8 + v);
-      H[v] = word_at<kOff>(Q, v);
+      A[v] = at(L, v);
+      B[v] = at(L, 8 + v);
+      H[v] = at(Q, v);
     }
-    S[0] = h ? word_at<kOff>(T, 2) : word_at<kOff>(T, 0);
-    S[1] = h ? word_at<kOff>(T, 3) : word_at<kOff>(T, 1);
-    dw = T[4 + kOff / 4] >> (kOff & 2 ? 16 : 0);
+    S[0] = h ? at(T, 2) : at(T, 0);
+    S[1] = h ? at(T, 3) : at(T, 1);
+    dw = T[4 + f] >> bits;
   };
-  switch (off) {
-    case 0: shift(std::integral_constant<int, 0>{}); break;
-    case 2: shift(std::integral_constant<int, 2>{}); break;
-    case 4: shift(std::integral_constant<int, 4>{}); break;
-    case 6: shift(std::integral_constant<int, 6>{}); break;
-    case 8: shift(std::integral_constant<int, 8>{}); break;
-    case 10: shift(std::integral_constant<int, 10>{}); break;
-    case 12: shift(std::integral_constant<int, 12>{}); break;
-    default: shift(std::integral_constant<int, 14>{}); break;
+  if constexpr (kBytes == 4) {
+    shift(std::integral_constant<int, 0>{}, 8u * off);
+  } else {
+    switch (off) {
+      case 0: shift(std::integral_constant<int, 0>{}, 0u); break;
+      case 2: shift(std::integral_constant<int, 0>{}, 16u); break;
+      case 4: shift(std::integral_constant<int, 1>{}, 0u); break;
+      case 6: shift(std::integral_constant<int, 1>{}, 16u); break;
+      case 8: shift(std::integral_constant<int, 2>{}, 0u); break;
+      case 10: shift(std::integral_constant<int, 2>{}, 16u); break;
+      case 12: shift(std::integral_constant<int, 3>{}, 0u); break;
+      default: shift(std::integral_constant<int, 3>{}, 16u); break;
+    }
   }
 }
 
 // One Q6_K block of row r (address rb), lane half h (weights 128h .. 128h+127,
 // scale groups 8h .. 8h+7): y += sum over the 8 groups of
 // d_x * d * sc * (IDOT(q6 + 32) - 32 * ISUM).
-template <bool kWide>
+template <int kBytes>
 __device__ __forceinline__ void q6_block_q8(uint32_t rb, const XHalf& x, int h, float& y) {
-  uint32_t A[8], B[8], H[8], S[2], dw;  // dw: d is its low half
-  if constexpr (kWide) {
-    q6_words_wide(rb, h, A, B, H, S, dw);
-  } else {
-    const bool a2 = (rb & 3u) != 0;
-#pragma unroll
-    for (int v = 0; v < 8; v += 2) {
-      lds_pair(rb + 64u * (uint32_t)h + 4u * (uint32_t)v, a2, A[v], A[v + 1]);
-      lds_pair(rb + 64u * (uint32_t)h + 32u + 4u * (uint32_t)v, a2, B[v], B[v + 1]);
-      lds_pair(rb + 128u + 32u * (uint32_t)h + 4u * (uint32_t)v, a2, H[v], H[v + 1]);
-    }
-    uint32_t before;
-    lds_pair(rb + 192u + 8u * (uint32_t)h, a2, S[0], S[1]);
-    lds_pair(rb + 204u, a2, before, dw);  // bytes 204..211: d is bytes 208..209
-  }
+  uint32_t A[8], B[8], H[8], S[2], dw;
+  q6_words<kBytes>(rb, h, A, B, H, S, dw);
   int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // [field g6][half of l]
 #pragma unroll
   for (int v = 0; v < 8; ++v) {
@@ -1231,8 +1221,8 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
   // A tile's blocks j = cls mod kDW are this warp's, and its partials go to slot
   // cls, whose order the sums follow.  The classes move on by nb from tile to
   // tile, so that a warp with a block less in one tile has one more in another,
-  // in the stages ahead.  131072 x 3072 Q4_K (12 blocks for 8 warps): fp16 x
-  // 48.8 -> 47.0 us, int8 x 54.7 -> 48.0.
+  // in the stages ahead.  65536 x 2304 Q4_K (9 blocks for 8 warps), fp16 x: 25.7
+  // -> 21.6 us; 65536 x 2560 Q6_K: 40.0 -> 34.6.
   int cls = warp;
   const unsigned class_step = (unsigned)(kDW - nb % kDW);
   auto next_class = [&](int c) { return (int)(((unsigned)c + class_step) % kDW); };
@@ -1257,12 +1247,15 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
         if constexpr (QT == kQ4K) {
           q4_block_q8(rb, x, Q, a0);
           if (ncomb == 2) q4_block_q8(rb + comb_bytes, x, Q, a1);
-        } else if (pitch % 16 == 0) {
-          q6_block_q8<true>(rb, x, Q.half, a0);
-          if (ncomb == 2) q6_block_q8<true>(rb + comb_bytes, x, Q.half, a1);
         } else {
-          q6_block_q8<false>(rb, x, Q.half, a0);
-          if (ncomb == 2) q6_block_q8<false>(rb + comb_bytes, x, Q.half, a1);
+          auto rows = [&](auto bytes) {
+            q6_block_q8<decltype(bytes)::value>(rb, x, Q.half, a0);
+            if (ncomb == 2) q6_block_q8<decltype(bytes)::value>(rb + comb_bytes, x, Q.half, a1);
+          };
+          if (pitch % 16 == 0)
+            rows(std::integral_constant<int, 16>{});
+          else
+            rows(std::integral_constant<int, 4>{});
         }
       }
       if (chunk == nchunks - 1) {
