@@ -1423,6 +1423,11 @@ constexpr size_t kGemvSmem = 227 * 1024;
 #define QK_Q6_COST 1.7
 #endif
 constexpr double kQ6CostPerByte = QK_Q6_COST;
+// With int8 x a Q6_K byte costs less than a Q4_K byte (fewer quants in it, the
+// same dot products): us of 30000 + 30000 rows of both at K = 4096 with 0.6, 0.7,
+// 0.8, 0.9, 1.0, 1.7: 42.2, 39.6, 37.4, 39.2, 41.8, 58.7; 2560 rows of each of
+// Q4_K, Q4_K, Q6_K at K = 2560: 5.1, 5.2, 5.2, 5.2, 5.4, 5.9.
+constexpr double kQ6CostPerByteQ8 = 0.8;
 
 // The token slots of the kernel that runs M tokens: 1 (decode layout) or 8.
 int slots_for(int64_t M) { return M <= 1 ? 1 : 8; }
@@ -1526,7 +1531,7 @@ bool plan_gemv(const GemvDesc* d, int count, int sms, GemvBatch* out, size_t* sm
     if (!plan_decode_problem(d[i], B.p[i], &s)) return false;
     smem = std::max(smem, s);
     const int bb = B.p[i].qtype == kQ4K ? kQ4KBytes : kQ6KBytes;
-    const double cost = B.p[i].qtype == kQ4K ? 1.0 : kQ6CostPerByte;
+    const double cost = B.p[i].qtype == kQ4K ? 1.0 : d[i].q8x ? kQ6CostPerByteQ8 : kQ6CostPerByte;
     tile_cost[i] = 16.0 * (B.p[i].K / kQK) * bb * (1 + B.p[i].kind) * cost;
     B.p[i].ctas = 1;
   }
