@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <algorithm>
+#include <new>
 #include <vector>
 
 #include "../../include/qk.h"
@@ -440,7 +441,7 @@ qk_status qk_matmul_q8x_q6k(const void* blocks, const uint16_t* x_f16, float* y,
 }
 
 // x already in int8, with its scales.
-qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc* descs, int count, qk_stream_t stream) {
+static qk_status matmul_batch_q8(const qk_matmul_q8_desc* descs, int count, cudaStream_t s) {
   if (count < 0) return QK_ERR_SHAPE;
   if (count == 0) return QK_OK;
   if (!descs) return QK_ERR_NULL;
@@ -470,7 +471,15 @@ qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc* descs, int count, qk_strea
     g.xd = p.x_d;
     group.push_back(g);
   }
-  return run_batch_q8(group, reinterpret_cast<cudaStream_t>(stream));
+  return run_batch_q8(group, s);
+}
+
+qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc* descs, int count, qk_stream_t stream) {
+  try {
+    return matmul_batch_q8(descs, count, reinterpret_cast<cudaStream_t>(stream));
+  } catch (const std::bad_alloc&) {  // host memory for the checks of so many problems
+    return QK_ERR_CUDA;
+  }
 }
 
 qk_status qk_matmul_q4k(const void* blocks, const uint16_t* x_f16, float* y, int64_t M, int64_t N, int64_t K,
