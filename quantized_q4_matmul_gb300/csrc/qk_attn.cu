@@ -16,7 +16,10 @@
 // A decode step of qk_gqa_attention_window (position j <= p is visible to
 // position p when j > p - window or j < sinks; out fp16) is the decode kernel
 // with kWin: it walks two runs of tiles, the sinks' and the window's, and never
-// loads another position.  Its prefill is in qk_attn_win.cu.
+// loads another position.  Its prefill is in qk_attn_win.cu.  8 key/value heads,
+// 4096 positions and 4 sinks of 20001: 6.8 us between calls of a graph (16.8 MB,
+// 2.5 us at the memory's rate; the rest is the launch, the first tiles' latency
+// and the join of the ranks).
 //
 // Decode (M = 1): a cluster of C CTAs per key/value head splits the visible
 // positions into C ranges.  The G query heads of the group are the rows of

@@ -11,7 +11,9 @@
 // (m, S, T) per thread, rescaled when a batch's maximum passes it.
 //
 // HBM-bound for many rows: the row is read once, 8 independent 16-byte loads
-// per thread and batch.  The alternatives cost almost nothing on the way: a
+// per thread and batch.  1024 rows of 128256: 80 us without alternatives (6.5
+// TB/s), 94 us with 20 (5.6 TB/s): while one of an SM's two CTAs finds them, the
+// other's loads alone do not fill the memory's latency.  The alternatives cost almost nothing on the way: a
 // thread notes the maximum of every batch of 32 logits (a segment) that it
 // needs for the rescaling anyway.  Afterwards t0, the n-th largest of the maxima
 // of 64 groups of threads, is a lower bound of the n-th largest logit, so the
@@ -24,7 +26,8 @@
 // the order in which candidates are found.
 //
 // Few rows: a cluster of up to 8 CTAs splits a row; each finds its own sums and
-// top n, and rank 0 joins them (distributed shared memory, in rank order).
+// top n, and rank 0 joins them (distributed shared memory, in rank order).  One
+// row of 128256: 5.5 us between calls of a graph, latency from end to end.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -416,7 +419,9 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s) {
   // A cluster per row while the rows alone leave SMs idle and a CTA's share
-  // stays a quarter of a batch at least.
+  // stays a quarter of a batch at least.  Rows of 128256, top 5, us with 1, 2, 4,
+  // 8 CTAs: 1 row 13.9, 9.9, 7.2, 5.8; 19 rows 14.1, 10.0, 9.0, 7.9; 38 rows 14.2,
+  // 10.1, 10.1, 12.7; 152 rows 15.3, 15.1, 24.4, 34.8.
   int C = 1;
   while (C < kLpMaxCluster && a.M * C * 2 <= device_sms() && a.V / (2 * C) >= kLpBatch) C *= 2;
   switch (C) {

@@ -14,9 +14,10 @@
 //
 // HBM-bound for a prompt: one CTA per token computes the token's n_rot / 2
 // sines and cosines once, in shared memory, while its first inputs are on their
-// way, and turns every head with them; each input is read once.  A decode step
-// has one token: its heads are spread over several CTAs, each with its own
-// table.
+// way, and turns every head with them; each input is read once (2048 tokens, 32
+// + 8 + 8 heads of 128, 96 dimensions turning: 14.3 us or 5.3 TB/s).  A decode
+// step has one token: its heads are spread over several CTAs, each with its own
+// table (1.8 us between calls of a graph, all latency).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -171,7 +172,9 @@ cudaError_t launch_rope_kv(const RopeArgs& a, cudaStream_t s) {
   const bool vec = a.n_rot % 8 == 0;
   const int items = (a.H + 2 * a.Hkv) * (a.D / (vec ? 8 : 4));
   // Few tokens: a CTA per 256 items, so that the heads' loads are all in flight.
-  const int split = a.M < 64 ? (items + kRopeThreads - 1) / kRopeThreads : 1;
+  // 24 + 8 + 8 heads of 128, us so and with a CTA per token: 1 token 1.9, 2.7; 100
+  // tokens 2.9, 3.0; 300 4.0, 4.4; 2048 14.4, 10.8.
+  const int split = a.M <= 2 * (int64_t)device_sms() ? (items + kRopeThreads - 1) / kRopeThreads : 1;
   const dim3 grid((unsigned)a.M, (unsigned)split);
   return launch_dependent(vec ? rope_kv_kernel : rope_kv_any_kernel, grid, kRopeThreads, 0, 1, s, a);
 }
