@@ -135,15 +135,16 @@ __device__ __forceinline__ float exchange(float v, int o, bool down, int lane) {
 // of the threads that have any of the `nv` vectors (20000 rows of 511 logits,
 // top 20: 1619 us with 8 always, whose 16 maxima exclude nothing).
 __device__ __forceinline__ float bound_of_threads(LpShared& S, float v, int n, int64_t nv, int warp, int lane) {
-  int per = 1;
-  while (per < kLpThreads / kLpGroups && per * kLpGroups < nv) per *= 2;
+  int lg = 3;  // a group is 2^lg threads
+  static_assert(kLpThreads == kLpGroups << 3, "groups of 8 take every thread");
+  while (lg > 0 && nv <= kLpGroups << (lg - 1)) --lg;
 #pragma unroll
   for (int o = 1; o < kLpThreads / kLpGroups; o <<= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    if (o < per) v = fmaxf(v, w);
+    if (o < 1 << lg) v = fmaxf(v, w);
   }
   const int t = 32 * warp + lane;
-  if (t % per == 0 && t / per < kLpGroups) S.top[t / per] = v;
+  if ((t & ((1 << lg) - 1)) == 0 && t >> lg < kLpGroups) S.top[t >> lg] = v;
   __syncthreads();
   float a = S.top[lane], b = S.top[lane + 32];
 #pragma unroll
