@@ -731,6 +731,14 @@ constexpr int kDMaxStages = 8;
 #endif
 constexpr uint32_t kDPiece = QK_DECODE_PIECE;  // bytes per bulk copy of a whole-row stage
 
+// Three stages of K chunks only where a row's share of a chunk is this many bytes
+// (it is one copy): two stages of larger copies stream faster than more of smaller
+// ones.  32768 rows, us with four stages of any size and so: Q6_K, K = 8192 (1680 ->
+// 3360 bytes) fp16 x 82.5, 54.1, int8 x 70.7, 44.4; K = 6144 (1680 -> whole rows)
+// 63.2, 42.7 and 54.1, 34.7; Q4_K, K = 8192 (2304 -> whole rows) 44.9, 36.0 and
+// 40.3, 33.5.
+constexpr int kDMinChunk = 3000;
+
 struct DecodeCtl {
   uint64_t full[kDMaxStages];   // stage landed (producer arrival + copy bytes)
   uint64_t empty[kDMaxStages];  // stage released by the kDW compute warps
@@ -1424,10 +1432,10 @@ constexpr size_t kGemvSmem = 227 * 1024;
 #endif
 constexpr double kQ6CostPerByte = QK_Q6_COST;
 // With int8 x a Q6_K byte costs less than a Q4_K byte (fewer quants in it, the
-// same dot products): us of 30000 + 30000 rows of both at K = 4096 with 0.6, 0.7,
-// 0.8, 0.9, 1.0, 1.7: 42.2, 39.6, 37.4, 39.2, 41.8, 58.7; 2560 rows of each of
-// Q4_K, Q4_K, Q6_K at K = 2560: 5.1, 5.2, 5.2, 5.2, 5.4, 5.9.
-constexpr double kQ6CostPerByteQ8 = 0.8;
+// same dot products).  us with 0.8, 0.85, 0.9, 1.7: 30000 rows of each at K = 4096
+// 37.4, 38.2, 39.3, 58.9; Q4_K, Q4_K and Q6_K, 2560 rows each, K = 2560, 5.2, 5.2,
+// 5.2, 5.9; a layer's seven linears with the first three 18.9, 16.4, 16.4.
+constexpr double kQ6CostPerByteQ8 = 0.85;
 
 // The token slots of the kernel that runs M tokens: 1 (decode layout) or 8.
 int slots_for(int64_t M) { return M <= 1 ? 1 : 8; }
@@ -1440,8 +1448,8 @@ int slots_for(int64_t M) { return M <= 1 ? 1 : 8; }
 // in place).  Stage geometry, first that fits: two adjacent whole tiles of
 // one tensor per stage (one token only) with at least 3 stages; whole tiles
 // (gate and up together) with 3; the largest 16-byte-aligned chunk of cb
-// blocks with 4, then 3; then the same with 2 stages (several tokens: with 2
-// stages from the start).
+// blocks with 3, of kDMinChunk bytes a row at least; then the same with 2
+// stages and chunks of any size (several tokens: with 2 stages from the start).
 bool plan_decode_problem(const GemvDesc& d, GemvProb& P, size_t* smem_out) {
   memset(&P, 0, sizeof(P));
   if (d.M < 1 || d.M > kMaxGemvM || d.N <= 0 || d.N >= ((int64_t)1 << 31) || d.K <= 0 || d.K % kQK != 0 ||
@@ -1493,13 +1501,11 @@ bool plan_decode_problem(const GemvDesc& d, GemvProb& P, size_t* smem_out) {
       cb = nb, S = stages_for((size_t)16 * RB * nten, false);
       break;
     }
-    for (int w2 : {want + (mt == 1 ? 1 : 0), want}) {
-      for (int c = nb - 1; c >= 1 && !cb; --c) {
-        if (nb % c != 0 || (c * bb) % 16 != 0 || RB % 16 != 0) continue;
-        if (stages_for((size_t)16 * c * bb * nten, false) >= w2)
-          cb = c, S = stages_for((size_t)16 * c * bb * nten, false);
-      }
-      if (cb) break;
+    for (int c = nb - 1; c >= 1 && !cb; --c) {
+      if (nb % c != 0 || (c * bb) % 16 != 0 || RB % 16 != 0) continue;
+      if (want > 2 && c * bb < kDMinChunk) continue;
+      if (stages_for((size_t)16 * c * bb * nten, false) >= want)
+        cb = c, S = stages_for((size_t)16 * c * bb * nten, false);
     }
     if (cb) break;
   }
