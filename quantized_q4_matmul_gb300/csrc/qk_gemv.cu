@@ -770,30 +770,41 @@ __device__ __forceinline__ int x_pos_q8(int b) {
   return QT == kQ4K ? b ^ ((b >> 2) & 1) : b;
 }
 
+// From fp16 x: a lane quantizes 8 values, four lanes share a block.
 template <int QT>
 __device__ void build_x_table_q8(uint32_t xs, int K, uint32_t xq, uint32_t dt, int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int b = warp; b < K / 32; b += kDW) {
-    uint32_t h;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(h) : "r"(xs + 2u * (uint32_t)(32 * b + lane)));
-    const float v = half_lo(h);
-    float a = fabsf(v);
+  for (int c = tid; c < K / 8; c += kDCompute) {  // K / 8 is a multiple of 32: a warp stays together
+    const int b = c >> 2, part = c & 3;
+    const uint4 u = lds128(xs + 16u * (uint32_t)c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float v[8], a = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int i = 0; i < 8; ++i) {
+      v[i] = half_lo(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+      a = fmaxf(a, fabsf(v[i]));
+    }
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
     const float d = __fdiv_rn(a, 127.0f);
-    int q = 0;
-    if (d != 0.0f) q = (int)fminf(fmaxf(roundf(__fdiv_rn(v, d)), -127.0f), 127.0f);
-    asm volatile("st.shared.s8 [%0], %1;" ::"r"(xq + (uint32_t)(32 * x_pos_q8<QT>(b) + lane)), "r"(q) : "memory");
-    int s = q;
+    uint32_t q[2] = {0u, 0u};
+    int s = 0;
+    if (d != 0.0f) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);  // within each half of the warp
-    if (lane == 0) {
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(dt + 16u * (uint32_t)b), "f"(d), "f"((float)s)
-                   : "memory");
-    } else if (lane == 16) {
+      for (int i = 0; i < 8; ++i) {
+        const int k = (int)fminf(fmaxf(roundf(__fdiv_rn(v[i], d)), -127.0f), 127.0f);
+        q[i >> 2] |= ((uint32_t)k & 0xFFu) << (8 * (i & 3));
+        s += k;
+      }
+    }
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(xq + (uint32_t)(32 * x_pos_q8<QT>(b) + 8 * part)),
+                 "r"(q[0]), "r"(q[1])
+                 : "memory");
+    s += __shfl_xor_sync(0xffffffffu, s, 1);  // 16 values
+    if (part == 0)
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(dt + 16u * (uint32_t)b), "f"(d), "f"((float)s) : "memory");
+    else if (part == 2)
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(dt + 16u * (uint32_t)b + 8u), "f"((float)s), "f"(0.0f)
                    : "memory");
-    }
   }
 }
 
