@@ -555,7 +555,7 @@ struct GemvProb {
   const float* xd;      // int8 x given with its scales: x points at K int8 values, xd at K / 32 scales
   int N, K, qtype, kind;
   int pair;             // one tensor, whole rows: a stage holds two adjacent 16-row tiles
-  int cb;               // K blocks per chunk (a stage holds 16 rows x cb blocks per weight tensor)
+  int cb;               // K blocks per chunk, the last maybe fewer (a stage holds 16 rows x cb blocks per weight tensor)
   int stages;           // pipeline depth of this problem's CTAs
   uint32_t stage_bytes;
   uint32_t ctl_off, red_off, ring_off;  // shared-memory layout of this problem's CTAs
@@ -1040,7 +1040,7 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
   const int ncomb = pair ? 2 : nten;  // row sets per stage: two tiles, or gate and up
   const int redw = ncomb * 16 * MT;   // partial floats per warp and stage
   const int64_t RB = (int64_t)nb * kBB;
-  const int nchunks = nb / cb;
+  const int nchunks = (nb + cb - 1) / cb;  // the last may be smaller
   const uint32_t SB = P.stage_bytes;
   const uint32_t comb_bytes = (uint32_t)(16 * cb * kBB);  // one row set's share of a stage
   const uint32_t pitch = cb == nb ? (uint32_t)RB : (uint32_t)(cb * kBB);
@@ -1129,13 +1129,13 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
       } else {
         // a K chunk: one copy per row of cb blocks (16-byte aligned by construction)
         const int rows = min(16, N - n0);
-        const uint32_t row_bytes = (uint32_t)(cb * kBB);
+        const uint32_t row_bytes = (uint32_t)(min(cb, nb - chunk * cb) * kBB);
         if (lane == 0) mbar_arrive_expect_tx(&ctl->full[s], row_bytes * (uint32_t)(rows * nten));
         __syncwarp();
         for (int i = lane; i < rows * nten; i += 32) {
           const int t = i / rows, r = i - t * rows;
           fence_proxy_async_smem();
-          bulk_copy_g2s(dst + (size_t)t * comb_bytes + (size_t)r * row_bytes,
+          bulk_copy_g2s(dst + (size_t)t * comb_bytes + (size_t)r * pitch,
                         (t ? P.w[1] : P.w[0]) + (int64_t)(n0 + r) * RB + (int64_t)chunk * cb * kBB, row_bytes,
                         &ctl->full[s]);
         }
@@ -1254,11 +1254,11 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
     for (int st = 0; st < steps; ++st) {
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
-      const int j0 = chunk * cb;
+      const int j0 = chunk * cb, blocks = min(cb, nb - j0);
       int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_r + (uint32_t)s * SB;
-      for (; ok && b < cb; b += kDW) {
+      for (; ok && b < blocks; b += kDW) {
         const int j = j0 + b;
         const uint32_t rb = stg + (uint32_t)(b * kBB);
         const uint32_t xa = xq + 256u * (uint32_t)j, da = dq + 128u * (uint32_t)j;
@@ -1309,11 +1309,11 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
       // this warp's blocks of the chunk: j = chunk * cb + b with j mod kDW = cls
-      const int j0 = chunk * cb;
+      const int j0 = chunk * cb, blocks = min(cb, nb - j0);
       int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_s + (uint32_t)s * SB;
-      for (; ok && b < cb; b += kDW) {
+      for (; ok && b < blocks; b += kDW) {
         const int j = j0 + b;
         const uint32_t r0 = stg + (uint32_t)(b * kBB);
         const uint32_t xa = xt_lane + (uint32_t)j * L.xt_stride;
@@ -1365,11 +1365,11 @@ __device__ __forceinline__ void decode_problem(const GemvProb& P, int cta, uint8
     for (int st = 0; st < steps; ++st) {
       const int s = st % S, chunk = st % nchunks;
       if (ok) ok = mbar_wait(&ctl->full[s], (uint32_t)(st / S) & 1u, &ctl->abort_flag, &g_gemv_status);
-      const int j0 = chunk * cb;
+      const int j0 = chunk * cb, blocks = min(cb, nb - j0);
       int b = cls - j0 % kDW;
       if (b < 0) b += kDW;
       const uint32_t stg = ring_s + (uint32_t)s * SB;
-      for (; ok && b < cb; b += kDW) {
+      for (; ok && b < blocks; b += kDW) {
         const int j = j0 + b;
         const uint32_t r0 = stg + (uint32_t)(b * kBB);
         uint32_t xa[NT];
@@ -1458,9 +1458,10 @@ int slots_for(int64_t M) { return M <= 1 ? 1 : 8; }
 // (several tokens: x is copied straight into the table area and rearranged
 // in place).  Stage geometry, first that fits: two adjacent whole tiles of
 // one tensor per stage (one token only) with at least 3 stages; whole tiles
-// (gate and up together) with 3; the largest 16-byte-aligned chunk of cb
-// blocks with 3, of kDMinChunk bytes a row at least; then the same with 2
-// stages and chunks of any size (several tokens: with 2 stages from the start).
+// (gate and up together) with 3; the fewest 16-byte-aligned chunks of cb blocks
+// (the last may have fewer) with 3, of kDMinChunk bytes a row at least; then the
+// same with 2 stages and chunks of any size (several tokens: with 2 stages from
+// the start).
 bool plan_decode_problem(const GemvDesc& d, GemvProb& P, size_t* smem_out) {
   memset(&P, 0, sizeof(P));
   if (d.M < 1 || d.M > kMaxGemvM || d.N <= 0 || d.N >= ((int64_t)1 << 31) || d.K <= 0 || d.K % kQK != 0 ||
@@ -1512,9 +1513,12 @@ bool plan_decode_problem(const GemvDesc& d, GemvProb& P, size_t* smem_out) {
       cb = nb, S = stages_for((size_t)16 * RB * nten, false);
       break;
     }
-    for (int c = nb - 1; c >= 1 && !cb; --c) {
-      if (nb % c != 0 || (c * bb) % 16 != 0 || RB % 16 != 0) continue;
-      if (want > 2 && c * bb < kDMinChunk) continue;
+    if (RB % 16 != 0) continue;
+    // as few chunks as can be, of a size (the last may be smaller)
+    const int unit = bb % 16 == 0 ? 1 : 8;  // blocks that are a multiple of 16 bytes
+    for (int k = 2; k <= nb / unit && !cb; ++k) {
+      const int c = (nb + k * unit - 1) / (k * unit) * unit, last = nb - (nb - 1) / c * c;
+      if (want > 2 && last * bb < kDMinChunk) continue;
       if (stages_for((size_t)16 * c * bb * nten, false) >= want)
         cb = c, S = stages_for((size_t)16 * c * bb * nten, false);
     }

@@ -152,6 +152,29 @@ def test_matmul_q8(qk_lib, cuda, qtype, N, K):
     assert np.abs(_host(y1) - ref).max() <= 2e-3 * np.sqrt((ref ** 2).mean())
 
 
+@pytest.mark.parametrize("qtype,N,K", [("q4k", 40, 11008), ("q4k", 2500, 9472), ("q4k", 17, 12032), ("q6k", 40, 14336),
+                                       ("q6k", 2500, 10240), ("q6k", 33, 22528)])
+def test_matmul_rows_in_unequal_chunks(qk_lib, cuda, qtype, N, K):
+    """Rows that go out in chunks of which the last is smaller: int8 x as above, and
+    fp16 x of one token and of four within the fp16 path's bar."""
+    test_matmul_q8(qk_lib, cuda, qtype, N, K)
+    import torch
+    rng = synth.rng_for(226, N * K)
+    W, x = synth.weights(rng, qtype, N, K), synth.activations(rng, 4, K)
+    ref = oracle.matmul(QT[qtype], W, x, N, K)
+    w, f = _dev(W, cuda), qk_lib.qk_matmul_q4k if qtype == "q4k" else qk_lib.qk_matmul_q6k
+    for M in (1, 4):
+        y = torch.full((M, N), math.nan, device=cuda)
+        f(w, _dev(x[:M].view(np.uint16), cuda), y, M, N, K)
+        qk_lib.qk_get_device_status()
+        assert np.abs(_host(y) - ref[:M]).max() <= 1e-2 * np.sqrt((ref[:M] ** 2).mean())
+    if qtype == "q4k":
+        y = torch.full((1, N), math.nan, dtype=torch.float16, device=cuda)
+        qk_lib.qk_gateup_swiglu_q4k(w, w, _dev(x[:1].view(np.uint16), cuda), y, 1, N, K)
+        ref = oracle.gateup_swiglu(W, W, x[:1], N, K)
+        assert np.abs(_host(y).astype(np.float64) - ref).max() <= 1e-2 * np.sqrt((ref ** 2).mean())
+
+
 def test_matmul_q8_extreme_values(qk_lib, cuda):
     """Any int8, -128 among them, and any finite scale."""
     import torch
