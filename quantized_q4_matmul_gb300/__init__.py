@@ -195,6 +195,11 @@ def _n(v) -> int:
     return v if v > 0 else 0
 
 
+def _size(a: int, b: int, c: int = 1) -> int:
+    """a * b * c, or 0 where one of them is not positive."""
+    return a * b * c if a > 0 and b > 0 and c > 0 else 0
+
+
 _BLOCK_BYTES = {QK_Q4_K: 144, QK_Q6_K: 210}
 
 
@@ -204,18 +209,21 @@ def _weight_bytes(qtype, N, K) -> int:
 
 
 _raw_stream = None  # device index -> the address of torch's current stream on it
+_device = None      # the current device's index
 
 
 def _stream(stream) -> int:
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object: 2.8 us of a call,
-        # against 0.3 us for the stream's address alone.
-        global _raw_stream
-        import torch
+        # against 0.2 us for the stream's address alone.
+        global _raw_stream, _device
         if _raw_stream is None:
+            import torch
+            torch.cuda.current_device()  # sets torch's CUDA state up
+            _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -326,13 +334,13 @@ def qk_matmul_batch_q8(problems, stream=None) -> None:
         M, N, K = int(p["M"]), int(p["N"]), int(p["K"])
         up = p.get("up_blocks")
         gu = up is not None
-        wb = _weight_bytes(qt, N, K)
-        n = _n(M) * _n(K)
+        wb = _size(N, K // 256, _BLOCK_BYTES.get(qt, 0))
+        n = _size(M, K)
         arr[i] = qk_matmul_q8_desc(qt, _buf(p["blocks"], wb, ("qk_matmul_batch_q8[%d]: blocks", i)),
                                    _buf(up, wb, ("qk_matmul_batch_q8[%d]: up_blocks", i)),
                                    _buf(p["x_q8"], n, ("qk_matmul_batch_q8[%d]: x_q8", i), _I8),
                                    _buf(p["x_d"], n // 8, ("qk_matmul_batch_q8[%d]: x_d", i), _F32),
-                                   _buf(p["y"], _n(M) * _n(N) * (2 if gu else 4), ("qk_matmul_batch_q8[%d]: y", i),
+                                   _buf(p["y"], _size(M, N, 2 if gu else 4), ("qk_matmul_batch_q8[%d]: y", i),
                                         _F16 if gu else _F32), M, N, K)
     _check(lib().qk_matmul_batch_q8(arr, len(problems), _stream(stream)), "qk_matmul_batch_q8")
 
@@ -403,14 +411,15 @@ def qk_rope_kv_append(q, k, v, inv_freq, q_f16, k_cache, v_cache, M: int, H: int
     """Rotary positions on the QKV projections' outputs and the new cache rows (see
     include/qk.h): q, k, v fp32 [M][heads][D], inv_freq float64 [n_rot / 2], q_f16
     [M][H][D] fp16, caches [H_kv][L_max][D] fp16."""
-    qn, kn, cn = _n(M) * _n(H) * _n(D), _n(M) * _n(H_kv) * _n(D), _n(H_kv) * _n(L_max) * _n(D)
+    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    qn, kn, cn = _size(M, H, D), _size(M, H_kv, D), _size(H_kv, L_max, D)
     _check(lib().qk_rope_kv_append(_buf(q, 4 * qn, "qk_rope_kv_append: q", _F32), _buf(k, 4 * kn, "qk_rope_kv_append: k", _F32),
                                    _buf(v, 4 * kn, "qk_rope_kv_append: v", _F32),
                                    _buf(inv_freq, 4 * _n(n_rot), "qk_rope_kv_append: inv_freq", _F64),
                                    _buf(q_f16, 2 * qn, "qk_rope_kv_append: q_f16", _F16),
                                    _buf(k_cache, 2 * cn, "qk_rope_kv_append: k_cache", _F16),
-                                   _buf(v_cache, 2 * cn, "qk_rope_kv_append: v_cache", _F16), int(M), int(H), int(H_kv), int(D),
-                                   int(n_rot), int(pos0), int(L_max), int(layout), float(magnitude),
+                                   _buf(v_cache, 2 * cn, "qk_rope_kv_append: v_cache", _F16), M, H, H_kv, D,
+                                   int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
                                    _stream(stream)), "qk_rope_kv_append")
 
 
@@ -536,13 +545,13 @@ def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_
                             L_max: int, scale: float, window: int, sinks: int = 0, stream=None) -> None:
     """qk_gqa_attention with a sliding window of `window` positions and the first
     `sinks` positions always visible (see include/qk.h); out [M][H][D] fp16."""
-    qn = _n(M) * _n(H) * _n(D)
-    cn = _n(H_kv) * _n(L_max) * _n(D)
+    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
     _check(lib().qk_gqa_attention_window(_buf(q_f16, 2 * qn, "qk_gqa_attention_window: q_f16", _F16),
                                          _buf(k_cache, 2 * cn, "qk_gqa_attention_window: k_cache", _F16),
                                          _buf(v_cache, 2 * cn, "qk_gqa_attention_window: v_cache", _F16),
-                                         _buf(out_f16, 2 * qn, "qk_gqa_attention_window: out_f16", _F16), int(M), int(H), int(H_kv),
-                                         int(D), int(pos0), int(L_max), float(scale), int(window), int(sinks),
+                                         _buf(out_f16, 2 * qn, "qk_gqa_attention_window: out_f16", _F16), M, H, H_kv,
+                                         D, int(pos0), L_max, float(scale), int(window), int(sinks),
                                          _stream(stream)), "qk_gqa_attention_window")
 
 
