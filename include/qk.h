@@ -387,11 +387,11 @@ qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const
  * and a query that sees nothing (window = sinks = 0) gives zeros.  Only the
  * rows of the caches that some query of the call sees are used: rows between
  * the sinks and the first query's window, and rows past the last query, may
- * hold anything.  (A non-finite value in a row that only later queries of a
- * prefill see can still reach the outputs of earlier queries.)  scale is
- * finite, and scale * log2(e) * q . k must stay within fp32.  Other arguments,
- * limits and errors as in qk_gqa_attention; out: [M][H][D] fp16, within about
- * 2^-10 * max|v| of the exact value plus its own rounding.
+ * hold anything.  What a row holds, NaN and infinities included, reaches the
+ * queries that see it and no other.  scale is finite, and scale * log2(e) *
+ * q . k must stay within fp32.  Other arguments, limits and errors as in
+ * qk_gqa_attention; out: [M][H][D] fp16, within about 2^-10 * max|v| of the
+ * exact value plus its own rounding.
  */
 qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,
                                   uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,

@@ -31,6 +31,9 @@
 // Pairs of query tiles that would leave most of a last round of SMs idle are
 // taken apart: a CTA for each tile.
 //
+// Rows whose result is not finite are computed again without the positions that
+// they do not see (attend_row).
+//
 // Bound by the softmax beside the tensor core: 4095 queries after 4001, 24 heads
 // over 8, window 2048: 109 us, 953 TFLOP/s of the visible pairs (the tensor
 // pipe is active in 44 % of the cycles, the schedulers issue in 42 %); 2048
@@ -79,9 +82,10 @@ struct WpShared {
 };
 
 struct WpArgs {
+  const __half *q, *kc, *vc;
   __half* out;
   int H, Hkv, G, queries;  // query heads, key/value heads, heads per key/value head, queries per tile
-  int64_t M, pos0, window, sinks;
+  int64_t M, pos0, Lmax, window, sinks;
   float scale_log2e;
   unsigned units, pairs;  // pairs of query tiles of all key/value heads; those of them that are one CTA's
   int split;              // CTAs (of a cluster) that share a pair of query tiles
@@ -129,6 +133,73 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// One query row of one head by one warp, over the positions that it sees and no
+// other; lane t takes the dimensions 4 t .. 4 t + 3 of the result.  The tensor
+// core multiplies a hidden position's value row by the weight 0, and 0 times
+// infinity is not 0: rows that come out non-finite are done again here, so that
+// a non-finite value row reaches those queries alone that see it.
+__device__ __noinline__ void attend_row(const WpArgs& A, int64_t row, int head) {
+  const int lane = threadIdx.x & 31;
+  const int64_t p = A.pos0 + row, kv = (int64_t)(head / A.G) * A.Lmax * kD;
+  const uint4* qr = reinterpret_cast<const uint4*>(A.q + (row * A.H + head) * kD);
+  const int64_t end1 = min(A.sinks, p + 1), from2 = max(end1, p - A.window + 1);
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int run = 0; run < 2; ++run) {
+    const int64_t end = run == 0 ? end1 : p + 1;
+    for (int64_t base = run == 0 ? 0 : from2; base < end; base += 32) {
+      const int64_t j = base + lane;
+      float s = -INFINITY;
+      if (j < end) {
+        const uint4* kr = reinterpret_cast<const uint4*>(A.kc + kv + j * kD);
+        s = 0.f;
+        for (int i = 0; i < kD / 8; ++i) {
+          const uint4 a = qr[i], b = kr[i];
+          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+            s = fmaf(u.y, v.y, fmaf(u.x, v.x, s));
+          }
+        }
+        s *= A.scale_log2e;
+      }
+      float mn = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mn = fmaxf(mn, m);
+      const float ref = mn == -INFINITY ? 0.f : mn, corr = exp2f(m - ref);
+      m = mn;
+      const float w = exp2f(s - ref);
+      float sum = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = fmaf(l, corr, sum);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] *= corr;
+      for (int e = 0; e < 32 && base + e < end; ++e) {
+        const float we = __shfl_sync(0xffffffffu, w, e);
+        const uint2 v = *reinterpret_cast<const uint2*>(A.vc + kv + (base + e) * kD + 4 * lane);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+        acc[0] = fmaf(we, a.x, acc[0]);
+        acc[1] = fmaf(we, a.y, acc[1]);
+        acc[2] = fmaf(we, b.x, acc[2]);
+        acc[3] = fmaf(we, b.y, acc[3]);
+      }
+      // nothing more to find out about a row that is NaN throughout
+      const bool nan = acc[0] != acc[0] && acc[1] != acc[1] && acc[2] != acc[2] && acc[3] != acc[3];
+      if (__all_sync(0xffffffffu, nan || l != l)) {
+        run = 2;
+        break;
+      }
+    }
+  }
+  const float inv = 1.0f / l;
+  *reinterpret_cast<uint2*>(A.out + (row * A.H + head) * kD + 4 * lane) =
+      make_uint2(pack_h2(acc[0] * inv, acc[1] * inv), pack_h2(acc[2] * inv, acc[3] * inv));
 }
 
 // Bits e of 0 .. 31 with lo <= e < hi.
@@ -502,19 +573,29 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const float inv = 1.0f / (a + b);
       const bool on = r < G * A.queries && row < A.M;
       __half* dst = A.out + (row * A.H + g * G + r % G) * kD;
+      uint64_t check2 = 0;  // 0, or NaN from a product of 0 and a value that is not finite
 #pragma unroll 1
       for (int c = 0; c < kD / 16; ++c) {
         uint32_t w[16], o[8];
         tmem_ld16(t_o + (uint32_t)(16 * c), w);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 8; ++e) {
+          check2 = fma2(pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])), 0, check2);
           o[e] = pack_h2(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+        }
         if (on) {
           uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
           d[0] = make_uint4(o[0], o[1], o[2], o[3]);
           d[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
+      }
+      unpack2(check2, a, b);
+      uint32_t again = __ballot_sync(0xffffffffu, on && !(a + b + inv * 0.f == 0.f));
+      __syncwarp();
+      for (; again; again &= again - 1) {
+        const int rr = 32 * (warp & 3) + __ffs((int)again) - 1;
+        attend_row(A, q0 + t * A.queries + rr / G, g * G + rr % G);
       }
     }
     __syncwarp();
@@ -548,8 +629,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         o.w = fmaf(w, v.w, o.w);
       }
       const float inv = 1.0f / l;
-      *reinterpret_cast<uint2*>(A.out + (row * A.H + g * G + r % G) * kD + 4 * lane) =
-          make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+      if (__any_sync(0xffffffffu, !((o.x + o.y + o.z + o.w + inv) * 0.f == 0.f)))
+        attend_row(A, row, g * G + r % G);
+      else
+        *reinterpret_cast<uint2*>(A.out + (row * A.H + g * G + r % G) * kD + 4 * lane) =
+            make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
     }
     __syncwarp();
     cluster_sync_all();  // no CTA leaves while its part is read
@@ -648,13 +732,17 @@ cudaError_t launch_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t
   // 9.6; 2048 after 8000, window 2048 (200): 70.0, 64.8.
   const int64_t sms = device_sms(), over = units % sms;
   const int64_t singles = split == 1 && M > queries && 2 * over <= sms ? over : 0;
-  const WpArgs A{reinterpret_cast<__half*>(out),
+  const WpArgs A{reinterpret_cast<const __half*>(q),
+                 reinterpret_cast<const __half*>(kc),
+                 reinterpret_cast<const __half*>(vc),
+                 reinterpret_cast<__half*>(out),
                  H,
                  Hkv,
                  G,
                  queries,
                  M,
                  pos0,
+                 Lmax,
                  window,
                  sinks,
                  sl2e,

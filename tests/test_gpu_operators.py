@@ -440,6 +440,31 @@ def test_window_empty_rows_are_zero(qk_lib, cuda):
         assert (_attn(qk_lib, cuda, q, k, v, 6, 2, 50, 0, 0) == 0).all()
 
 
+@pytest.mark.parametrize("M,pos0,window,sinks,H,Hkv", [
+    (130, 0, 60, 0, 6, 2), (130, 200, 90, 5, 24, 8), (300, 400, 150, 0, 4, 4), (9, 3000, 2500, 4, 8, 2),
+    (40, 5, 10 ** 6, 0, 7, 1), (70, 10, 0, 40, 6, 2), (1, 500, 200, 3, 6, 2)])
+def test_window_values_reach_only_who_sees_them(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
+    """Non-finite keys and values at positions that some queries of a tile see and
+    others do not: the others' outputs are what they would be without them."""
+    q, k, v = _attn_inputs(227, M, H, Hkv, pos0, pos0 + M, window, sinks)
+    p1 = pos0 + M - 1
+    for n, (j, what, dims) in enumerate([(p1, np.nan, slice(None)), (pos0 + M // 2, np.inf, slice(0, 5)),
+                                         (max(0, pos0 - window + 1), -np.inf, slice(60, None)),
+                                         (pos0 + M // 3, np.nan, slice(7, 8))]):
+        v[:, j, dims] = what
+        if n == 0:
+            k[:, j, 3] = np.nan
+    got = _attn(qk_lib, cuda, q, k, v, H, Hkv, pos0, window, sinks).astype(np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = _attn_reference(q, k, v, H, Hkv, pos0, window, sinks)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    inf = np.isinf(ref)
+    assert np.array_equal(got[inf], ref[inf]) and not np.isinf(got[~inf]).any()
+    fine = np.isfinite(ref)
+    assert fine.any() or M == 1
+    _attn_check(got[fine], ref[fine], v, "beside non-finite values")
+
+
 @pytest.mark.parametrize("scale_sign", [1.0, -1.0])
 def test_window_large_scores(qk_lib, cuda, scale_sign):
     """Scores of hundreds (one position takes all the weight), either sign of scale."""
