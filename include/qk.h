@@ -186,8 +186,9 @@ qk_status qk_matmul_q8x_q6k(const void *blocks, const uint16_t *x_f16, float *y,
  *   xhat[m][k] = fp16( x[m][k] / sqrt(mean_k x[m][k]^2 + eps) * gamma[k] )
  * (sum of squares, scale and products in fp32; gamma is fp16[K], the same K
  * for every problem of the call; eps finite and >= 0) and the problems then
- * run as in qk_matmul_batch.  Problems the GEMV runs (M <= 8, see
- * qk_uses_gemv) normalize inside its x staging: no extra pass, no scratch.
+ * run as in qk_matmul_batch.  Problems the GEMV runs (M <= 8 where its plan
+ * fits with gamma beside x; qk_uses_gemv answers for no norm, and some K fit
+ * there alone) normalize inside its x staging: no extra pass, no scratch.
  * Problems the tensor-core GEMM runs first have their xhat written to
  * `scratch`, a caller-owned device buffer of at least qk_rmsnorm_scratch_bytes
  * (the largest M * K * 2 over those problems; NULL is allowed when no problem

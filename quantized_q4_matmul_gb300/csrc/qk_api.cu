@@ -311,11 +311,14 @@ qk_status matmul_batch(const qk_matmul_desc* d, int count, cudaStream_t s) {
 }
 
 // Bytes of RMSNorm scratch one problem needs: 0 when the GEMV runs it (the
-// norm is fused into its x staging), else M * K fp16.
+// norm is fused into its x staging), else M * K fp16.  Asked of the plan that
+// run_batch makes: gamma is staged in shared memory too, so some K fit the GEMV
+// without a norm and not with one.
 int64_t norm_scratch_bytes(const qk_matmul_desc& d) {
   if (d.M == 0 || d.N == 0) return 0;
   const QType t = d.qtype == QK_Q4_K ? qk::kQ4K : qk::kQ6K;
-  const qk::GemvDesc g{t, d.blocks, d.up_blocks, d.x_f16, d.y, d.M, d.N, d.K, nullptr, 0.f};
+  const uint16_t* gamma = reinterpret_cast<const uint16_t*>(uintptr_t(16));  // marks the norm, not dereferenced
+  const qk::GemvDesc g{t, d.blocks, d.up_blocks, d.x_f16, d.y, d.M, d.N, d.K, gamma, 0.f};
   return use_gemv(g) ? 0 : d.M * d.K * 2;
 }
 
