@@ -252,8 +252,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          // relative to 0 where no visible score is a number yet: hidden scores
+          // have weight 0 there too, and NaN, which the maximum passes over, stays
           const float m = mrow[c >> 1];
-          const float p = m == -INFINITY ? 0.f : exp2f(sc[j][c] - m);
+          const float p = exp2f(sc[j][c] - (m == -INFINITY ? 0.f : m));
           sc[j][c] = p;
           lrow[c >> 1] += p;
         }
@@ -299,8 +301,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (e > 0) {
         acc = 0.f;
         for (int w = 0; w < kDecWarps; ++w) {
+          // a warp that saw nothing has sum 0; one that saw NaN alone has no
+          // maximum either, but a NaN sum
           const float mw = part[w][row][0];
-          if (mw != -INFINITY) acc = fmaf(exp2f(mw - M), part[w][row][e], acc);
+          if (mw != -INFINITY || part[w][row][1] != 0.f) acc = fmaf(exp2f(mw - M), part[w][row][e], acc);
         }
       }
       st_cluster_f32(red0 + 4u * (uint32_t)i, acc);
