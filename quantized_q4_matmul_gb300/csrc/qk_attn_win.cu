@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (A.split > 1) {
       // Every UMMA of both query tiles is done: their key and value tiles may go.
       named_bar_sync(1, 256u);
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_stat(S, t, r)), "f"(ok ? m : -INFINITY), "f"(a + b)
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(part_stat(S, t, r)), "f"(ok ? m : -INFINITY),
+                   "f"(ok ? a + b : 0.f)
                    : "memory");
       if (ok) {
         tc_fence_after();
@@ -619,7 +620,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < kWMaxSplit; ++c) {
-        if (st[c].x == -INFINITY) continue;  // it saw nothing of this row
+        // It saw nothing of this row.  One that saw NaN alone has no maximum
+        // either, but its sum is NaN, and so is the row's then.
+        if (st[c].x == -INFINITY && st[c].y == 0.f) continue;
         const float w = exp2f(st[c].x - mx);
         const float4 v = ld_cluster4(mapa_shared(part_chunk(S, t, r, lane), (uint32_t)c));
         l = fmaf(w, st[c].y, l);

@@ -59,3 +59,29 @@ def test_causal_decode_keys(qk_lib, cuda, pos0, at):
         ref = _attn_reference(q, k, v, H, Hkv, pos0, pos0 + 1, 0)
     assert np.isnan(ref[:, :3]).all() and np.isfinite(ref[:, 3:]).all()
     _compare(_host(out), ref, v, "causal decode")
+
+
+# One key that is NaN, at the edges of what a query sees and of what a CTA of the
+# cluster takes.  M = 256: 18 key tiles from position 5953, two or three for each of
+# eight CTAs; the last query's window begins at 6208, the last row of the first two.
+@pytest.mark.parametrize("M,H,Hkv,pos0,window,sinks,at", [
+    (256, 8, 8, 8000, 2048, 0, [6208, 6207, 6209, 8000, 8127, 8128, 8255]),
+    (256, 8, 8, 8000, 2048, 1, [0, 6208]), (2, 6, 2, 6000, 4096, 0, [1905, 1906, 6001, 4000]),
+    (9, 4, 1, 4000, 0, 4000, [0, 3999]), (300, 8, 8, 100, 150, 100, [0, 99, 399]), (40, 24, 8, 3000, 2900, 7, [140, 6])])
+def test_window_prefill_keys(qk_lib, cuda, M, H, Hkv, pos0, window, sinks, at):
+    """The queries that see it are NaN, in the heads that have it; every other
+    output keeps its bits."""
+    q, k, v = _attn_inputs(232, M, H, Hkv, pos0, pos0 + M, window, sinks)
+    k, v = np.nan_to_num(k, posinf=0, neginf=0), np.nan_to_num(v, posinf=0, neginf=0)
+    clean = _attn(qk_lib, cuda, q, k, v, H, Hkv, pos0, window, sinks)
+    assert np.isfinite(clean).all()
+    p = pos0 + np.arange(M)
+    for j in at:
+        bad = k.copy()
+        bad[Hkv - 1, j, 77] = np.nan
+        got = _attn(qk_lib, cuda, q, bad, v, H, Hkv, pos0, window, sinks)
+        sees = (j <= p) & ((j > p - window) | (j < sinks))
+        hit = np.zeros(got.shape, bool)
+        hit[sees, H - H // Hkv:] = True
+        assert np.array_equal(np.isnan(got), hit), (j, np.isnan(got).any((1, 2)).sum(), sees.sum())
+        assert np.array_equal(got[~hit], clean[~hit]), j
