@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     S.abort_flag = 0;
     fence_mbar_init();
   }
+  __syncwarp();        // each warp arrives converged (the cluster barrier is .aligned)
   cluster_sync_all();  // barriers initialised; every CTA of the cluster is running (DSMEM below)
   if (kWin) dependent_wait();
 

@@ -602,6 +602,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __syncwarp();
   }
   if (A.split > 1) {
+    __syncwarp();        // each warp arrives converged (the cluster barrier is .aligned)
     cluster_sync_all();  // every CTA's part is in its shared memory
     // A warp joins one row at a time, a lane four of its columns.
     for (int i = warp * A.split + rank; i < 256; i += kWWarps * A.split) {

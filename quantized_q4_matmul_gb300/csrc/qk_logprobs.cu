@@ -246,7 +246,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   const int64_t v0 = nv * rank / C, v1 = nv * (rank + 1) / C;
   const int batches = (int)((v1 - v0 + kLpBatch - 1) / kLpBatch);
   const int per_seg = (batches + kLpSegs - 1) / kLpSegs;  // batches per segment (1 up to 131072 logits)
-  if (C > 1) cluster_arrive();
+  if (C > 1) {
+    __syncwarp();  // each warp arrives converged (the cluster barrier is .aligned)
+    cluster_arrive();
+  }
   dependent_wait();
   const int token = rank == 0 && tid == 0 && A.logprob ? A.tokens[row] : -1;
   if (tid == 0) S.n_above = S.n_equal = S.n_cand = 0;
@@ -378,6 +381,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
   }
   const uint64_t* best = S.best;
   if (C > 1) {
+    __syncwarp();
     cluster_wait();  // every CTA of the cluster is running
     if (warp == 0) {
       const uint32_t to = mapa_shared(smem_u32(&S.cstat[rank]), 0);
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
                      "l"(S.best[lane])
                      : "memory");
     }
+    __syncwarp();
     cluster_sync_all();
     if (rank != 0) return;
     if (n > 0) select_n_sorted(S.best, S.all, C, n, tid);
