@@ -392,7 +392,9 @@ qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const
  * queries that see it and no other.  scale is finite, and scale * log2(e) *
  * q . k must stay within fp32.  Other arguments, limits and errors as in
  * qk_gqa_attention; out: [M][H][D] fp16, within about 2^-10 * max|v| of the
- * exact value plus its own rounding.
+ * exact value plus its own rounding where a query sees 2^20 positions at most
+ * (weights below 2^-25 of the largest of a warp's own share in decode, 2^-32 of
+ * a query's in prefill, count in the sum alone).
  */
 qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,
                                   uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,

@@ -490,13 +490,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ext[0] = fminf(fminf(ext[0], ext[1]), fminf(ext[2], ext[3]));
       }
       const float tmax = ext[0] * scale;
-      // The reference max moves only when the row max grows by more than 2^8:
-      // the weights 2^(s - m) then stay below 256 (fp16 holds them) and O is
-      // rescaled rarely; O and l use the same reference, so the result is the
-      // same softmax.  A row that has seen nothing yet keeps m = -inf, and its
-      // weights, all 0, are taken relative to 0.
-      const bool upd = (m == -INFINITY && tmax != -INFINITY) || tmax > m + 8.0f;
-      const float mn = upd ? tmax : m;
+      // The reference m is 7 below the row's maximum and moves only when that
+      // grows by more than 8: the weights 2^(s - m) then reach 2^15 (fp16 holds
+      // them) and O is rescaled rarely; O and l use the same reference, so the
+      // result is the same softmax.  The 7 keep small weights: fp16 drops what is
+      // 2^-32 of the largest or less, where it dropped 2^-25, of which 2^17
+      // positions hold 2^-8 of the sum.  A row that has seen nothing yet keeps
+      // m = -inf, and its weights, all 0, are taken relative to 0.
+      const bool upd = (m == -INFINITY && tmax != -INFINITY) || tmax > m + 15.0f;
+      const float mn = upd ? tmax - 7.0f : m;
       const float corr = upd ? exp2f(m - mn) : 1.0f;
       m = mn;
       const float mref = m == -INFINITY ? 0.f : m;
