@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         acc = fmaf(c, S.red[r][row][2 + d], acc);
       }
       if (kWin)
-        W.out[(int64_t)(g * G + row) * kD + d] = __float2half_rn(acc / lsum);
+        W.out[(int64_t)(g * G + row) * kD + d] = __float2half_rn(within_half(acc / lsum));
       else
         out[(int64_t)(g * G + row) * kD + d] = acc / lsum;
     }

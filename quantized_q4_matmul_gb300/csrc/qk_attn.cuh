@@ -55,6 +55,13 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// An average of fp16 values, in fp32, for its rounding to fp16: weights that are
+// rounded one by one can carry it past the largest finite value, which the exact
+// average never passes.  Infinities stay.
+__device__ __forceinline__ float within_half(float x) {
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+}
+
 constexpr int kTBox = 128 * 128;           // one 64-wide box of 128 rows of 128 bytes: 16 KB
 constexpr int kTTile = 2 * kTBox;          // 32 KB: Q, one key or value tile, or P
 

@@ -199,7 +199,8 @@ __device__ __noinline__ void attend_row(const WpArgs& A, int64_t row, int head) 
   }
   const float inv = 1.0f / l;
   *reinterpret_cast<uint2*>(A.out + (row * A.H + head) * kD + 4 * lane) =
-      make_uint2(pack_h2(acc[0] * inv, acc[1] * inv), pack_h2(acc[2] * inv, acc[3] * inv));
+      make_uint2(pack_h2(within_half(acc[0] * inv), within_half(acc[1] * inv)),
+                 pack_h2(within_half(acc[2] * inv), within_half(acc[3] * inv)));
 }
 
 // Bits e of 0 .. 31 with lo <= e < hi.
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           check2 = fma2(pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])), 0, check2);
-          o[e] = pack_h2(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+          o[e] = pack_h2(within_half(__uint_as_float(w[2 * e]) * inv), within_half(__uint_as_float(w[2 * e + 1]) * inv));
         }
         if (on) {
           uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
@@ -639,7 +640,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         attend_row(A, row, g * G + r % G);
       else
         *reinterpret_cast<uint2*>(A.out + (row * A.H + g * G + r % G) * kD + 4 * lane) =
-            make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+            make_uint2(pack_h2(within_half(o.x * inv), within_half(o.y * inv)),
+                       pack_h2(within_half(o.z * inv), within_half(o.w * inv)));
     }
     __syncwarp();
     cluster_sync_all();  // no CTA leaves while its part is read

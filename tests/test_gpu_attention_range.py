@@ -1,4 +1,5 @@
-"""qk_gqa_attention_window at the ends of its range: a long tail of tiny weights."""
+"""qk_gqa_attention_window at the ends of its range: a long tail of tiny weights,
+and averages at the largest fp16 value."""
 import math
 
 import numpy as np
@@ -33,3 +34,27 @@ def test_a_long_tail_of_small_weights(qk_lib, cuda, M, H, Hkv):
     err = np.abs(_host(out).astype(np.float64) - ref).max()
     assert err <= 2.0 ** -10, err
     del k, v
+
+
+@pytest.mark.parametrize("M,H,Hkv,pos0,window,sinks", [
+    (1, 24, 8, 15, 16, 0), (1, 6, 2, 15, 100, 0), (300, 24, 8, 0, 300, 0), (40, 8, 8, 2000, 2100, 0),
+    (300, 8, 8, 500, 200, 1)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_values_at_the_largest_half(qk_lib, cuda, M, H, Hkv, pos0, window, sinks, sign):
+    """Every value is +-65504, so every average is.  Position 0 has weight 1 and
+    each other one 0.5 + 2^-12 + 2e-6, which rounds up to 0.5 + 2^-11 in fp16: the
+    rounded weights' sum is up to 2^-11 too large, past 65520, which would round to
+    infinity.  A row that does not reach it may be 2^-10 off."""
+    import torch
+    L = pos0 + M
+    scale = float(np.float32(-math.log(0.5 + 2.0 ** -12 + 2e-6)))
+    q = torch.zeros(M, H, D, dtype=torch.float16, device=cuda)
+    q[:, :, 0] = 1
+    k = torch.zeros(Hkv, L, D, dtype=torch.float16, device=cuda)
+    k[:, 1:, 0] = -1
+    v = torch.full((Hkv, L, D), 65504.0 * sign, dtype=torch.float16, device=cuda)
+    out = torch.full((M, H, D), math.nan, dtype=torch.float16, device=cuda)
+    qk_lib.qk_gqa_attention_window(q, k, v, out, M, H, Hkv, D, pos0, L, scale, window, sinks)
+    qk_lib.qk_get_device_status()
+    got = _host(out).astype(np.float64) * sign
+    assert np.isfinite(got).all() and (got >= 65504 * (1 - 2.0 ** -10)).all(), (np.isinf(got).sum(), got.min())
