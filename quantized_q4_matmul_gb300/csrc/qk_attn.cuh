@@ -62,6 +62,13 @@ __device__ __forceinline__ float within_half(float x) {
   return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
 }
 
+// The same in the rounding itself; infinities become the largest finite value.
+__device__ __forceinline__ uint32_t pack_h2_finite(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 constexpr int kTBox = 128 * 128;           // one 64-wide box of 128 rows of 128 bytes: 16 KB
 constexpr int kTTile = 2 * kTBox;          // 32 KB: Q, one key or value tile, or P
 

@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           check2 = fma2(pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])), 0, check2);
-          o[e] = pack_h2(within_half(__uint_as_float(w[2 * e]) * inv), within_half(__uint_as_float(w[2 * e + 1]) * inv));
+          o[e] = pack_h2_finite(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
         }
         if (on) {
           uint4* d = reinterpret_cast<uint4*>(dst + 16 * c);
