@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (row < G) {
         float* pr = part[warp][row];
         if (tq == 0) {
-          pr[0] = mrow[r];
+          // -inf: it saw nothing.  A warp that saw NaN alone has no maximum either,
+          // but a NaN sum: with NaN as its maximum it counts, and the row is NaN.
+          pr[0] = mrow[r] == -INFINITY && lrow[r] != 0.f ? NAN : mrow[r];
           pr[1] = lrow[r];
         }
 #pragma unroll
@@ -302,10 +304,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (e > 0) {
         acc = 0.f;
         for (int w = 0; w < kDecWarps; ++w) {
-          // a warp that saw nothing has sum 0; one that saw NaN alone has no
-          // maximum either, but a NaN sum
           const float mw = part[w][row][0];
-          if (mw != -INFINITY || part[w][row][1] != 0.f) acc = fmaf(exp2f(mw - M), part[w][row][e], acc);
+          if (mw != -INFINITY) acc = fmaf(exp2f(mw - M), part[w][row][e], acc);
         }
       }
       st_cluster_f32(red0 + 4u * (uint32_t)i, acc);
