@@ -288,6 +288,9 @@ qk_status qk_matmul_batch_q8(const qk_matmul_q8_desc *descs, int count, qk_strea
  * q = round(xhat / d), ties away from zero, d = 0 gives q = 0; finite xhat):
  * xq int8 [M][K] and xd fp32 [M][K / 32], one row of which is the x of
  * qk_matmul_batch_q8.  K is a multiple of 32 there.
+ * How many threads share a row follows M and the device, so the last bit of a
+ * row can differ between calls of different M; the same call repeats its bits.
+ * qk_matmul_batch_q8 takes one row of qk_add_rmsnorm_q8's output a call.
  * M = 0 is a no-op.
  */
 qk_status qk_add_rmsnorm(const void *residual, int residual_type, const float *delta, const uint16_t *gamma_f16,
@@ -370,8 +373,11 @@ qk_status qk_rope_inv_freq(const qk_rope_config *config, int64_t n_rot, double *
  * up to 8 CTAs per key/value head; M >= 2 (prefill, or a chunk of it after
  * pos0 cached positions) runs causal 128-query blocks on tcgen05.  Both score
  * on the tensor cores (fp16 operands, fp32 sums) and round the softmax weights
- * to fp16 for the P.V product: the result is within about 2^-10 * max|v| of
- * the exact value.  M = 0 is a no-op.  Errors: QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ALIAS,
+ * to fp16 for the P.V product (weights below 2^-25 of the largest count in the
+ * sum alone): the result is within about (2^-11 + n 2^-25) * max|v| of the exact
+ * value for n visible positions, 2^-10 up to 2^14 of them; in decode n is what
+ * one warp takes of them, about 1 / 64 from 2048 positions on.  M = 0 is a
+ * no-op.  Errors: QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ALIAS,
  * QK_ERR_POINTER, QK_ERR_UNSUPPORTED_DEVICE before anything is enqueued;
  * QK_ERR_CUDA if the launch fails.
  */
@@ -389,12 +395,19 @@ qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const
  * rows of the caches that some query of the call sees are used: rows between
  * the sinks and the first query's window, and rows past the last query, may
  * hold anything.  What a row holds, NaN and infinities included, reaches the
- * queries that see it and no other.  scale is finite, and scale * log2(e) *
- * q . k must stay within fp32.  Other arguments, limits and errors as in
+ * queries that see it and no other (an infinite value whose weight rounds to 0
+ * arrives as NaN; with scale 0, M >= 2, an infinite score is infinite still).
+ * Non-finite results are slow for M >= 2: each such row and head is computed
+ * again by one warp, so an infinite value that a whole chunk sees costs 100 to
+ * 1000 times the chunk's time (4095 queries, 24 heads, window 2048: 0.11 ms ->
+ * 39 ms).  scale is finite, and scale * log2(e) * q . k must stay within fp32
+ * for finite q and k.  Other arguments, limits and errors as in
  * qk_gqa_attention; out: [M][H][D] fp16, within about 2^-10 * max|v| of the
  * exact value plus its own rounding where a query sees 2^20 positions at most
- * (weights below 2^-25 of the largest of a warp's own share in decode, 2^-32 of
- * a query's in prefill, count in the sum alone).
+ * (in prefill weights down to 2^-32 of the largest count; decode as in
+ * qk_gqa_attention).  Finite values give finite results.  How a chunk's work is
+ * shared among CTAs follows M, so a query's last bits can differ between chunks
+ * of different sizes; the same call repeats its bits.
  */
 qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,
                                   uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,
@@ -416,8 +429,10 @@ qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache
  * (both NULL: not wanted), so do top_ids and top_logprobs (top_n = 0); entropy
  * may be NULL.  0 <= top_n <= 32 and top_n <= V; V below 2^31, M at most
  * 2^31 - 1.  Rows need not be 16-byte aligned (any V), the buffers do.  No
- * output may overlap another or an input.  M = 0 is a no-op; V = 0 is
- * QK_ERR_SHAPE.
+ * output may overlap another or an input.  How many CTAs share a row follows M
+ * and the device, so the last bits of its sums can differ between calls of
+ * different M; the same call repeats its bits, and the ids never differ.  M = 0
+ * is a no-op; V = 0 is QK_ERR_SHAPE.
  */
 qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob, float *entropy, int top_n,
                       int32_t *top_ids, float *top_logprobs, int64_t M, int64_t V, qk_stream_t stream);

@@ -38,7 +38,9 @@
 // max that moves only when the row max grows by more than 2^8, so O is rarely
 // rescaled.
 //
-// All waits are bounded; a timeout raises the device status word.
+// Waits on mbarriers are bounded; a timeout raises the device status word.  The
+// decode step's cluster barriers and the prefill's named barrier have no limit
+// of their own: every thread reaches them on every path, those that gave up too.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -837,8 +837,8 @@ __device__ void build_x_sums_q8(uint32_t xd, int K, uint32_t xq, uint32_t dt, in
 // rows of one half read together.  Q4_K: 4 rows of both halves, and where rows
 // are an even number of 16 bytes apart a lane takes the 16-byte pieces of its
 // 64 in the order i ^ mask, so that 8 lanes always read 8 different groups of
-// four banks.  (65536 x 4096, int8 x: 39.7 us; with 8 rows of one half together
-// in one order 58.3.)
+// four banks.  (65536 x 4096: 39.7 us when this came, with 8 rows of one half
+// together in one order 58.3; 35.5 now.)
 template <int QT>
 struct Q8Lane {
   int r, half, mask;
@@ -944,9 +944,9 @@ __device__ __forceinline__ void lds_words(uint32_t* w, uint32_t a, int n) {
 // kBytes = 16 where rows are aligned to it: the offset (2 b mod 16 for block b)
 // is then the same for the whole warp, the shift to its word a uniform branch,
 // and rows an odd number of 16 bytes apart share no bank (10 loads of 4
-// wavefronts; word by word each of 32 would take 4 or more).  128256 x 4096,
-// int8 x: 84 us, with words 142.  Rows that are not: kBytes = 4 (loads of 8 where
-// rows allow those were slower).
+// wavefronts; word by word each of 32 would take 4 or more).  128256 x 4096: 84
+// us when this came, with words 142; 79.9 now.  Rows that are not: kBytes = 4
+// (loads of 8 where rows allow those were slower).
 template <int kBytes>
 __device__ __forceinline__ void q6_words(uint32_t rb, int h, uint32_t (&A)[8], uint32_t (&B)[8], uint32_t (&H)[8],
                                          uint32_t (&S)[2], uint32_t& dw) {

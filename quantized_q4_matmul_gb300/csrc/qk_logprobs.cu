@@ -12,10 +12,10 @@
 //
 // HBM-bound for many rows: the row is read once, 8 independent 16-byte loads
 // per thread and batch.  1024 rows of 128256: 80 us without alternatives (6.5
-// TB/s), 94 us with 20 (5.6 TB/s): while one of an SM's two CTAs finds them, the
-// other's loads alone do not fill the memory's latency.  The alternatives cost almost nothing on the way: a
-// thread notes the maximum of every batch of 32 logits (a segment) that it
-// needs for the rescaling anyway.  Afterwards t0, the n-th largest of the maxima
+// TB/s), 95.3 us with 20 (5.5 TB/s): while one of an SM's two CTAs finds them,
+// the other's loads alone do not fill the memory's latency.  The alternatives
+// cost almost nothing on the way: a thread notes the maximum of every batch of
+// 32 logits (a segment) that it needs for the rescaling anyway.  Afterwards t0, the n-th largest of the maxima
 // of 64 groups of threads, is a lower bound of the n-th largest logit, so the
 // alternatives lie in the few segments whose maximum reaches it; only those
 // (about 1.2 n of 4008) are read again.
