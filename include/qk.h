@@ -325,6 +325,44 @@ qk_status qk_rope_kv_append(const float *q, const float *k, const float *v, cons
                             qk_stream_t stream);
 
 /*
+ * qk_rope_kv_append with an RMSNorm of every query and key head in front, for
+ * models that normalize them: a head's D values x become
+ *   x / sqrt(mean x^2 + eps) * gamma      (fp32; before the rotation)
+ * with q_gamma_f16 for the query heads and k_gamma_f16 for the key heads, fp16[D]
+ * each; where a gamma is NULL its heads are not normalized.  v never is.  eps is
+ * finite and >= 0, and x^2 must stay within fp32.  The rest as in
+ * qk_rope_kv_append; M is below 2^31.
+ * qk_norm_rope_kv_append_q4 writes the new rows into a cache held in 4 bits,
+ * k_q4 and v_q4 [H_kv][L_max][D / 2] bytes with k_dm and v_dm
+ * [H_kv][L_max][D / 32][2] fp16, D a multiple of 32.  Each 32 values x of a row
+ * are a group, held as v = d q + m:
+ *   m = fp16(min x),  d = fp16(max(max x - m, 0) / 15),
+ *   q = the nearest of 0 .. 15 to (x - m) / d (ties to even; 0 where d = 0),
+ * from the fp32 values and in fp32.  Byte j of a group has the q of value 2 j in
+ * its low and of 2 j + 1 in its high half; dm has d, then m.  |x| is at most
+ * 65000 (so that every v is a finite fp16); a group with a value that is not
+ * finite, or whose m or d is beyond fp16, is stored as NaN (d and m).
+ */
+qk_status qk_norm_rope_kv_append(const float *q, const float *k, const float *v, const uint16_t *q_gamma_f16,
+                                 const uint16_t *k_gamma_f16, float eps, const double *inv_freq, uint16_t *q_f16,
+                                 uint16_t *k_cache, uint16_t *v_cache, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                                 int64_t n_rot, int64_t pos0, int64_t L_max, int layout, float magnitude,
+                                 qk_stream_t stream);
+qk_status qk_norm_rope_kv_append_q4(const float *q, const float *k, const float *v, const uint16_t *q_gamma_f16,
+                                    const uint16_t *k_gamma_f16, float eps, const double *inv_freq, uint16_t *q_f16,
+                                    uint8_t *k_q4, uint16_t *k_dm, uint8_t *v_q4, uint16_t *v_dm, int64_t M, int64_t H,
+                                    int64_t H_kv, int64_t D, int64_t n_rot, int64_t pos0, int64_t L_max, int layout,
+                                    float magnitude, qk_stream_t stream);
+
+/*
+ * Rows pos0 .. pos0 + M - 1 of one tensor of a 4-bit cache as fp16:
+ * out_f16[g][r] = fp16(d q + m) (one rounding) of position pos0 + r, [H_kv][M][D].
+ * D is a multiple of 32, at most 512; pos0 + M <= L_max < 2^31; H_kv at most 1024.
+ */
+qk_status qk_dequant_kv_q4(const uint8_t *q4, const uint16_t *dm, uint16_t *out_f16, int64_t H_kv, int64_t D,
+                           int64_t pos0, int64_t M, int64_t L_max, qk_stream_t stream);
+
+/*
  * Host-only: the rotation frequencies, in radians per position, into
  * out[0 .. n_rot / 2 - 1] (host memory; the caller copies them to the device).
  *   f_i = theta^(-2 i / n_rot) / freq_factors[i]  (freq_factors NULL: 1),
@@ -412,6 +450,30 @@ qk_status qk_gqa_attention(const uint16_t *q_f16, const uint16_t *k_cache, const
 qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache, const uint16_t *v_cache,
                                   uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0,
                                   int64_t L_max, float scale, int64_t window, int64_t sinks, qk_stream_t stream);
+
+/*
+ * qk_gqa_attention_window over a cache held in 4 bits (the layout of
+ * qk_norm_rope_kv_append_q4; keys and values are fp16(d q + m), which must be
+ * finite or NaN).  Up to 32 columns, M * H / H_kv (a decode step, or a few
+ * drafted tokens), read the 4-bit rows directly: a cluster of up to 16 CTAs per
+ * key/value head splits them, and scratch may be NULL.  More tokens have the
+ * rows that their queries see written to `scratch` as fp16 first, a caller-owned
+ * device buffer of at least qk_gqa_attention_q4_scratch_bytes (512 bytes a
+ * position and key/value head); calls that may overlap on the GPU need a
+ * scratch each, captured graphs included.  The library cannot check its size.
+ * pos0 + M is below 2^30.  Window, sinks, rows that no query sees, other limits,
+ * accuracy, non-finite rows and errors as in qk_gqa_attention_window (weights
+ * below 2^-25 of the largest count in the sum alone for up to 32 columns, as in
+ * its decode).
+ */
+qk_status qk_gqa_attention_q4(const uint16_t *q_f16, const uint8_t *k_q4, const uint16_t *k_dm, const uint8_t *v_q4,
+                              const uint16_t *v_dm, uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                              int64_t pos0, int64_t L_max, float scale, int64_t window, int64_t sinks, void *scratch,
+                              qk_stream_t stream);
+
+/* Host-only query: bytes of scratch that such a call needs (0: none), or -1 for invalid arguments. */
+int64_t qk_gqa_attention_q4_scratch_bytes(int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0, int64_t window,
+                                          int64_t sinks);
 
 /*
  * Log probabilities from the LM head's logits (the pages' "[02] the pipeline",

@@ -25,7 +25,8 @@ __all__ = [
     "qk_gemm_plan_info", "qk_gqa_attention", "qk_gqa_attention_window", "qk_matmul_batch_q8", "qk_matmul_q8_desc",
     "qk_add_rmsnorm", "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_rope_config", "qk_logprobs",
     "QK_F16", "QK_F32", "QK_ROPE_INTERLEAVED", "QK_ROPE_HALF", "QK_ROPE_SCALE_NONE", "QK_ROPE_SCALE_LINEAR",
-    "QK_ROPE_SCALE_BANDED",
+    "QK_ROPE_SCALE_BANDED", "qk_norm_rope_kv_append", "qk_norm_rope_kv_append_q4", "qk_dequant_kv_q4",
+    "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +39,8 @@ SYMBOLS = ("qk_dequant_q4k", "qk_dequant_q6k", "qk_matmul_q4k", "qk_matmul_q6k",
            "qk_rmsnorm_matmul_q6k", "qk_rmsnorm_gateup_swiglu_q4k", "qk_rmsnorm_scratch_bytes",
     "qk_rmsnorm_matmul_batch_static", "qk_status_string",
            "qk_version", "qk_gqa_attention", "qk_gqa_attention_window", "qk_matmul_batch_q8", "qk_add_rmsnorm",
-           "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_logprobs")
+           "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_logprobs", "qk_norm_rope_kv_append",
+           "qk_norm_rope_kv_append_q4", "qk_dequant_kv_q4", "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes")
 
 QK_Q4_K, QK_Q6_K = 0, 1
 _QTYPES = {"q4k": QK_Q4_K, "q6k": QK_Q6_K}
@@ -140,6 +142,18 @@ def lib():
         L.qk_add_rmsnorm_q8.argtypes = [vp, i32, vp, vp, f32, vp, vp, vp, i64, i64, vp]
         L.qk_rope_kv_append.restype = i32
         L.qk_rope_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32, f32, vp]
+        L.qk_norm_rope_kv_append.restype = i32
+        L.qk_norm_rope_kv_append.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64,
+                                             i32, f32, vp]
+        L.qk_norm_rope_kv_append_q4.restype = i32
+        L.qk_norm_rope_kv_append_q4.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64,
+                                                i64, i64, i32, f32, vp]
+        L.qk_dequant_kv_q4.restype = i32
+        L.qk_dequant_kv_q4.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, vp]
+        L.qk_gqa_attention_q4.restype = i32
+        L.qk_gqa_attention_q4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, f32, i64, i64, vp, vp]
+        L.qk_gqa_attention_q4_scratch_bytes.restype = i64
+        L.qk_gqa_attention_q4_scratch_bytes.argtypes = [i64] * 7
         L.qk_rope_inv_freq.restype = i32
         L.qk_rope_inv_freq.argtypes = [ctypes.POINTER(qk_rope_config), i64, ctypes.POINTER(ctypes.c_double)]
         L.qk_logprobs.restype = i32
@@ -156,6 +170,7 @@ _F32 = ("torch.float32",)
 _F64 = ("torch.float64",)
 _I8 = ("torch.int8",)
 _I32 = ("torch.int32",)
+_U8 = ("torch.uint8",)
 
 
 _dtype_names = {}  # torch dtype -> its name: str() of a dtype takes longer than the lookup
@@ -423,6 +438,50 @@ def qk_rope_kv_append(q, k, v, inv_freq, q_f16, k_cache, v_cache, M: int, H: int
                                    _stream(stream)), "qk_rope_kv_append")
 
 
+def qk_norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_freq, q_f16, k_cache, v_cache, M: int,
+                           H: int, H_kv: int, D: int, n_rot: int, pos0: int, L_max: int,
+                           layout: int = QK_ROPE_INTERLEAVED, magnitude: float = 1.0, stream=None) -> None:
+    """qk_rope_kv_append with an RMSNorm of each query and key head in front (see
+    include/qk.h): gammas fp16 [D], or None for heads that are not normalized."""
+    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    cn = 2 * _size(H_kv, L_max, D)
+    w = "qk_norm_rope_kv_append: %s"
+    a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
+    _check(lib().qk_norm_rope_kv_append(*a, _buf(k_cache, cn, (w, "k_cache"), _F16), _buf(v_cache, cn, (w, "v_cache"), _F16),
+                                        M, H, H_kv, D, int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
+                                        _stream(stream)), "qk_norm_rope_kv_append")
+
+
+def _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot):
+    qn, kn = _size(M, H, D), _size(M, H_kv, D)
+    return (_buf(q, 4 * qn, (w, "q"), _F32), _buf(k, 4 * kn, (w, "k"), _F32), _buf(v, 4 * kn, (w, "v"), _F32),
+            _buf(q_gamma_f16, 2 * _n(D), (w, "q_gamma_f16"), _F16), _buf(k_gamma_f16, 2 * _n(D), (w, "k_gamma_f16"), _F16),
+            float(eps), _buf(inv_freq, 4 * _n(n_rot), (w, "inv_freq"), _F64), _buf(q_f16, 2 * qn, (w, "q_f16"), _F16))
+
+
+def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_freq, q_f16, k_q4, k_dm, v_q4, v_dm,
+                              M: int, H: int, H_kv: int, D: int, n_rot: int, pos0: int, L_max: int,
+                              layout: int = QK_ROPE_INTERLEAVED, magnitude: float = 1.0, stream=None) -> None:
+    """qk_norm_rope_kv_append into a cache held in 4 bits (see include/qk.h): k_q4, v_q4
+    uint8 [H_kv][L_max][D / 2], k_dm, v_dm fp16 [H_kv][L_max][D / 32][2]."""
+    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    cn = _size(H_kv, L_max, D)
+    w = "qk_norm_rope_kv_append_q4: %s"
+    a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
+    _check(lib().qk_norm_rope_kv_append_q4(*a, _buf(k_q4, cn // 2, (w, "k_q4"), _U8), _buf(k_dm, cn // 8, (w, "k_dm"), _F16),
+                                           _buf(v_q4, cn // 2, (w, "v_q4"), _U8), _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
+                                           M, H, H_kv, D, int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
+                                           _stream(stream)), "qk_norm_rope_kv_append_q4")
+
+
+def qk_dequant_kv_q4(q4, dm, out_f16, H_kv: int, D: int, pos0: int, M: int, L_max: int, stream=None) -> None:
+    """Rows pos0 .. pos0 + M - 1 of one tensor of a 4-bit cache as fp16 [H_kv][M][D] (see include/qk.h)."""
+    cn = _size(int(H_kv), int(L_max), int(D))
+    _check(lib().qk_dequant_kv_q4(_buf(q4, cn // 2, "qk_dequant_kv_q4: q4", _U8), _buf(dm, cn // 8, "qk_dequant_kv_q4: dm", _F16),
+                                  _buf(out_f16, 2 * _size(int(H_kv), int(M), int(D)), "qk_dequant_kv_q4: out_f16", _F16),
+                                  int(H_kv), int(D), int(pos0), int(M), int(L_max), _stream(stream)), "qk_dequant_kv_q4")
+
+
 def qk_rmsnorm_scratch_bytes(qtype, M: int, K: int, gateup: bool = False) -> int:
     """Scratch bytes an M-token problem needs under the RMSNorm entry points
     (0 when the GEMV fuses the norm); host only."""
@@ -553,6 +612,31 @@ def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_
                                          _buf(out_f16, 2 * qn, "qk_gqa_attention_window: out_f16", _F16), M, H, H_kv,
                                          D, int(pos0), L_max, float(scale), int(window), int(sinks),
                                          _stream(stream)), "qk_gqa_attention_window")
+
+
+def qk_gqa_attention_q4_scratch_bytes(M: int, H: int, H_kv: int, D: int, pos0: int, window: int, sinks: int = 0) -> int:
+    """Scratch bytes that qk_gqa_attention_q4 needs (0: none); host only."""
+    r = int(lib().qk_gqa_attention_q4_scratch_bytes(int(M), int(H), int(H_kv), int(D), int(pos0), int(window), int(sinks)))
+    if r < 0:
+        raise ValueError("qk_gqa_attention_q4_scratch_bytes: invalid sizes")
+    return r
+
+
+def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, H_kv: int, D: int, pos0: int, L_max: int,
+                        scale: float, window: int, sinks: int = 0, scratch=None, stream=None) -> None:
+    """qk_gqa_attention_window over a cache held in 4 bits (see include/qk.h); scratch:
+    qk_gqa_attention_q4_scratch_bytes of device memory where that is not 0."""
+    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    pos0, window, sinks = int(pos0), int(window), int(sinks)
+    qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
+    need = max(0, lib().qk_gqa_attention_q4_scratch_bytes(M, H, H_kv, D, pos0, window, sinks))
+    w = "qk_gqa_attention_q4: %s"
+    _check(lib().qk_gqa_attention_q4(_buf(q_f16, 2 * qn, (w, "q_f16"), _F16), _buf(k_q4, cn // 2, (w, "k_q4"), _U8),
+                                     _buf(k_dm, cn // 8, (w, "k_dm"), _F16), _buf(v_q4, cn // 2, (w, "v_q4"), _U8),
+                                     _buf(v_dm, cn // 8, (w, "v_dm"), _F16), _buf(out_f16, 2 * qn, (w, "out_f16"), _F16), M,
+                                     H, H_kv, D, pos0, L_max, float(scale), window, sinks,
+                                     _buf(scratch, need, (w, "scratch"), _F16 + _U8) if need else 0, _stream(stream)),
+           "qk_gqa_attention_q4")
 
 
 def qk_logprobs(logits, tokens, logprob, entropy, top_n: int, top_ids, top_logprobs, M: int, V: int,

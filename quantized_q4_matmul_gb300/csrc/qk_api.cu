@@ -649,6 +649,125 @@ qk_status qk_rope_kv_append(const float* q, const float* k, const float* v, cons
   return map_cuda(qk::launch_rope_kv(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// qk_norm_rope_kv_append (caches fp16) and qk_norm_rope_kv_append_q4 (c given).
+static qk_status norm_rope_kv_append(const float* q, const float* k, const float* v, const uint16_t* q_gamma,
+                                     const uint16_t* k_gamma, float eps, const double* inv_freq, uint16_t* q_f16,
+                                     uint16_t* k_cache, uint16_t* v_cache, const qk::Q4Cache* c, int64_t M, int64_t H,
+                                     int64_t H_kv, int64_t D, int64_t n_rot, int64_t pos0, int64_t L_max, int layout,
+                                     float magnitude, cudaStream_t s) {
+  if (M < 0 || M >= kMaxDim || H <= 0 || H_kv <= 0 || H > 1024 || H_kv > 1024 || D <= 0 || D > 512 ||
+      D % (c ? 32 : 8) != 0 || n_rot < 0 || n_rot > D || n_rot % 2 != 0 || pos0 < 0 || L_max <= 0 ||
+      L_max >= kMaxDim || M > L_max - pos0 || (layout != QK_ROPE_INTERLEAVED && layout != QK_ROPE_HALF) ||
+      !std::isfinite(magnitude) || !(eps >= 0.0f) || !std::isfinite(eps))
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  const int64_t qn = M * H * D, kn = M * H_kv * D, cn = H_kv * L_max * D;  // below 2^51
+  Span b[11];
+  int n = 0;
+  b[n++] = {q, 4 * qn, false};
+  b[n++] = {k, 4 * kn, false};
+  b[n++] = {v, 4 * kn, false};
+  b[n++] = {q_f16, 2 * qn, true};
+  if (c) {
+    b[n++] = {c->k_q4, cn / 2, true};
+    b[n++] = {c->k_dm, cn / 8, true};
+    b[n++] = {c->v_q4, cn / 2, true};
+    b[n++] = {c->v_dm, cn / 8, true};
+  } else {
+    b[n++] = {k_cache, 2 * cn, true};
+    b[n++] = {v_cache, 2 * cn, true};
+  }
+  if (q_gamma) b[n++] = {q_gamma, 2 * D, false};
+  if (k_gamma) b[n++] = {k_gamma, 2 * D, false};
+  if (n_rot > 0) b[n++] = {inv_freq, 4 * n_rot, false};
+  qk_status st = check_spans_host(b, n);
+  if (st == QK_OK) st = check_spans_device(b, n);
+  if (st != QK_OK) return st;
+  qk::NormRopeArgs a = {};
+  a.rope = qk::RopeArgs{q, k, v, inv_freq, q_f16, k_cache, v_cache, M, pos0, L_max, (int)H, (int)H_kv, (int)D,
+                        (int)n_rot, layout == QK_ROPE_HALF ? 1 : 0, magnitude};
+  a.q_gamma = q_gamma;
+  a.k_gamma = k_gamma;
+  a.eps = eps;
+  if (c) {
+    a.k_q4 = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(c->k_q4));
+    a.v_q4 = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(c->v_q4));
+    a.k_dm = reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(c->k_dm));
+    a.v_dm = reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(c->v_dm));
+  }
+  return map_cuda(qk::launch_norm_rope(a, s));
+}
+
+qk_status qk_norm_rope_kv_append(const float* q, const float* k, const float* v, const uint16_t* q_gamma_f16,
+                                 const uint16_t* k_gamma_f16, float eps, const double* inv_freq, uint16_t* q_f16,
+                                 uint16_t* k_cache, uint16_t* v_cache, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                                 int64_t n_rot, int64_t pos0, int64_t L_max, int layout, float magnitude,
+                                 qk_stream_t stream) {
+  return norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, k_cache, v_cache, nullptr, M, H,
+                             H_kv, D, n_rot, pos0, L_max, layout, magnitude, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qk_status qk_norm_rope_kv_append_q4(const float* q, const float* k, const float* v, const uint16_t* q_gamma_f16,
+                                    const uint16_t* k_gamma_f16, float eps, const double* inv_freq, uint16_t* q_f16,
+                                    uint8_t* k_q4, uint16_t* k_dm, uint8_t* v_q4, uint16_t* v_dm, int64_t M, int64_t H,
+                                    int64_t H_kv, int64_t D, int64_t n_rot, int64_t pos0, int64_t L_max, int layout,
+                                    float magnitude, qk_stream_t stream) {
+  const qk::Q4Cache c{k_q4, v_q4, k_dm, v_dm};
+  return norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, nullptr, nullptr, &c, M, H, H_kv,
+                             D, n_rot, pos0, L_max, layout, magnitude, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qk_status qk_dequant_kv_q4(const uint8_t* q4, const uint16_t* dm, uint16_t* out_f16, int64_t H_kv, int64_t D,
+                           int64_t pos0, int64_t M, int64_t L_max, qk_stream_t stream) {
+  if (M < 0 || H_kv <= 0 || H_kv > 1024 || D <= 0 || D > 512 || D % 32 != 0 || pos0 < 0 || L_max <= 0 ||
+      L_max >= kMaxDim || M > L_max - pos0)
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  const int64_t cn = H_kv * L_max * D;  // below 2^50
+  const Span b[3] = {{q4, cn / 2, false}, {dm, cn / 8, false}, {out_f16, 2 * H_kv * M * D, true}};
+  qk_status st = check_spans_host(b, 3);
+  if (st == QK_OK) st = check_spans_device(b, 3);
+  if (st != QK_OK) return st;
+  const qk::Q4Cache c{q4, nullptr, dm, nullptr};
+  // rows from pos0 on: nothing before them, and they lie pos0 further on
+  return map_cuda(qk::launch_dequant_kv_q4(c, out_f16, nullptr, (int)H_kv, (int)D, L_max, M, 0, pos0,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool attention_q4_shape(int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0, int64_t window,
+                               int64_t sinks) {
+  constexpr int64_t kMaxL = (int64_t)1 << 30;
+  return M >= 0 && M <= kMaxM && H > 0 && H <= 1024 && H_kv > 0 && H % H_kv == 0 && H / H_kv <= 8 && D == 128 &&
+         pos0 >= 0 && pos0 < kMaxL && pos0 + M < kMaxL && window >= 0 && sinks >= 0;
+}
+
+int64_t qk_gqa_attention_q4_scratch_bytes(int64_t M, int64_t H, int64_t H_kv, int64_t D, int64_t pos0, int64_t window,
+                                          int64_t sinks) {
+  if (!attention_q4_shape(M, H, H_kv, D, pos0, window, sinks)) return -1;
+  return qk::attn_q4_scratch(M, (int)H, (int)H_kv, pos0, window, sinks);
+}
+
+qk_status qk_gqa_attention_q4(const uint16_t* q_f16, const uint8_t* k_q4, const uint16_t* k_dm, const uint8_t* v_q4,
+                              const uint16_t* v_dm, uint16_t* out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D,
+                              int64_t pos0, int64_t L_max, float scale, int64_t window, int64_t sinks, void* scratch,
+                              qk_stream_t stream) {
+  if (!attention_q4_shape(M, H, H_kv, D, pos0, window, sinks) || L_max >= kMaxDim || M > L_max - pos0 ||
+      !std::isfinite(scale))
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  const int64_t q_bytes = M * H * D * 2, cn = H_kv * L_max * D;  // below 2^53
+  const int64_t scratch_bytes = qk::attn_q4_scratch(M, (int)H, (int)H_kv, pos0, window, sinks);
+  Span b[7] = {{q_f16, q_bytes, false}, {k_q4, cn / 2, false}, {k_dm, cn / 8, false},  {v_q4, cn / 2, false},
+               {v_dm, cn / 8, false},   {out_f16, q_bytes, true}, {scratch, scratch_bytes, true}};
+  const int n = scratch_bytes > 0 ? 7 : 6;
+  qk_status st = check_spans_host(b, n);
+  if (st == QK_OK) st = check_spans_device(b, n);
+  if (st != QK_OK) return st;
+  const qk::Q4Cache c{k_q4, v_q4, k_dm, v_dm};
+  return map_cuda(qk::launch_gqa_attention_q4(q_f16, c, out_f16, M, (int)H, (int)H_kv, pos0, L_max, scale, window, sinks,
+                                              scratch, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 qk_status qk_rope_inv_freq(const qk_rope_config* c, int64_t n_rot, double* out) {
   if (!c) return QK_ERR_NULL;
   if (n_rot < 0 || n_rot > 512 || n_rot % 2 != 0) return QK_ERR_SHAPE;

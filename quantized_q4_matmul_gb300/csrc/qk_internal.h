@@ -111,6 +111,18 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_kv(const RopeArgs& a, cudaStream_t s);
 
+// The same with an RMSNorm of each head in front (qk_norm_rope_kv_append; gammas
+// may be null) and, where k_q4 is set, the rows in 4 bits instead
+// (qk_norm_rope_kv_append_q4): 8 values a word of k_q4 / v_q4, (d, m) as two fp16
+// a word of k_dm / v_dm.  Arguments validated.
+struct NormRopeArgs {
+  RopeArgs rope;
+  const uint16_t *q_gamma, *k_gamma;
+  float eps;
+  uint32_t *k_q4, *v_q4, *k_dm, *v_dm;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
+
 // Log probabilities, entropy and top alternatives (qk_logprobs); arguments validated.
 struct LogprobArgs {
   const float* logits;
@@ -146,6 +158,23 @@ cudaError_t launch_gqa_attention_window(const uint16_t* q, const uint16_t* kc, c
                                         int64_t M, int H, int Hkv, int64_t pos0, int64_t Lmax, float scale,
                                         int64_t window, int64_t sinks, cudaStream_t s);
 uint32_t attn_take_status();
+
+// The 4-bit cache: rows of D values as D / 2 bytes (q4) and D / 32 pairs of fp16
+// (dm), [H_kv][Lmax] of them.  Arguments validated.
+struct Q4Cache {
+  const uint8_t *k_q4, *v_q4;
+  const uint16_t *k_dm, *v_dm;
+};
+// fp16 rows out[g][r] of `count` tensors (1 or 2): row r is position r where r <
+// sinks, else r + gap.
+cudaError_t launch_dequant_kv_q4(const Q4Cache& c, uint16_t* k_out, uint16_t* v_out, int Hkv, int D, int64_t Lmax,
+                                 int64_t rows, int64_t sinks, int64_t gap, cudaStream_t s);
+// qk_gqa_attention_q4: few tokens by the decode kernel, others through the
+// scratch (attn_q4_scratch bytes).
+int64_t attn_q4_scratch(int64_t M, int H, int Hkv, int64_t pos0, int64_t window, int64_t sinks);
+cudaError_t launch_gqa_attention_q4(const uint16_t* q, const Q4Cache& c, uint16_t* out, int64_t M, int H, int Hkv,
+                                    int64_t pos0, int64_t Lmax, float scale, int64_t window, int64_t sinks,
+                                    void* scratch, cudaStream_t s);
 uint32_t attn_win_take_status();
 
 // A kernel whose single bounded wait can never complete (see qk_debug_wait_timeout).

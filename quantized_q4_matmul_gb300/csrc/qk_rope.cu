@@ -23,6 +23,7 @@
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
+#include "qk_rope.cuh"
 
 namespace qk {
 
@@ -30,16 +31,6 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 256;  // D <= 512
-
-// Sine and cosine of every pair of the token at position p, times the magnitude.
-__device__ __forceinline__ void fill_table(const RopeArgs& A, int64_t p, float2* cs) {
-  for (int j = threadIdx.x; j < A.n_rot / 2; j += kRopeThreads) {
-    const double t = (double)p * A.inv_freq[j] * 0.15915494309189533577;  // turns
-    float s, c;
-    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
-    cs[j] = make_float2(c * A.magnitude, s * A.magnitude);
-  }
-}
 
 // Where head `hd` of the q heads, k heads and v heads of token i (position p)
 // comes from and goes to; the return value says whether it turns.
@@ -90,7 +81,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
       }
     }
     if (!ready) {
-      fill_table(A, p, cs);
+      fill_table(A, p, cs, kRopeThreads);
       __syncthreads();
       ready = true;
     }
@@ -140,7 +131,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_any_kernel(const __grid_
   __shared__ float2 cs[kRopeMaxPairs];
   const int64_t i = blockIdx.x, p = A.pos0 + i;
   dependent_wait();
-  fill_table(A, p, cs);
+  fill_table(A, p, cs, kRopeThreads);
   __syncthreads();
   const int n4 = A.D / 4, items = (A.H + 2 * A.Hkv) * n4, h = A.n_rot / 2;
   for (int w = blockIdx.y * kRopeThreads + threadIdx.x; w < items; w += gridDim.y * kRopeThreads) {
