@@ -500,6 +500,35 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
                       int32_t *top_ids, float *top_logprobs, int64_t M, int64_t V, qk_stream_t stream);
 
 /*
+ * A token from each row of logits fp32 [M][V] (the pages' "[02] the pipeline",
+ * compartment 07: the sampler) and a given uniform random number u[m] in 0 .. 1.
+ * With a row's tokens in descending order of their logits x (equal ones by the
+ * lower token; -inf, banned tokens, never count), w = exp((x - max x) / temperature)
+ * and C(n) the sum of the first n weights, the kept tokens are the first n, the
+ * least of
+ *   top_k (0: all of them),
+ *   the first n with C(n) >= top_p C(top_k)   (top_p 1: all),
+ *   the number of tokens with w >= min_p      (min_p 0: all),
+ * and
+ *   token[m]   = the first in that order whose C exceeds u[m] C(n),
+ *   logprob[m] = log of its share w / C(n) of the kept weights (may be NULL),
+ *   kept[m]    = n (may be NULL).
+ * temperature 0 gives the first token in the order, a logprob of 0 and kept 1.  A
+ * row that holds NaN or +inf, or nothing but -inf, gives token -1, a NaN logprob
+ * and kept 0.  u below 0 or NaN counts as 0, u of 1 or more as the largest fp32
+ * number below 1.  The sums are exact to about 2^-40 of the largest weight a
+ * token (weights below 2^-45 of the largest count as 0 in them), so that a token
+ * follows from the definition rather than from the order of a sum; the same call
+ * repeats its bits, whatever M.  temperature is 0 or 1e-6 .. 1e6, top_p 0 .. 1, min_p
+ * 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need not be 16-byte aligned
+ * (any V), the buffers do.  No output may overlap another or an input.  Thousands
+ * of equal logits around the last kept token, or around the chosen one, make a
+ * row slow (0.1 to 1 ms).  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
+ */
+qk_status qk_sample(const float *logits, const float *u, int32_t *token, float *logprob, int32_t *kept, int64_t M,
+                    int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream);
+
+/*
  * Synchronise `stream`, then report and clear the device-side status flags
  * that the library's kernels set when a bounded wait expires.  Returns QK_OK,
  * QK_ERR_TIMEOUT, or QK_ERR_CUDA if the synchronisation itself failed.  A

@@ -26,7 +26,7 @@ __all__ = [
     "qk_add_rmsnorm", "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_rope_config", "qk_logprobs",
     "QK_F16", "QK_F32", "QK_ROPE_INTERLEAVED", "QK_ROPE_HALF", "QK_ROPE_SCALE_NONE", "QK_ROPE_SCALE_LINEAR",
     "QK_ROPE_SCALE_BANDED", "qk_norm_rope_kv_append", "qk_norm_rope_kv_append_q4", "qk_dequant_kv_q4",
-    "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes",
+    "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes", "qk_sample",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +40,8 @@ SYMBOLS = ("qk_dequant_q4k", "qk_dequant_q6k", "qk_matmul_q4k", "qk_matmul_q6k",
     "qk_rmsnorm_matmul_batch_static", "qk_status_string",
            "qk_version", "qk_gqa_attention", "qk_gqa_attention_window", "qk_matmul_batch_q8", "qk_add_rmsnorm",
            "qk_add_rmsnorm_q8", "qk_rope_kv_append", "qk_rope_inv_freq", "qk_logprobs", "qk_norm_rope_kv_append",
-           "qk_norm_rope_kv_append_q4", "qk_dequant_kv_q4", "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes")
+           "qk_norm_rope_kv_append_q4", "qk_dequant_kv_q4", "qk_gqa_attention_q4", "qk_gqa_attention_q4_scratch_bytes",
+           "qk_sample")
 
 QK_Q4_K, QK_Q6_K = 0, 1
 _QTYPES = {"q4k": QK_Q4_K, "q6k": QK_Q6_K}
@@ -158,6 +159,8 @@ def lib():
         L.qk_rope_inv_freq.argtypes = [ctypes.POINTER(qk_rope_config), i64, ctypes.POINTER(ctypes.c_double)]
         L.qk_logprobs.restype = i32
         L.qk_logprobs.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, vp]
+        L.qk_sample.restype = i32
+        L.qk_sample.argtypes = [vp, vp, vp, vp, vp, i64, i64, f32, i32, f32, f32, vp]
         L.qk_status_string.restype, L.qk_status_string.argtypes = ctypes.c_char_p, [i32]
         L.qk_version.restype, L.qk_version.argtypes = i32, []
         _lib = L
@@ -653,6 +656,17 @@ def qk_logprobs(logits, tokens, logprob, entropy, top_n: int, top_ids, top_logpr
                              _buf(top_ids, m * _n(top_n), "qk_logprobs: top_ids", _I32),
                              _buf(top_logprobs, m * _n(top_n), "qk_logprobs: top_logprobs", _F32), int(M), int(V),
                              _stream(stream)), "qk_logprobs")
+
+
+def qk_sample(logits, u, token, logprob, kept, M: int, V: int, temperature: float = 1.0, top_k: int = 0,
+              top_p: float = 1.0, min_p: float = 0.0, stream=None) -> None:
+    """A token from each row of logits fp32 [M][V] and a given random number u fp32 [M]
+    (see include/qk.h): token int32 [M], logprob fp32 [M] and kept int32 [M] or None."""
+    m = 4 * _n(M)
+    _check(lib().qk_sample(_buf(logits, m * _n(V), "qk_sample: logits", _F32), _buf(u, m, "qk_sample: u", _F32),
+                           _buf(token, m, "qk_sample: token", _I32), _buf(logprob, m, "qk_sample: logprob", _F32),
+                           _buf(kept, m, "qk_sample: kept", _I32), int(M), int(V), float(temperature), int(top_k),
+                           float(top_p), float(min_p), _stream(stream)), "qk_sample")
 
 
 def qk_get_device_status(stream=None) -> None:

@@ -824,6 +824,23 @@ qk_status qk_logprobs(const float* logits, const int32_t* tokens, float* logprob
   return map_cuda(qk::launch_logprobs(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+qk_status qk_sample(const float* logits, const float* u, int32_t* token, float* logprob, int32_t* kept, int64_t M,
+                    int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream) {
+  if (M < 0 || M >= kMaxDim || V <= 0 || V > ((int64_t)1 << 19) || top_k < 0 || !(top_p >= 0.f && top_p <= 1.f) ||
+      !(min_p == 0.f || (min_p >= 1e-12f && min_p <= 1.f)) || !(temperature == 0.f || (temperature >= 1e-6f && temperature <= 1e6f)))
+    return QK_ERR_SHAPE;
+  if (M == 0) return QK_OK;
+  Span b[5] = {{logits, 4 * M * V, false}, {u, 4 * M, false}, {token, 4 * M, true}};  // below 2^53
+  int c = 3;
+  if (logprob) b[c++] = {logprob, 4 * M, true};
+  if (kept) b[c++] = {kept, 4 * M, true};
+  qk_status st = check_spans_host(b, c);
+  if (st == QK_OK) st = check_spans_device(b, c);
+  if (st != QK_OK) return st;
+  const qk::SampleArgs a{logits, u, token, logprob, kept, M, (int)V, top_k, temperature, top_p, min_p};
+  return map_cuda(qk::launch_sample(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 qk_status qk_get_device_status(qk_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QK_ERR_CUDA;
   const uint32_t v =

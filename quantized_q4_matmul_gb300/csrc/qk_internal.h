@@ -134,6 +134,18 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
 
+// A token from each row of logits (qk_sample); arguments validated.
+struct SampleArgs {
+  const float *logits, *u;
+  int32_t* token;
+  float* logprob;
+  int32_t* kept;
+  int64_t M;
+  int V, top_k;
+  float temperature, top_p, min_p;
+};
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
 // The built-in scratch of qk_rmsnorm_matmul_batch_static (bytes) and its
 // device address on the current device (looked up once per device).
 constexpr size_t kStaticScratchBytes = size_t(8) << 20;
