@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int64_t row = q0 + t * A.queries + r / G;  // this row's query
     const int64_t p = A.pos0 + row;
     const float scale = A.scale_log2e;
-    const bool neg = scale < 0.f;
+    const bool neg = scale < 0.f, query = r < G * A.queries;
     float m = -INFINITY;
     uint64_t l2 = 0, l3 = 0;  // the row's sum, as four partial sums (short chains)
     bool ok = true;
@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       // 2^-32 of the largest or less, where it dropped 2^-25, of which 2^17
       // positions hold 2^-8 of the sum.  A row that has seen nothing yet keeps
       // m = -inf, and its weights, all 0, are taken relative to 0.
-      const bool upd = (m == -INFINITY && tmax != -INFINITY) || tmax > m + 15.0f;
+      // Rows past the tile's queries hold what was in shared memory: they update
+      // nothing, as an update adds up the other rows' sums in another order.
+      const bool upd = query && ((m == -INFINITY && tmax != -INFINITY) || tmax > m + 15.0f);
       const float mn = upd ? tmax - 7.0f : m;
       const float corr = upd ? exp2f(m - mn) : 1.0f;
       m = mn;
