@@ -339,9 +339,9 @@ qk_status qk_rope_kv_append(const float *q, const float *k, const float *v, cons
  *   m = fp16(min x),  d = fp16(max(max x - m, 0) / 15),
  *   q = the nearest of 0 .. 15 to (x - m) / d (ties to even; 0 where d = 0),
  * from the fp32 values and in fp32.  Byte j of a group has the q of value 2 j in
- * its low and of 2 j + 1 in its high half; dm has d, then m.  |x| is at most
- * 65000 (so that every v is a finite fp16); a group with a value that is not
- * finite, or whose m or d is beyond fp16, is stored as NaN (d and m).
+ * its low and of 2 j + 1 in its high half; dm has d, then m.  A group with a value
+ * that is not finite or beyond fp16, or whose values lie more than about 65000
+ * apart (15 d is a finite fp16 number), is stored as NaN (d and m).
  */
 qk_status qk_norm_rope_kv_append(const float *q, const float *k, const float *v, const uint16_t *q_gamma_f16,
                                  const uint16_t *k_gamma_f16, float eps, const double *inv_freq, uint16_t *q_f16,
@@ -453,18 +453,19 @@ qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache
 
 /*
  * qk_gqa_attention_window over a cache held in 4 bits (the layout of
- * qk_norm_rope_kv_append_q4; keys and values are fp16(d q + m), which must be
- * finite or NaN).  Up to 32 columns, M * H / H_kv (a decode step, or a few
- * drafted tokens), read the 4-bit rows directly: a cluster of up to 16 CTAs per
- * key/value head splits them, and scratch may be NULL.  More tokens have the
- * rows that their queries see written to `scratch` as fp16 first, a caller-owned
- * device buffer of at least qk_gqa_attention_q4_scratch_bytes (512 bytes a
- * position and key/value head); calls that may overlap on the GPU need a
- * scratch each, captured graphs included.  The library cannot check its size.
- * pos0 + M is below 2^30.  Window, sinks, rows that no query sees, other limits,
- * accuracy, non-finite rows and errors as in qk_gqa_attention_window (weights
- * below 2^-25 of the largest count in the sum alone for up to 32 columns, as in
- * its decode).
+ * qk_norm_rope_kv_append_q4; d q + m and 15 d must be finite fp16 numbers, or d
+ * or m NaN).  Up to 32 columns, M * H / H_kv (a decode step, or a few drafted
+ * tokens), read the 4-bit rows directly: over a cluster of CTAs per key/value
+ * head, or, from 32768 positions of all key/value heads on, over all SMs, joined
+ * by a second kernel through `scratch`.  More tokens have the rows that their
+ * queries see written to `scratch` as fp16 first (512 bytes a position and
+ * key/value head).  scratch is a caller-owned device buffer of at least
+ * qk_gqa_attention_q4_scratch_bytes, NULL where that is 0; what it holds before
+ * and after is of no account.  Calls that may overlap on the GPU need a scratch
+ * each, captured graphs included.  The library cannot check its size.  pos0 + M
+ * is below 2^30.  Window, sinks, rows that no query sees, other limits, accuracy,
+ * non-finite rows (not slow for few tokens) and errors as in
+ * qk_gqa_attention_window.
  */
 qk_status qk_gqa_attention_q4(const uint16_t *q_f16, const uint8_t *k_q4, const uint16_t *k_dm, const uint8_t *v_q4,
                               const uint16_t *v_dm, uint16_t *out_f16, int64_t M, int64_t H, int64_t H_kv, int64_t D,

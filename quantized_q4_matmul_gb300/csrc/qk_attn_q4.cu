@@ -11,10 +11,10 @@
 //
 // Few tokens (a decode step, or drafted tokens: M * H / H_kv <= 32 columns, a
 // column being a query head of one token).  A cluster of up to 16 CTAs per
-// key/value head splits the visible positions; a warp takes 16 of them at a time,
-// straight from global memory into registers (a lane has one whole group of 32
-// key and value quants of a position, 16 bytes, so a warp's load is 512
-// contiguous bytes), with the next 16 on their way.  mma.sync, whose 8-wide N side
+// key/value head splits the visible positions; a warp takes 16 of them at a time
+// through a ring of its own in shared memory (a lane has one whole group of 32
+// key and value quants of a position, 16 bytes), three more 16s on their way.
+// mma.sync, whose 8-wide N side
 // holds the columns, multiplies:
 //   S^T = K Q^T  (16 positions x 8 columns): the product's k axis is permuted to
 //     what the lanes hold, so nothing is exchanged;
@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <atomic>
 
 #include "qk_attn.cuh"
@@ -47,23 +48,38 @@ namespace {
 
 constexpr int kQMaxCluster = 16;
 constexpr int kQMaxCols = 32;
+constexpr int kQMaxSplit = 160;   // CTAs of a call that join through the scratch
+constexpr int64_t kQSplitFrom = 8 * 4096;  // positions of all key/value heads from which they do
 constexpr int kUnit = 16;  // positions of a warp's step
 
-// The shape of a CTA for NT tiles of 8 columns.
-template <int NT>
+// The shape of a CTA for NT tiles of 8 columns and W warps.
+template <int NT, int W>
 struct Q4Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;  // registers for the columns' O
+  static constexpr int kWarps = W;
   static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kPerSm = NT == 1 ? 16 / W : 1;  // CTAs of an SM: registers for the columns' O
   static constexpr int kCols = 8 * NT;
+  static constexpr bool kSharedQ = NT > 2;
 };
 
-template <int NT>
+// 16 rows of one key/value head.
+struct Q4Stage {
+  uint4 k[64], v[64];  // lane l copies and reads chunks l and l + 32: group l % 4 of rows l / 4 and l / 4 + 8
+  uint4 ks[16], vs[16];
+};
+constexpr int kStages = 4;  // 16s in flight or in use for each warp
+
+template <int NT, int W>
 struct Q4Shared {
-  using Sh = Q4Shape<NT>;
-  float part[Sh::kWarps][Sh::kCols * kD];  // the warps' O
+  using Sh = Q4Shape<NT, W>;
+  union {
+    Q4Stage ring[kStages];
+    float part[Sh::kCols * kD];  // after its last rows: the warp's O
+  } warp[Sh::kWarps];
   float red[kQMaxCluster * 4 + Sh::kCols * kD];  // what the CTAs send: [rank][this CTA's share of the outputs]
   float2 stat[kQMaxCluster][Sh::kCols];    // and their (max, sum)
   float wmax[Sh::kWarps][Sh::kCols], wsum[Sh::kWarps][Sh::kCols];
+  uint2 q[Sh::kSharedQ ? 8 * NT : 1][32];  // Q's fragments, where registers do not hold them
 };
 
 struct Q4Args {
@@ -75,23 +91,52 @@ struct Q4Args {
   int64_t pos0, Lmax, window, sinks;
   int64_t sink_rows, gap, total;  // visible position u is u, or u + gap from sink_rows on: `total` of them
   float scale_log2e;
-  int C;
+  int C;         // CTAs that share a key/value head: a cluster, or, with `part`, any number
+  float* part;   // [H_kv][columns][C] partial O of 128, and after them their (max, sum)
 };
-
-// The nibbles of a word as four pairs of fp16 (nibble i of the low half and of
-// the high half), exact.
-__device__ __forceinline__ void unpack_pairs(uint32_t w, __half2 (&q)[4]) {
-  const uint32_t k1024 = 0x64006400u, k64 = 0x54005400u;
-  const __half2 o1024 = *reinterpret_cast<const __half2*>(&k1024), o64 = *reinterpret_cast<const __half2*>(&k64);
-  const uint32_t h = w >> 8;
-  const uint32_t u[4] = {lop_and_or<0x000f000fu>(w, k1024), lop_and_or<0x00f000f0u>(w, k64),
-                         lop_and_or<0x000f000fu>(h, k1024), lop_and_or<0x00f000f0u>(h, k64)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __hsub2(*reinterpret_cast<const __half2*>(&u[i]), i & 1 ? o64 : o1024);
-}
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// The nibbles of a word as four pairs of fp16 (nibble i of the low half and of
+// the high half) with the exponent of 2^10, 1024 + q, or, 4 bits higher, of 2^6, 64 + q.
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&u)[4]) {
+  const uint32_t h = w >> 8;
+  u[0] = lop_and_or<0x000f000fu>(w, 0x64006400u);
+  u[1] = lop_and_or<0x00f000f0u>(w, 0x54005400u);
+  u[2] = lop_and_or<0x000f000fu>(h, 0x64006400u);
+  u[3] = lop_and_or<0x00f000f0u>(h, 0x54005400u);
+}
+
+// The same without the offsets, exact.
+__device__ __forceinline__ void unpack_pairs(uint32_t w, __half2 (&q)[4]) {
+  uint32_t u[4];
+  spread(w, u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = __hsub2(as_h2(u[i]), as_h2(i & 1 ? 0x54005400u : 0x64006400u));
+}
+
+// fp16(d q) of a word's nibbles, one rounding each.  Where |d| < 60 the offsets
+// go with the product, d (1024 + q) - 1024 d, whose last term is exact.
+struct Scaled {
+  __half2 d, c1024, c64;
+  __device__ __forceinline__ explicit Scaled(uint32_t pair)
+      : d(as_h2(pair)), c1024(__hmul2(as_h2(pair), as_h2(0xE400E400u))), c64(__hmul2(as_h2(pair), as_h2(0xD400D400u))) {}
+  template <bool kWide>
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&v)[4]) const {
+    if (kWide) {
+      __half2 q[4];
+      unpack_pairs(w, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hmul2(q[i], d));
+    } else {
+      spread(w, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hfma2(as_h2(v[i]), d, i & 1 ? c64 : c1024));
+    }
+  }
+};
+constexpr uint32_t kWideD = 0x5380u;  // 60 as fp16
 
 // Transposes an 8 x 8 matrix of 16-bit values: lane 4 r + c holds row r, columns 2 c and 2 c + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -108,55 +153,67 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// A lane's part of 16 rows: group lane % 4 of rows lane / 4 and lane / 4 + 8.
-struct Q4Unit {
-  uint4 k[2], v[2];
-  uint32_t ks[2], vs[2];
-};
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Up to 8 NT columns against the visible positions of one key/value head.  Rank r
 // of the cluster takes visible positions [r n / C, (r + 1) n / C) in multiples of
 // 16, its warps every kWarps-th 16 of them.  kMulti: more than one token, so that
 // columns see different positions.
-template <int NT, bool kMulti>
-__global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kernel(const __grid_constant__ Q4Args A) {
-  using Sh = Q4Shape<NT>;
+template <int NT, int W, bool kMulti>
+__global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPerSm)
+    attn_q4_decode_kernel(const __grid_constant__ Q4Args A) {
+  using Sh = Q4Shape<NT, W>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Q4Shared<NT>& S = *reinterpret_cast<Q4Shared<NT>*>(smem_raw);
+  Q4Shared<NT, W>& S = *reinterpret_cast<Q4Shared<NT, W>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 2, tq = lane & 3;
   const int g = blockIdx.y;
-  const int rank = (int)cluster_rank();
+  const int rank = (int)blockIdx.x;
   const int units = (int)((A.total + kUnit - 1) / kUnit);
   const int unit1 = (int)((int64_t)(rank + 1) * units / A.C);
   int unit = (int)((int64_t)rank * units / A.C) + warp;
-  const int total = (int)A.total, sink_rows = (int)A.sink_rows, gap = (int)A.gap;
+  const int total = (int)A.total, sink_rows = (int)A.sink_rows, gap = (int)A.gap, last_p = (int)A.pos0 + A.M - 1;
   const uint4 *kq = A.k_q4 + (int64_t)g * A.Lmax * 4 + tq, *vq = A.v_q4 + (int64_t)g * A.Lmax * 4 + tq;
-  const uint32_t *kd = A.k_dm + (int64_t)g * A.Lmax * 4 + tq, *vd = A.v_dm + (int64_t)g * A.Lmax * 4 + tq;
+  const uint4* dm = reinterpret_cast<const uint4*>(lane < 16 ? A.k_dm : A.v_dm) + (int64_t)g * A.Lmax;
+  auto& ring = S.warp[warp].ring;
   __syncwarp();
-  cluster_arrive();  // its wait is before the first write to another CTA
+  if (!A.part) cluster_arrive();  // its wait is before the first write to another CTA
   dependent_wait();
 
-  auto load = [&](int at, Q4Unit& x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int u = min(kUnit * at + grp + 8 * i, total - 1);  // past the end: the last row again
-      const int64_t j = 4 * (int64_t)(u < sink_rows ? u : u + gap);
-      x.k[i] = ldg_stream16(kq + j);
-      x.ks[i] = ldg_stream4(kd + j);
-      x.v[i] = ldg_stream16(vq + j);
-      x.vs[i] = ldg_stream4(vd + j);
-    }
+  // Rows past the last visible one are copies of it.
+  auto position = [&](int u) -> int64_t {
+    u = min(u, total - 1);
+    return u < sink_rows ? u : u + gap;
   };
-  Q4Unit x;
-  if (unit < unit1) load(unit, x);
+  auto fetch = [&](int at, int stage) {
+    if (at < unit1) {
+      Q4Stage& R = ring[stage];
+      const int64_t j0 = 4 * position(kUnit * at + grp), j1 = 4 * position(kUnit * at + grp + 8);
+      copy16(&R.k[lane], kq + j0);
+      copy16(&R.k[lane + 32], kq + j1);
+      copy16((lane < 16 ? R.ks : R.vs) + (lane & 15), dm + position(kUnit * at + (lane & 15)));
+      copy16(&R.v[lane], vq + j0);
+      copy16(&R.v[lane + 32], vq + j1);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(unit + i * Sh::kWarps, i);
 
   // Q: the product's k axis in step (word j, half h) is dims 32 tq + 8 j + 2 h and + 4
   // (first register), and those + 1 (second), of this lane's tq.
-  uint32_t qb[NT][4][2][2];
+  uint2 qb[NT][4][2];
   int cpos[NT][2];    // the positions of this lane's columns
   float o[NT][8][4];  // [column tile][2 j + h]: dims 32 (grp / 2) + 8 j + 4 (grp % 2) + 2 h (+ 1: elements 2, 3), columns 2 tq (+ 1)
-  float m[NT][2], l[NT][2];
+  float om[NT][4];    // elements 0, 1: what their group's m adds to all of these; 2, 3: the columns' sums of weights
+  float m[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int col = 8 * n + grp;
@@ -165,16 +222,21 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint4 y = col < A.M * A.G ? qr[j] : make_uint4(0u, 0u, 0u, 0u);
-      qb[n][j][0][0] = prmt(y.x, y.z, 0x5410);
-      qb[n][j][0][1] = prmt(y.x, y.z, 0x7632);
-      qb[n][j][1][0] = prmt(y.y, y.w, 0x5410);
-      qb[n][j][1][1] = prmt(y.y, y.w, 0x7632);
+      const uint2 b0 = make_uint2(prmt(y.x, y.z, 0x5410), prmt(y.x, y.z, 0x7632));
+      const uint2 b1 = make_uint2(prmt(y.y, y.w, 0x5410), prmt(y.y, y.w, 0x7632));
+      if (!Sh::kSharedQ) {
+        qb[n][j][0] = b0;
+        qb[n][j][1] = b1;
+      } else if (warp == 0) {
+        S.q[8 * n + 2 * j][lane] = b0;
+        S.q[8 * n + 2 * j + 1][lane] = b1;
+      }
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       cpos[n][e] = (int)A.pos0 + (kMulti ? min((8 * n + 2 * tq + e) / A.G, A.M - 1) : 0);
       m[n][e] = -INFINITY;
-      l[n][e] = 0.f;
+      om[n][e] = om[n][e + 2] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -182,20 +244,28 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
       for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
   }
 
-  for (; unit < unit1; unit += Sh::kWarps) {
+  if (Sh::kSharedQ) __syncthreads();
+  for (int stage = 0; unit < unit1; unit += Sh::kWarps, stage = stage + 1 == kStages ? 0 : stage + 1) {
+    copy_wait<kStages - 2>();
+    __syncwarp();  // the scales are other lanes' copies; and all lanes are done with the stage before
+    fetch(unit + (kStages - 1) * Sh::kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    const Q4Stage& R = ring[stage];
+    const uint4 k0 = R.k[lane], k1 = R.k[lane + 32], v0 = R.v[lane], v1 = R.v[lane + 32];
+    const uint32_t* sk = reinterpret_cast<const uint32_t*>(R.ks) + lane;
+    const uint32_t* sv = reinterpret_cast<const uint32_t*>(R.vs) + lane;
+    const uint32_t ks0 = sk[0], ks1 = sk[32], vs0 = sv[0], vs1 = sv[32];
     const int u = kUnit * unit, rows = total - u;  // rows past them are copies
-    Q4Unit next = x;
-    if (unit + Sh::kWarps < unit1) load(unit + Sh::kWarps, next);
     // ---- scores: rows grp and grp + 8, this lane's group of the dimensions
     float sc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
     {
-      const __half2 d0 = as_h2(prmt(x.ks[0], x.ks[0], 0x1010)), m0 = as_h2(prmt(x.ks[0], x.ks[0], 0x3232));
-      const __half2 d1 = as_h2(prmt(x.ks[1], x.ks[1], 0x1010)), m1 = as_h2(prmt(x.ks[1], x.ks[1], 0x3232));
-      const uint32_t a0[4] = {x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w}, a1[4] = {x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w};
+      float part[NT][2][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[n][0][e] = part[n][1][e] = 0.f;
+      const __half2 d0 = as_h2(prmt(ks0, ks0, 0x1010)), m0 = as_h2(prmt(ks0, ks0, 0x3232));
+      const __half2 d1 = as_h2(prmt(ks1, ks1, 0x1010)), m1 = as_h2(prmt(ks1, ks1, 0x3232));
+      const uint32_t a0[4] = {k0.x, k0.y, k0.z, k0.w}, a1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         __half2 p0[4], p1[4];
@@ -206,133 +276,156 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
           const uint32_t a[4] = {as_u32(__hfma2(p0[2 * h], d0, m0)), as_u32(__hfma2(p1[2 * h], d1, m1)),
                                  as_u32(__hfma2(p0[2 * h + 1], d0, m0)), as_u32(__hfma2(p1[2 * h + 1], d1, m1))};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(sc[n], a, qb[n][j][h][0], qb[n][j][h][1]);
-        }
-      }
-    }
-    // ---- weights
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float tmax[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {  // e: column e & 1, row grp + 8 (e >> 1)
-        const int r = grp + 8 * (e >> 1);
-        bool seen = r < rows;
-        if (kMulti) {
-          const int j = u + r + (u + r < sink_rows ? 0 : gap), p = cpos[n][e & 1];
-          seen = seen && j <= p && (p - j < A.window || j < A.sinks);
-        }
-        const float v = seen ? sc[n][e] * A.scale_log2e : -INFINITY;
-        sc[n][e] = v;
-        tmax[e & 1] = fmaxf(tmax[e & 1], v);
-      }
-      bool grows = false;
-      float mn[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        tmax[e] = fmaxf(tmax[e], __shfl_xor_sync(0xffffffffu, tmax[e], 4));
-        tmax[e] = fmaxf(tmax[e], __shfl_xor_sync(0xffffffffu, tmax[e], 8));
-        tmax[e] = fmaxf(tmax[e], __shfl_xor_sync(0xffffffffu, tmax[e], 16));
-        mn[e] = fmaxf(m[n][e], tmax[e]);
-        grows = grows || mn[e] > m[n][e];
-      }
-      if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float corr = mn[e] == -INFINITY ? 1.f : ex2_approx(m[n][e] - mn[e]);
-          m[n][e] = mn[e];
-          l[n][e] *= corr;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[n][i][e] *= corr;
-            o[n][i][e + 2] *= corr;
+          for (int n = 0; n < NT; ++n) {
+            const uint2 b = Sh::kSharedQ ? S.q[8 * n + 2 * j + h][lane] : qb[n][j][h];
+            mma16816(part[n][h], a, b.x, b.y);
           }
         }
       }
-      // relative to 0 where no visible score is a number yet: hidden scores have
-      // weight 0 there too, and NaN, which the maximum passes over, stays
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = (part[n][0][e] + part[n][1][e]) * A.scale_log2e;
+    }
+    // ---- hidden positions; none where every column sees all 16
+    const int j0 = u + (u < sink_rows ? 0 : gap), j1 = u + kUnit - 1 + (u + kUnit - 1 < sink_rows ? 0 : gap);
+    const bool whole = rows >= kUnit && (!kMulti || (j1 <= (int)A.pos0 && (j0 > last_p - A.window || j1 < A.sinks)));
+    if (!whole) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // e: column e & 1, row grp + 8 (e >> 1)
+          const int r = grp + 8 * (e >> 1);
+          bool seen = r < rows;
+          if (kMulti) {
+            const int j = u + r + (u + r < sink_rows ? 0 : gap), p = cpos[n][e & 1];
+            seen = seen && j <= p && (p - j < A.window || j < A.sinks);
+          }
+          if (!seen) sc[n][e] = -INFINITY;
+        }
+    }
+    // ---- weights, relative to a reference that is 7 below a column's largest score
+    // and moves only when that grows by more than 8: weights reach 2^15, O is
+    // rescaled rarely, and fp16 keeps weights down to 2^-32 of the largest.  A column
+    // that has seen nothing keeps -inf, and its weights, all 0, are relative to 0.
+    // NaN, which the maximum passes over, stays.
+    bool moves = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) moves = moves || fmaxf(sc[n][e], sc[n][e + 2]) > m[n][e] + 15.f;
+    if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(sc[n][e], sc[n][e + 2]);
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          if (t > m[n][e] + 15.f) {
+            const float corr = ex2_approx(m[n][e] - (t - 7.f));
+            m[n][e] = t - 7.f;
+            om[n][e] *= corr;
+            om[n][e + 2] *= corr;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[n][i][e] *= corr;
+              o[n][i][e + 2] *= corr;
+            }
+          }
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float ref = m[n][e & 1];
         p[e] = ex2_approx(sc[n][e] - (ref == -INFINITY ? 0.f : ref));
-        l[n][e & 1] += p[e];
       }
       pb[n][0] = transpose8(pack_h2(p[0], p[1]));
       pb[n][1] = transpose8(pack_h2(p[2], p[3]));
     }
     // ---- O^T += V^T P: after transposing, this lane has group grp / 2 of the
     // dimensions and rows 2 tq, 2 tq + 1 (and those + 8)
-    __half2 dv[2], mv[2];
+    uint32_t dv[2], mv[2];
     bool odd = false;  // a row has a value that is not finite
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // even lanes' rows get d, odd ones m, of the pair of positions
-      const uint32_t mine = transpose8(grp + 8 * i < rows ? x.vs[i] : 0u);
+      const uint32_t mine = transpose8(grp + 8 * i < rows ? (i ? vs1 : vs0) : 0u);
       const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
-      uint32_t d = grp & 1 ? other : mine, mm = grp & 1 ? mine : other;
+      dv[i] = grp & 1 ? other : mine;
+      mv[i] = grp & 1 ? mine : other;
       if (kMulti) {
-        // the largest value; infinity and NaN have the exponent's bits all set
-        const uint32_t top = as_u32(__hfma2(__float2half2_rn(15.f), as_h2(d), as_h2(mm)));
-        const bool b0 = (top & 0x7C00u) == 0x7C00u, b1 = (top & 0x7C000000u) == 0x7C000000u;
+        // infinity and NaN have the exponent's bits all set
+        const uint32_t top = as_u32(__hmul2(__float2half2_rn(15.f), as_h2(dv[i])));
+        const bool b0 = (top & 0x7C00u) == 0x7C00u || (mv[i] & 0x7C00u) == 0x7C00u;
+        const bool b1 = (top & 0x7C000000u) == 0x7C000000u || (mv[i] & 0x7C000000u) == 0x7C000000u;
         const uint32_t keep = (b0 ? 0u : 0xFFFFu) | (b1 ? 0u : 0xFFFF0000u);
-        d &= keep;
-        mm &= keep;
+        dv[i] &= keep;
+        mv[i] &= keep;
         odd = odd || b0 || b1;
       }
-      dv[i] = as_h2(d);
-      mv[i] = as_h2(mm);
     }
-    const uint32_t v0[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w}, v1[4] = {x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
+    const Scaled s0(dv[0]), s1(dv[1]);
+    const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
+    auto values = [&](auto wide) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __half2 p0[4], p1[4];
-      unpack_pairs(transpose8(v0[j]), p0);
-      unpack_pairs(transpose8(v1[j]), p1);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t p0[4], p1[4];
+        s0.template operator()<decltype(wide)::value>(transpose8(a0[j]), p0);
+        s1.template operator()<decltype(wide)::value>(transpose8(a1[j]), p1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t a[4] = {as_u32(__hfma2(p0[2 * h], dv[0], mv[0])), as_u32(__hfma2(p0[2 * h + 1], dv[0], mv[0])),
-                               as_u32(__hfma2(p1[2 * h], dv[1], mv[1])), as_u32(__hfma2(p1[2 * h + 1], dv[1], mv[1]))};
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a[4] = {p0[2 * h], p0[2 * h + 1], p1[2 * h], p1[2 * h + 1]};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(o[n][2 * j + h], a, pb[n][0], pb[n][1]);
+          for (int n = 0; n < NT; ++n) mma16816(o[n][2 * j + h], a, pb[n][0], pb[n][1]);
+        }
       }
+    };
+    if (__any_sync(0xffffffffu, max(vs0 & 0x7FFFu, vs1 & 0x7FFFu) > kWideD))
+      values(std::true_type{});
+    else
+      values(std::false_type{});
+    {
+      const uint32_t a[4] = {mv[0], 0x3C003C00u, mv[1], 0x3C003C00u};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816(om[n], a, pb[n][0], pb[n][1]);
     }
     if (kMulti && __any_sync(0xffffffffu, odd)) {
       // Such a value has entered the product as 0: it is NaN for the columns that
       // see its row, and nothing for the others.
       for (int r = 0; r < kUnit && r < rows; ++r) {
         const int j = u + r + (u + r < sink_rows ? 0 : gap);
-        const uint32_t w = (vd - tq)[4 * (int64_t)j + (grp >> 1)];
-        const __half2 top = __hfma2(__float2half2_rn(15.f), as_h2(w), as_h2(w >> 16));
-        if ((as_u32(top) & 0x7C00u) != 0x7C00u) continue;
+        const uint32_t w = reinterpret_cast<const uint32_t*>(R.vs)[4 * r + (grp >> 1)];
+        const uint32_t top = as_u32(__hmul2(__float2half2_rn(15.f), as_h2(w)));
+        if ((top & 0x7C00u) != 0x7C00u && (w & 0x7C000000u) != 0x7C000000u) continue;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int p = cpos[n][e];
-            if (j <= p && (p - j < A.window || j < A.sinks))
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[n][i][e] = o[n][i][e + 2] = NAN;
+            if (j <= p && (p - j < A.window || j < A.sinks)) om[n][e] = NAN;
           }
       }
     }
-    x = next;
   }
-  // The lanes of a column join their sums; the warp's maximum and sum.
+  copy_wait<0>();
+  __syncwarp();
+  // The warp's references and sums of weights.
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-      // -inf: it saw nothing.  A warp that saw NaN alone has no maximum either, but
-      // a NaN sum: with NaN as its maximum it counts, and the column is NaN.
-      if (m[n][e] == -INFINITY && l[n][e] != 0.f) m[n][e] = NAN;
+      // -inf: it saw nothing.  A warp that saw NaN alone has no reference either, but
+      // a NaN sum: with NaN as its reference it counts, and the column is NaN.
+      if (m[n][e] == -INFINITY && om[n][e + 2] != 0.f) m[n][e] = NAN;
       if (grp == 0) {
         S.wmax[warp][8 * n + 2 * tq + e] = m[n][e];
-        S.wsum[warp][8 * n + 2 * tq + e] = l[n][e];
+        S.wsum[warp][8 * n + 2 * tq + e] = om[n][e + 2];
       }
     }
   __syncthreads();
@@ -344,32 +437,39 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
       float M = -INFINITY;
       for (int w = 0; w < Sh::kWarps; ++w) M = fmaxf(M, S.wmax[w][col]);
       const float f = m[n][e] == -INFINITY ? 0.f : exp2f(m[n][e] - M);
-      float* dst = &S.part[warp][col * kD + 32 * (grp >> 1) + 4 * (grp & 1)];
+      if (col >= A.M * A.G) continue;
+      float* dst = &S.warp[warp].part[col * kD + 32 * (grp >> 1) + 4 * (grp & 1)];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float4*>(dst + 8 * j) =
-            make_float4(f * o[n][2 * j][e], f * o[n][2 * j][e + 2], f * o[n][2 * j + 1][e], f * o[n][2 * j + 1][e + 2]);
+            make_float4(f * (o[n][2 * j][e] + om[n][e]), f * (o[n][2 * j][e + 2] + om[n][e]),
+                        f * (o[n][2 * j + 1][e] + om[n][e]), f * (o[n][2 * j + 1][e + 2] + om[n][e]));
     }
   __syncthreads();
   __syncwarp();
-  cluster_wait();  // every CTA of the cluster is running
+  if (!A.part) cluster_wait();  // every CTA of the cluster is running
   // The CTA's sums, the warps in order, go to the CTA of the cluster that writes
-  // them out: shares of the M G 128 outputs in runs of four.
+  // them out, shares of the M G 128 outputs in runs of four, or to the scratch.
   const int cols = A.M * A.G, quads = cols * (kD / 4);
   const int share = (quads + A.C - 1) / A.C;
   for (int i = threadIdx.x; i < quads; i += Sh::kThreads) {
-    float4 a = *reinterpret_cast<const float4*>(&S.part[0][4 * i]);
+    float4 a = *reinterpret_cast<const float4*>(&S.warp[0].part[4 * i]);
     for (int w = 1; w < Sh::kWarps; ++w) {
-      const float4 b = *reinterpret_cast<const float4*>(&S.part[w][4 * i]);
+      const float4 b = *reinterpret_cast<const float4*>(&S.warp[w].part[4 * i]);
       a.x += b.x;
       a.y += b.y;
       a.z += b.z;
       a.w += b.w;
     }
-    const int to = i / share;
-    st_cluster_v4(mapa_shared(smem_u32(&S.red[4 * (rank * share + i - to * share)]), (uint32_t)to), a);
+    if (A.part) {
+      const int64_t at = ((int64_t)g * cols + i / (kD / 4)) * A.C + rank;
+      reinterpret_cast<float4*>(A.part)[at * (kD / 4) + i % (kD / 4)] = a;
+    } else {
+      const int to = i / share;
+      st_cluster_v4(mapa_shared(smem_u32(&S.red[4 * (rank * share + i - to * share)]), (uint32_t)to), a);
+    }
   }
-  for (int i = threadIdx.x; i < cols * A.C; i += Sh::kThreads) {
+  for (int i = threadIdx.x; i < cols * (A.part ? 1 : A.C); i += Sh::kThreads) {
     const int to = i / cols, col = i - to * cols;
     float M = -INFINITY, L = 0.f;
     for (int w = 0; w < Sh::kWarps; ++w) M = fmaxf(M, S.wmax[w][col]);
@@ -379,8 +479,13 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
       if (mw != -INFINITY) L = fmaf(exp2f(mw - M), S.wsum[w][col], L);
       nan = nan || mw != mw;
     }
-    st_cluster_v2(mapa_shared(smem_u32(&S.stat[rank][col]), (uint32_t)to), make_float2(nan ? NAN : M, L));
+    const float2 st = make_float2(nan ? NAN : M, L);
+    if (A.part)
+      reinterpret_cast<float2*>(A.part + (int64_t)A.Hkv * cols * A.C * kD)[((int64_t)g * cols + col) * A.C + rank] = st;
+    else
+      st_cluster_v2(mapa_shared(smem_u32(&S.stat[rank][col]), (uint32_t)to), st);
   }
+  if (A.part) return;
   __syncwarp();
   cluster_sync_all();
   for (int i = threadIdx.x; i < share && rank * share + i < quads; i += Sh::kThreads) {
@@ -408,9 +513,56 @@ __global__ void __launch_bounds__(Q4Shape<NT>::kThreads, 1) attn_q4_decode_kerne
   }
 }
 
+// One column of one key/value head from its C partial results, in order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_q4_join_kernel(const __grid_constant__ Q4Args A) {
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float totals[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cols = A.M * A.G, g = blockIdx.x / cols, col = blockIdx.x - g * cols;
+  const float4* o = reinterpret_cast<const float4*>(A.part) + (int64_t)blockIdx.x * A.C * (kD / 4) + lane;
+  const float2* st = reinterpret_cast<const float2*>(A.part + (int64_t)A.Hkv * cols * A.C * kD) + (int64_t)blockIdx.x * A.C;
+  dependent_wait();
+  float M = -INFINITY;
+  for (int r = lane; r < A.C; r += 32) M = fmaxf(M, st[r].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = warp; r < A.C; r += kJoinWarps) {
+    const float2 s = st[r];
+    const float4 b = o[(int64_t)r * (kD / 4)];
+    const float f = s.x == -INFINITY ? 0.f : exp2f(s.x - M);  // -inf: it saw nothing, and has zeros
+    L = fmaf(f, s.y, L);
+    a.x = fmaf(f, b.x, a.x);
+    a.y = fmaf(f, b.y, a.y);
+    a.z = fmaf(f, b.z, a.z);
+    a.w = fmaf(f, b.w, a.w);
+  }
+  sums[warp][lane] = a;
+  if (lane == 0) totals[warp] = L;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    const float4 b = sums[w][lane];
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+    L += totals[w];
+  }
+  const float inv = 1.0f / L;
+  const int token = col / A.G;
+  __half* dst = A.out + ((int64_t)token * A.H + g * A.G + (col - token * A.G)) * kD + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_h2(within_half(a.x * inv), within_half(a.y * inv)),
+                                              pack_h2(within_half(a.z * inv), within_half(a.w * inv)));
+}
+
 // How many clusters of `c` CTAs of the kernel the device runs at once (a cluster
 // lies within one GPC).  Asked once per device and size; attributes are set before.
-template <int NT, bool kMulti>
+template <int NT, int W, bool kMulti>
 int max_clusters(int c) {
   static std::atomic<int> known[kMaxDevices][kQMaxCluster + 1];
   const int dev = current_device();
@@ -419,8 +571,8 @@ int max_clusters(int c) {
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c);
-    cfg.blockDim = dim3(Q4Shape<NT>::kThreads);
-    cfg.dynamicSmemBytes = sizeof(Q4Shared<NT>);
+    cfg.blockDim = dim3(Q4Shape<NT, W>::kThreads);
+    cfg.dynamicSmemBytes = sizeof(Q4Shared<NT, W>);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)c;
@@ -428,7 +580,7 @@ int max_clusters(int c) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, attn_q4_decode_kernel<NT, kMulti>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, attn_q4_decode_kernel<NT, W, kMulti>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -438,26 +590,39 @@ int max_clusters(int c) {
   return n;
 }
 
-template <int NT, bool kMulti>
+// CTAs for each key/value head where they need not be a cluster: one for every SM.
+int split_ctas(int64_t units, int Hkv, int per_sm) {
+  const int64_t c = std::max(1, std::min(per_sm * device_sms(), kQMaxSplit) / Hkv);
+  return (int)std::min<int64_t>(c, units);
+}
+
+template <int NT, int W, bool kMulti>
 cudaError_t launch_decode(Q4Args A, cudaStream_t s) {
-  static_assert(sizeof(Q4Shared<NT>) <= 227 * 1024, "shared memory of a CTA");
+  static_assert(sizeof(Q4Shared<NT, W>) <= 227 * 1024, "shared memory of a CTA");
   static PerDeviceFlag attr_set;
   const int dev = current_device();
   if (!attr_set.done(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(attn_q4_decode_kernel<NT, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Q4Shared<NT>));
+    cudaError_t e = cudaFuncSetAttribute(attn_q4_decode_kernel<NT, W, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(Q4Shared<NT, W>));
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_q4_decode_kernel<NT, kMulti>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(attn_q4_decode_kernel<NT, W, kMulti>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
-  // Every warp has 16 positions at least, and all clusters run at once.
   const int64_t units = (A.total + kUnit - 1) / kUnit;
+  if (A.part) {
+    A.C = split_ctas(units, A.Hkv, Q4Shape<NT, W>::kPerSm);
+    const cudaError_t e = launch_dependent(attn_q4_decode_kernel<NT, W, kMulti>, dim3((unsigned)A.C, (unsigned)A.Hkv),
+                                           Q4Shape<NT, W>::kThreads, sizeof(Q4Shared<NT, W>), 1, s, A);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_q4_join_kernel, dim3((unsigned)(A.Hkv * A.M * A.G)), 32 * kJoinWarps, 0, 1, s, A);
+  }
+  // Every warp has 16 positions at least, and all clusters run at once.
   int c = 1;
-  while (c < kQMaxCluster && units > Q4Shape<NT>::kWarps * c && A.Hkv <= max_clusters<NT, kMulti>(2 * c)) c *= 2;
+  while (c < kQMaxCluster && units > Q4Shape<NT, W>::kWarps * c && A.Hkv <= max_clusters<NT, W, kMulti>(2 * c)) c *= 2;
   A.C = c;
-  return launch_dependent(attn_q4_decode_kernel<NT, kMulti>, dim3((unsigned)c, (unsigned)A.Hkv), Q4Shape<NT>::kThreads,
-                          sizeof(Q4Shared<NT>), (unsigned)c, s, A);
+  return launch_dependent(attn_q4_decode_kernel<NT, W, kMulti>, dim3((unsigned)c, (unsigned)A.Hkv), Q4Shape<NT, W>::kThreads,
+                          sizeof(Q4Shared<NT, W>), (unsigned)c, s, A);
 }
 
 // ---------------------------------------------------------------------------
@@ -525,6 +690,11 @@ Visible visible(int64_t M, int64_t pos0, int64_t window, int64_t sinks) {
   return {sinks, first - sinks, sinks + end - first};
 }
 
+// Whether a call of few tokens splits its positions over all SMs, joined by a
+// second kernel through the scratch, rather than over a cluster for each key/value
+// head, of which a GPC takes few.
+bool over_all_sms(int64_t total, int Hkv) { return total * Hkv >= kQSplitFrom; }
+
 bool few_tokens(int64_t M, int H, int Hkv) { return M * (H / Hkv) <= kQMaxCols; }
 
 }  // namespace
@@ -551,8 +721,10 @@ cudaError_t launch_dequant_kv_q4(const Q4Cache& c, uint16_t* k_out, uint16_t* v_
 }
 
 int64_t attn_q4_scratch(int64_t M, int H, int Hkv, int64_t pos0, int64_t window, int64_t sinks) {
-  if (M == 0 || few_tokens(M, H, Hkv) || (window == 0 && sinks == 0)) return 0;
-  return 2 * Hkv * visible(M, pos0, window, sinks).total * kRowBytes;
+  if (M == 0 || (window == 0 && sinks == 0)) return 0;
+  const int64_t total = visible(M, pos0, window, sinks).total;
+  if (!few_tokens(M, H, Hkv)) return 2 * Hkv * total * kRowBytes;
+  return !over_all_sms(total, Hkv) ? 0 : std::max(kQMaxSplit, Hkv) * M * (H / Hkv) * (kD + 2) * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_gqa_attention_q4(const uint16_t* q, const Q4Cache& c, uint16_t* out, int64_t M, int H, int Hkv,
@@ -588,10 +760,12 @@ cudaError_t launch_gqa_attention_q4(const uint16_t* q, const Q4Cache& c, uint16_
                  see.gap,
                  see.total,
                  scale * 1.4426950408889634f,
-                 1};
+                 1,
+                 over_all_sms(see.total, Hkv) ? static_cast<float*>(scratch) : nullptr};
   const int nt = (int)((M * (H / Hkv) + 7) / 8);
-  if (nt == 1) return M == 1 ? launch_decode<1, false>(A, s) : launch_decode<1, true>(A, s);
-  return nt == 2 ? launch_decode<2, true>(A, s) : launch_decode<4, true>(A, s);
+  if (nt == 1 && A.part) return M == 1 ? launch_decode<1, 16, false>(A, s) : launch_decode<1, 16, true>(A, s);
+  if (nt == 1) return M == 1 ? launch_decode<1, 8, false>(A, s) : launch_decode<1, 8, true>(A, s);
+  return nt == 2 ? launch_decode<2, 8, true>(A, s) : launch_decode<4, 8, true>(A, s);
 }
 
 }  // namespace qk

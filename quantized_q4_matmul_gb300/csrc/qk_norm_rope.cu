@@ -57,9 +57,9 @@ __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], uint32_t& dm)
   }
   const float m = __half2float(__float2half_rn(lo));
   const float d = __half2float(__float2half_rn(fmaxf(hi - m, 0.f) / 15.f));
-  // a value that is not finite, or m or d past fp16, makes the group NaN (d is
+  // a value that is not finite, or m or 15 d past fp16, makes the group NaN (d is
   // infinite then, or NaN where m is: infinity less infinity)
-  const bool fine = fabsf(m) < INFINITY && d < INFINITY;
+  const bool fine = fabsf(m) < INFINITY && d <= 4366.f;
   uint32_t q = 0;
   if (d > 0.f)
 #pragma unroll

@@ -252,7 +252,6 @@ def test_attention_group_sizes(qk_lib, cuda, H, Hkv):
     (4, 4000, 0, 900, 16, 2), (4, 3, 0, 5, 16, 2), (8, 500, 1, 0, 12, 3), (31, 100, 50, 60, 2, 2), (2, 40, 20, 10 ** 7, 6, 2)])
 def test_attention_few_tokens(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
     """Several tokens in one to four tiles of columns; each its own window."""
-    assert qk_lib.qk_gqa_attention_q4_scratch_bytes(M, H, Hkv, D, pos0, window, sinks) == 0
     _check(qk_lib, cuda, 405, M, H, Hkv, pos0, window, sinks)
 
 
@@ -289,7 +288,7 @@ def test_attention_non_finite_rows(qk_lib, cuda, M, H, Hkv):
     """A NaN key makes its row's queries NaN; a NaN or infinite value group its 32 dimensions;
     queries that do not see the row are as without it.  Alone in a warp's share too."""
     pos0, window, sinks = 600, 100, 3
-    need = qk_lib.qk_gqa_attention_q4_scratch_bytes(M, H, Hkv, D, pos0, window, sinks)
+    need = M * (H // Hkv) > 32  # a chunk
     for key, row in ((False, pos0 + M - 1), (False, pos0 - 50), (False, 1), (True, pos0 + M - 1), (True, pos0 - 97),
                      (True, 2)):
         for bad in (np.nan, np.inf):
