@@ -17,11 +17,13 @@
 // degree 4) and summed in pairs within a thread and in 64-bit integers, multiples
 // of 2^-44 of the largest weight, between threads: no order changes a result.
 //
-// A cluster of C CTAs has a row and goes over it three times (it stays in L2):
-//   1. its maximum, minimum, and whether it can be sampled from;
+// A cluster of C CTAs has a row and goes over it three times (it stays in L2; kept
+// in shared memory it was no faster):
+//   1. its maximum and minimum, and whether it can be sampled from;
 //   2. a histogram over (max - x) of counts and mean positions within a bin, from
 //      which the bins that hold the three borders and the token follow, the sums
-//      being known to 1e-5;
+//      being known to some 1e-5.  With top_k, logits below the least of the
+//      threads' maxima are left out;
 //   3. the exact sums of what lies before, between and behind those bins, and a
 //      list of the tokens in them (candidates).
 // Rank 0 sorts the candidates, adds their weights up and answers the questions in
@@ -32,7 +34,7 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
+#include <cstddef>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
@@ -48,13 +50,18 @@ constexpr int kBins = 4096;
 constexpr int kBinsPer = kBins / kSaThreads;
 constexpr int kCap = 2048;  // candidates
 constexpr int kCapPer = kCap / kSaThreads;
-constexpr int kWhole = 1024;  // a kept set of at most so many is listed whole
+constexpr int kWhole = kSaThreads;  // a kept set of at most so many is listed whole
 constexpr int kSegs = 5;
 constexpr float kOne = 17592186044416.f;  // 2^44: the largest weight
-constexpr float kSlack = 4e-5f;           // of the histogram's sums, relative
+constexpr float kMagic = 12582912.f;      // 1.5 2^23: adding it rounds to an integer in the low bits
+constexpr float kSlack = 6e-5f;           // of the histogram's sums, relative
+// Bins further than this many T below the maximum go without mean positions: of
+// tokens of weight w that hold the whole sum, an error of a bin's 12th root each
+// leaves sqrt(w) of one, 1.5e-5 of the sum at 10 T.
+constexpr float kMeans = 10.f;
 
 struct SaTable {
-  float2 t[256];  // 2^(-i / 256) as a pair
+  float h[256], l[256];  // 2^(-i / 256) as a pair
 };
 
 struct SaArgs {
@@ -65,30 +72,51 @@ struct SaArgs {
 };
 
 struct SaStat {
-  unsigned long long first;  // order of the best token
-  float mn;                  // least finite logit
-  uint32_t finite;           // finite logits
-  uint32_t bad;              // NaN or +inf among them
-  uint32_t pad;
+  float mx;         // largest logit; NaN where one is
+  float mn;         // least finite logit
+  float cut;        // least of the threads' maxima
+  uint32_t finite;  // logits but -inf
 };
 
-struct SaShared {
-  uint32_t cnt[kBins], frac[kBins];  // a bin's tokens, and their positions in it in 4096ths
-  unsigned long long cand[kCap];     // the candidates' places in the order
-  uint8_t cls[kBins];
-  float2 table[256];
-  SaStat stat[kSaMaxCluster];
-  unsigned long long seg_sum[kSaMaxCluster][kSegs];
-  uint32_t seg_cnt[kSaMaxCluster][kSegs];
-  uint32_t ncand;
-  unsigned long long red64[kSaWarps];
-  uint32_t red32[kSaWarps];
-  float redf[kSaWarps];
-  int lo[4], hi[4];  // bins of the candidates: k, p, m, token
-  int found[4];
-  unsigned long long s_k, s_n, s_p;
-  uint32_t n_p;
+constexpr int kRing = 4;  // chunks of a thread in flight
+
+// What takes turns in the same place.
+union SaFirst {
+  struct {  // histogram: a bin's tokens, and their positions in it in 4096ths; later what lies before it
+    uint32_t cnt[kBins], frac[kBins];
+  };
+  float4 ring[kRing][kSaThreads];  // sums: the logits on their way
+  struct {                         // answers: each candidate's weight and C
+    unsigned long long w[kCap], upto[kCap];
+  };
 };
+union SaSecond {
+  float4 ring[kRing][kSaThreads];  // until the sums
+  float2 acc[kSegs][kSaThreads];   // sums of weights
+  struct {                         // answers: the candidates in order, their places; bit 31 is min_p's
+    unsigned long long sorted[kCap];
+    uint32_t place[kCap];
+  };
+};
+
+struct alignas(16) SaShared {
+  SaFirst first;
+  SaSecond second;
+  unsigned long long cand[kCap];  // the candidates' places in the order
+  alignas(8) uint8_t cls[kBins];
+  SaTable table;
+  alignas(16) SaStat stat[kSaMaxCluster];
+  unsigned long long seg_sum[kSaMaxCluster][kSegs];
+  unsigned long long red64[kSegs][kSaWarps];
+  unsigned long long base[kSegs];  // sums of the classes up to each
+  unsigned long long s_k, s_p;
+  uint32_t red32[kSaWarps];
+  float redf[3][kSaWarps];
+  uint32_t base_cnt[kSegs];  // tokens of the classes up to each
+  int found[4];
+  uint32_t ncand, n_p, best, included, total;
+};
+static_assert(sizeof(SaShared) % 16 == 0 && kBinsPer == 8, "16-byte accesses");
 
 // Ascending in the order of the tokens: by the logit from the largest, then by the token.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -98,59 +126,123 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key >> 31) ? key : ~key & 0x7FFFFFFFu);
 }
+__device__ __forceinline__ float value_of(unsigned long long order) { return value_of((uint32_t)(order >> 32)); }
 
 // A sum as a pair of fp32.
 struct Pair {
   float h = 0.f, l = 0.f;
-  __device__ __forceinline__ void add(float wh, float wl) {
-    const float s = __fadd_rn(h, wh), b = __fsub_rn(s, h);
-    const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(wh, b));
+  __device__ __forceinline__ void add(float2 w) {
+    const float s = __fadd_rn(h, w.x), b = __fsub_rn(s, h);
+    const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(w.x, b));
     h = s;
-    l = __fadd_rn(l, __fadd_rn(e, wl));
+    l = __fadd_rn(l, __fadd_rn(e, w.y));
   }
   __device__ __forceinline__ unsigned long long fixed() const {
     return (unsigned long long)(__float2ll_rn(h * kOne) + __float2ll_rn(l * kOne));
   }
 };
 
-// exp((x - mx) / T) as a pair, within 2^-42; x finite.
-__device__ __forceinline__ float2 weight(float x, float mx, float ch, float cl, const float2* table) {
-  // d = mx - x without error
-  const float d = __fsub_rn(mx, x), b = __fsub_rn(d, mx);
-  const float dl = __fsub_rn(__fsub_rn(mx, __fsub_rn(d, b)), __fadd_rn(x, b));
-  // t = 256 log2(e) d / T
-  const float th = __fmul_rn(d, ch);
-  if (!(th < 45.f * 256.f)) return make_float2(0.f, 0.f);
-  const float tl = __fmaf_rn(dl, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, -th)));
-  const float r = rintf(th), f = __fsub_rn(th, r);
-  const int m = (int)r;
-  // u = (f + tl) ln 2 / 256, at most 2^-9.5; exp(-u) = 1 - uh + s
-  constexpr double kLn = 0.69314718055994530942 / 256;
-  constexpr float L = (float)kLn, Ll = (float)(kLn - (double)L);
-  const float uh = __fmul_rn(f, L);
-  const float ul = __fmaf_rn(tl, L, __fmaf_rn(f, Ll, __fmaf_rn(f, L, -uh)));
-  const float q = __fmul_rn(__fmul_rn(uh, uh), __fmaf_rn(-uh, __fmaf_rn(-uh, 1.f / 24.f, 1.f / 6.f), 0.5f));
-  const float s = __fadd_rn(__fmaf_rn(uh, ul, q), -ul);
-  // 2^(-i / 256) (1 - uh + s)
-  const float2 t = table[m & 255];
-  const float p = __fmul_rn(t.x, uh), pl = __fmaf_rn(t.y, uh, __fmaf_rn(t.x, uh, -p));
-  const float h = __fsub_rn(t.x, p), e = __fsub_rn(__fsub_rn(t.x, h), p);
-  const float l = __fadd_rn(e, __fadd_rn(t.y, __fmaf_rn(t.x, s, -pl)));
-  const float scale = __uint_as_float((uint32_t)(127 - (m >> 8)) << 23);
-  return make_float2(__fmul_rn(h, scale), __fmul_rn(l, scale));
+// Two numbers in one register pair, for the instructions that take both.
+struct Two {
+  unsigned long long v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  }
+};
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
 }
 
-__device__ __forceinline__ unsigned long long weight_fixed(float x, float mx, const SaArgs& A, const float2* table) {
-  const float2 w = weight(x, mx, A.ch, A.cl, table);
-  Pair p;
-  p.h = w.x;
-  p.l = w.y;
-  return p.fixed();
+// What the weights of a row need.
+struct Weigh {
+  float mx, most;  // differences above `most`, 83 T or 2^-120 of the largest weight, count as it
+  float ch, cl;    // 256 log2(e) / T as a pair
+  const SaTable* table;
+};
+
+// exp((x - mx) / T) of two finite logits as pairs, within 2^-38.
+__device__ __forceinline__ void weights(const Weigh& W, float x0, float x1, float2& w0, float2& w1) {
+  constexpr double kLn = 0.69314718055994530942 / 256;
+  constexpr float L = (float)kLn, Ll = (float)(kLn - (double)L);
+  const Two minus(-1.f), mx(W.mx), ch(W.ch), x(x0, x1);
+  // d + dl = mx - x without error
+  Two d = fma2(x, minus, mx);
+  const Two b = fma2(mx, minus, d);
+  const Two dl = fma2(add2(x, b), minus, fma2(fma2(b, minus, d), minus, mx));
+  float d0, d1, l0, l1;
+  d.get(d0, d1);
+  d = Two(fminf(d0, W.most), fminf(d1, W.most));
+  // th + tl = 256 log2(e) (mx - x) / T, th = m + f with an integer m; tl is 2^-9 at
+  // most, but for differences above `most` (whose dl may be NaN)
+  const Two th = mul2(d, ch);
+  Two tl = fma2(dl, ch, fma2(d, Two(W.cl), fma2(d, ch, mul2(d, Two(-W.ch)))));
+  tl.get(l0, l1);
+  tl = Two(fminf(fmaxf(l0, -1.f), 1.f), fminf(fmaxf(l1, -1.f), 1.f));
+  const Two mag = add2(th, Two(kMagic));
+  const Two f = fma2(add2(mag, Two(-kMagic)), minus, th);
+  // u = (f + tl) ln 2 / 256, at most 2^-9.5; exp(-u) = 1 - uh + s
+  const Two uh = mul2(f, Two(L)), nuh = mul2(f, Two(-L));
+  const Two ul = fma2(tl, Two(L), fma2(f, Two(Ll), fma2(f, Two(L), nuh)));
+  const Two q = mul2(mul2(uh, uh), fma2(nuh, fma2(nuh, Two(1.f / 24.f), Two(1.f / 6.f)), Two(0.5f)));
+  const Two s = fma2(ul, minus, fma2(ul, fma2(q, minus, uh), q));
+  // 2^(-i / 256) (1 - uh + s), i = m modulo 256, times 2^-(m / 256)
+  float m0, m1;
+  mag.get(m0, m1);
+  const uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);  // m in the low bits
+  const Two t(W.table->h[b0 & 255u], W.table->h[b1 & 255u]), r(W.table->l[b0 & 255u], W.table->l[b1 & 255u]);
+  const Two np = mul2(t, nuh), pl = fma2(r, uh, fma2(t, uh, np));
+  const Two h = add2(t, np), e = add2(fma2(h, minus, t), np);
+  const Two l = add2(e, fma2(pl, minus, fma2(t, s, r)));
+  const Two scale(__uint_as_float((127u << 23) - ((b0 & 0x7F00u) << 15)),
+                  __uint_as_float((127u << 23) - ((b1 & 0x7F00u) << 15)));
+  mul2(h, scale).get(w0.x, w1.x);
+  mul2(l, scale).get(w0.y, w1.y);
+}
+__device__ __forceinline__ float2 weight(const Weigh& W, float x) {
+  float2 a, b;
+  weights(W, x, x, a, b);
+  return a;
 }
 
 // Whether a weight is at least min_p: the difference of two near numbers is exact.
 __device__ __forceinline__ bool at_least(float2 w, float min_p) {
   return __fadd_rn(__fsub_rn(w.x, min_p), w.y) >= 0.f;
+}
+
+// f S rounded down to an integer, 0 <= f <= 1; `rest`: whether something was lost.
+__device__ __forceinline__ unsigned long long times(unsigned long long S, float f, bool& rest) {
+  const uint32_t bits = __float_as_uint(f), ex = bits >> 23;
+  const uint32_t man = ex ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;
+  const int sh = 150 - (int)(ex ? ex : 1u);  // f = man 2^-sh, sh 23 .. 149
+  const unsigned long long lo = S * man, hi = __umul64hi(S, man);
+  if (sh < 64) {
+    rest = (lo << (64 - sh)) != 0;
+    return (lo >> sh) | (hi << (64 - sh));
+  }
+  const int k = sh - 64;
+  const unsigned long long r = k < 64 ? hi >> k : 0ull;
+  rest = lo != 0 || (k < 64 ? (r << k) != hi : hi != 0);
+  return r;
+}
+
+// (x - mx) / T less the logarithm of the kept sum, which is 1 at least: no cancellation.
+__device__ __forceinline__ float share_log(float x, float mx, float T, unsigned long long sum) {
+  return (x - mx) / T - log1pf((float)(sum - (1ull << 44)) * (1.f / kOne));
 }
 
 template <typename T>
@@ -173,124 +265,133 @@ __device__ __forceinline__ T cta_sum(T v, T* red) {
   return s;
 }
 
-// What lies before this thread's value, over the CTA.
+// Sum over this and the lanes before.
 template <typename T>
-__device__ __forceinline__ T cta_before(T v, T* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T x = v;
+__device__ __forceinline__ T warp_upto(T x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    if ((threadIdx.x & 31) >= o) x += y;
   }
-  __syncthreads();
-  if (lane == 31) red[warp] = x;
-  __syncthreads();
-  T before = 0;
-  for (int w = 0; w < warp; ++w) before += red[w];
-  return before + (x - v);
+  return x;
 }
 
-// Calls f(logit, token) for every finite logit of chunks c0 .. c1 - 1 of a row; a
-// chunk is 16 aligned bytes, the first has `pad` values before the row.
+// Calls f(four logits, chunk) for this thread's chunks c0 + threadIdx.x, ... below c1
+// of a row.  A chunk is 16 aligned bytes; the first has `pad` values before the row.
+// Where there is no logit it has -inf; -0 is 0.  Chunks come through the thread's
+// places in `ring`, kRing - 1 of them on their way.  Past its last one a thread's
+// logits are -inf.
 template <typename F>
-__device__ __forceinline__ void each_logit(const float* row, int V, int pad, int c0, int c1, F f) {
-  const int last = (V + pad + 3) / 4 - 1;
-  constexpr int kFlight = 4;
-  for (int c = c0 + (int)threadIdx.x; c < c1; c += kFlight * kSaThreads) {
-    float4 x[kFlight];
-#pragma unroll
-    for (int b = 0; b < kFlight; ++b) {
-      const int k = c + b * kSaThreads;
-      x[b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (k < c1) {
-        if (k > 0 && k < last) {
-          x[b] = __ldg(reinterpret_cast<const float4*>(row - pad) + k);
-        } else {  // the row's ends
-          const int v = 4 * k - pad;
-          if (v >= 0 && v < V) x[b].x = __ldg(row + v);
-          if (v + 1 >= 0 && v + 1 < V) x[b].y = __ldg(row + v + 1);
-          if (v + 2 >= 0 && v + 2 < V) x[b].z = __ldg(row + v + 2);
-          if (v + 3 >= 0 && v + 3 < V) x[b].w = __ldg(row + v + 3);
-        }
+__device__ __forceinline__ void each_chunk(const float* row, int V, int pad, int c0, int c1,
+                                           float4 (*ring)[kSaThreads], F f) {
+  const int tid = threadIdx.x;
+  auto fetch = [&](int k, int slot) {
+    if (k < c1) {
+      float4* to = &ring[slot][tid];
+      if (k > 0 && 4 * k + 3 - pad < V) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(row - pad + 4 * (int64_t)k)
+                     : "memory");
+      } else {  // the row's ends
+        const int v = 4 * k - pad;
+        float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (v >= 0 && v < V) x.x = __ldg(row + v);
+        if (v + 1 >= 0 && v + 1 < V) x.y = __ldg(row + v + 1);
+        if (v + 2 >= 0 && v + 2 < V) x.z = __ldg(row + v + 2);
+        if (v + 3 >= 0 && v + 3 < V) x.w = __ldg(row + v + 3);
+        *to = x;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int c = c0 + tid;
 #pragma unroll
-    for (int b = 0; b < kFlight; ++b) {
-      const int v = 4 * (c + b * kSaThreads) - pad;
-      const float y[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (y[e] != -INFINITY) f(__fadd_rn(y[e], 0.f), v + e);  // -0 is 0
-    }
+  for (int i = 0; i < kRing - 1; ++i) fetch(c + i * kSaThreads, i);
+  int slot = 0;
+#pragma unroll 1
+  for (; c - (tid & 31) < c1; c += kSaThreads) {  // as often for all lanes
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (c < c1) x = ring[slot][tid];
+    fetch(c + (kRing - 1) * kSaThreads, (slot + kRing - 1) & (kRing - 1));
+    slot = (slot + 1) & (kRing - 1);
+    const float y[4] = {__fadd_rn(x.x, 0.f), __fadd_rn(x.y, 0.f), __fadd_rn(x.z, 0.f), __fadd_rn(x.w, 0.f)};
+    f(y, c);
+    __syncwarp();  // lanes that f parted go on together
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// ---------------------------------------------------------------------------
+// The search, for rows whose borders the histogram does not separate
+// ---------------------------------------------------------------------------
 struct Sums {
   unsigned long long w;
   uint32_t n;
 };
 
-// The exact sum over the tokens up to `order`, by one CTA.
-__device__ __noinline__ Sums sums_upto(const SaArgs& A, SaShared& S, const float* row, int pad, float mx,
-                                       unsigned long long order) {
+// One CTA's view of a row.
+struct Row {
+  const float* x;
+  int V, pad;
+  Weigh weigh;
+};
+
+// The exact sum over the tokens up to `order`.
+__device__ __noinline__ Sums sums_upto(SaShared& S, const Row& R, unsigned long long order) {
   Pair sum;
   uint32_t n = 0;
-  each_logit(row, A.a.V, pad, 0, (A.a.V + pad + 3) / 4, [&](float x, int v) {
-    if ((((unsigned long long)key_of(x) << 32) | (uint32_t)v) <= order) {
-      const float2 w = weight(x, mx, A.ch, A.cl, S.table);
-      sum.add(w.x, w.y);
-      ++n;
-    }
+  each_chunk(R.x, R.V, R.pad, 0, (R.V + R.pad + 3) / 4, S.first.ring, [&](const float(&y)[4], int k) {
+    const int v = 4 * k - R.pad;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (y[e] != -INFINITY && (((unsigned long long)key_of(y[e]) << 32) | (uint32_t)(v + e)) <= order) {
+        sum.add(weight(R.weigh, y[e]));
+        ++n;
+      }
   });
   Sums r;
-  r.w = cta_sum(sum.fixed(), S.red64);
+  r.w = cta_sum(sum.fixed(), S.red64[0]);
   r.n = cta_sum(n, S.red32);
   return r;
 }
 
-// The first token in the order at which done(sums up to it) holds; it holds for
-// the last.  The key bit by bit, then the token.
-template <typename F>
-__device__ __forceinline__ unsigned long long first_where(const SaArgs& A, SaShared& S, const float* row, int pad,
-                                                          float mx, Sums& at, F done) {
-  uint32_t lo = 0u, hi = 0xFFFFFFFFu;
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (done(sums_upto(A, S, row, pad, mx, ((unsigned long long)mid << 32) | 0xFFFFFFFFull)))
-      hi = mid;
-    else
-      lo = mid + 1;
+// The first token in the order whose sums are at least `least` (of the weights, or,
+// with `count`, of the tokens); those of the last are.  The key bit by bit, then
+// the token.
+__device__ __noinline__ unsigned long long first_with(SaShared& S, const Row& R, bool count, unsigned long long least,
+                                                      Sums& at) {
+  unsigned long long key = 0;
+  for (int part = 0; part < 2; ++part) {
+    uint32_t lo = 0u, hi = part ? (uint32_t)R.V - 1u : 0xFFFFFFFFu;
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const Sums s = sums_upto(S, R, part ? key | mid : ((unsigned long long)mid << 32) | 0xFFFFFFFFull);
+      if (s.n > 0 && (count ? (unsigned long long)s.n : s.w) >= least)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    key = part ? key | lo : (unsigned long long)lo << 32;
   }
-  const unsigned long long key = (unsigned long long)lo << 32;
-  lo = 0u;
-  hi = (uint32_t)A.a.V - 1u;
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (done(sums_upto(A, S, row, pad, mx, key | mid)))
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  at = sums_upto(A, S, row, pad, mx, key | lo);
-  return key | lo;
+  at = sums_upto(S, R, key);
+  return key;
 }
 
-// The whole answer by searches; one CTA.
-__device__ __noinline__ void sample_slowly(const SaArgs& A, SaShared& S, const float* row, int pad, float mx,
-                                           uint32_t finite, float u, int64_t m) {
-  Sums all = sums_upto(A, S, row, pad, mx, ~0ull), at;
+// The whole answer; one CTA.
+__device__ __noinline__ void sample_slowly(const SaArgs& A, SaShared& S, const Row& R, uint32_t finite, float u,
+                                           int64_t m) {
+  Sums all = sums_upto(S, R, ~0ull), at;
   uint32_t n = finite;
   unsigned long long s_n = all.w;
+  bool rest;
   if (A.a.top_k > 0 && (uint32_t)A.a.top_k < finite) {
-    const uint32_t k = (uint32_t)A.a.top_k;
-    first_where(A, S, row, pad, mx, at, [&](const Sums& s) { return s.n >= k; });
+    first_with(S, R, true, (uint32_t)A.a.top_k, at);
     n = at.n;
     s_n = at.w;
   }
   if (A.a.top_p < 1.f) {
-    const double t = (double)A.a.top_p * (double)s_n;
-    first_where(A, S, row, pad, mx, at, [&](const Sums& s) { return s.n > 0 && (double)s.w >= t; });
+    const unsigned long long t = times(s_n, A.a.top_p, rest);
+    first_with(S, R, false, t + (rest ? 1u : 0u), at);
     if (at.n < n) {
       n = at.n;
       s_n = at.w;
@@ -298,35 +399,42 @@ __device__ __noinline__ void sample_slowly(const SaArgs& A, SaShared& S, const f
   }
   if (A.a.min_p > 0.f) {
     uint32_t c = 0;
-    each_logit(row, A.a.V, pad, 0, (A.a.V + pad + 3) / 4,
-               [&](float x, int) { c += at_least(weight(x, mx, A.ch, A.cl, S.table), A.a.min_p) ? 1u : 0u; });
+    each_chunk(R.x, R.V, R.pad, 0, (R.V + R.pad + 3) / 4, S.first.ring, [&](const float(&y)[4], int) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c += y[e] != -INFINITY && at_least(weight(R.weigh, y[e]), A.a.min_p) ? 1u : 0u;
+    });
     c = cta_sum(c, S.red32);
     if (c < n) {
-      first_where(A, S, row, pad, mx, at, [&](const Sums& s) { return s.n >= c; });
+      first_with(S, R, true, c, at);
       n = at.n;
       s_n = at.w;
     }
   }
-  const double t = (double)u * (double)s_n;
-  const unsigned long long order = first_where(A, S, row, pad, mx, at, [&](const Sums& s) { return (double)s.w > t; });
+  const unsigned long long order = first_with(S, R, false, times(s_n, u, rest) + 1u, at);
   if (threadIdx.x == 0) {
-    const unsigned long long w = weight_fixed(value_of((uint32_t)(order >> 32)), mx, A, S.table);
     A.a.token[m] = (int32_t)(uint32_t)order;
-    if (A.a.logprob) A.a.logprob[m] = (float)log((double)w / (double)s_n);
+    if (A.a.logprob) A.a.logprob[m] = share_log(value_of(order), R.weigh.mx, A.a.temperature, s_n);
     if (A.a.kept) A.a.kept[m] = (int32_t)n;
   }
 }
 
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
+// ---------------------------------------------------------------------------
+// Clusters
+// ---------------------------------------------------------------------------
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint2 v) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 __device__ __forceinline__ uint32_t atom_cluster_add(uint32_t addr, uint32_t v) {
   uint32_t old;
@@ -349,6 +457,23 @@ __device__ __forceinline__ void cluster_meet(int C) {
   }
 }
 
+// max(a, b), NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// The bin of the histogram in which sums from the first token on reach `target`, at
+// least 1: the last one with less before it.
+__device__ __forceinline__ int reach(const uint32_t* before, uint32_t target) {
+  int b = 0;
+#pragma unroll 1
+  for (int step = kBins / 2; step > 0; step /= 2)
+    if (before[b + step] < target) b += step;
+  return b;
+}
+
 // A row for each cluster of A.C CTAs along x.
 __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_constant__ SaArgs A) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -362,265 +487,353 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   const int chunks = (V + pad + 3) / 4;
   const int c0 = (int)((int64_t)rank * chunks / C), c1 = (int)((int64_t)(rank + 1) * chunks / C);
   const float T = A.a.temperature;
-  for (int i = tid; i < kBins; i += kSaThreads) S.cnt[i] = S.frac[i] = 0u;
-  if (tid < 256) S.table[tid] = A.table.t[tid];
-  if (tid == 0) S.ncand = 0u;
-  if (tid < 4) S.lo[tid] = S.hi[tid] = kBins, S.found[tid] = 0;
+  const bool with_p = A.a.top_p < 1.f, with_m = A.a.min_p > 0.f;
+  if (C > 1) {
+    __syncwarp();
+    cluster_arrive();  // its wait is before the first write to another CTA
+  }
+  for (int i = tid; i < kBins / 2; i += kSaThreads) reinterpret_cast<uint4*>(S.first.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 256) {
+    S.table.h[tid] = A.table.h[tid];
+    S.table.l[tid] = A.table.l[tid];
+  }
+  if (tid < 4) S.found[tid] = 0;
+  if (tid == 0) S.ncand = 0u, S.best = 0xFFFFFFFFu;
   dependent_wait();
 
-  // ---- 1. the best token, the least finite logit
-  {
-    unsigned long long first = ~0ull;
-    float mx = -INFINITY, mn = INFINITY;
-    int id = 0;
-    uint32_t finite = 0, bad = 0;
-    each_logit(row, V, pad, c0, c1, [&](float x, int v) {
-      if (x > mx) mx = x, id = v;  // a thread's tokens ascend: the first of equal ones stays
-      mn = fminf(mn, x);
-      bad |= !(x < INFINITY) ? 1u : 0u;
-      ++finite;
-    });
-    if (mx > -INFINITY) first = ((unsigned long long)key_of(mx) << 32) | (uint32_t)id;
+  // ---- 1. the largest and the least finite logit
+  float mx = -INFINITY, mn = INFINITY, cut;
+  uint32_t finite = 0;
+  each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    for (int e = 0; e < 4; ++e) {
+      const bool is = y[e] != -INFINITY;
+      mx = max_nan(mx, y[e]);
+      mn = fminf(mn, is ? y[e] : INFINITY);
+      finite += is ? 1u : 0u;
+    }
+  });
+  cut = mx;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+  }
+  finite = __reduce_add_sync(0xffffffffu, finite);
+  if (lane == 0) {
+    S.redf[0][warp] = mx;
+    S.redf[1][warp] = mn;
+    S.redf[2][warp] = cut;
+    S.red32[warp] = finite;
+  }
+  __syncthreads();  // also: the histogram is clear
+  if (C > 1) {
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster is running
+  }
+  if (warp == 0) {
+    const int i = lane & (kSaWarps - 1);
+    mx = S.redf[0][i];
+    mn = S.redf[1][i];
+    cut = S.redf[2][i];
+    finite = lane < kSaWarps ? S.red32[i] : 0u;
+#pragma unroll 1
+    for (int o = kSaWarps / 2; o > 0; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+      cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
     }
-    finite = warp_sum(finite);
-    if (lane == 0) {
-      S.red64[warp] = first;
-      S.redf[warp] = mn;
-      S.red32[warp] = (bad << 31) | finite;
-    }
-    __syncthreads();  // also: the histogram is clear
-    cluster_meet(C);  // every CTA of the cluster is running
-    if (tid < C) {
-      for (int w = 0; w < kSaWarps; ++w) {
-        first = w ? min(first, S.red64[w]) : S.red64[0];
-        mn = w ? fminf(mn, S.redf[w]) : S.redf[0];
-      }
-      finite = bad = 0;
-      for (int w = 0; w < kSaWarps; ++w) {
-        finite += S.red32[w] & 0x7FFFFFFFu;
-        bad |= S.red32[w] >> 31;
-      }
-      const uint32_t to = mapa_shared(smem_u32(&S.stat[rank]), (uint32_t)tid);
-      st_cluster_u64(to, first);
-      st_cluster_u32(to + 8, __float_as_uint(mn));
-      st_cluster_u32(to + 12, finite);
-      st_cluster_u32(to + 16, bad);
-    }
-    cluster_meet(C);
+    finite = __reduce_add_sync(0xffffffffu, finite);
+    if (lane < C)
+      st_cluster_v4(mapa_shared(smem_u32(&S.stat[rank]), (uint32_t)lane),
+                    make_uint4(__float_as_uint(mx), __float_as_uint(mn), __float_as_uint(cut), finite));
   }
-  unsigned long long first = ~0ull;
-  float mn = INFINITY;
-  uint32_t finite = 0, bad = 0;
-  for (int r = 0; r < C; ++r) {
-    first = min(first, S.stat[r].first);
-    mn = fminf(mn, S.stat[r].mn);
-    finite += S.stat[r].finite;
-    bad |= S.stat[r].bad;
+  cluster_meet(C);
+  {
+    SaStat st{-INFINITY, INFINITY, -INFINITY, 0u};
+    if (lane < C) st = S.stat[lane];
+    mx = st.mx;
+    mn = st.mn;
+    cut = st.cut;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+    }
+    finite = __reduce_add_sync(0xffffffffu, st.finite);
   }
-  if (bad || finite == 0 || T == 0.f) {  // nothing to sample from, or the best token
+  if (!(fabsf(mx) < INFINITY)) {  // NaN, +inf, or nothing but -inf
     if (rank == 0 && tid == 0) {
-      const bool none = bad || finite == 0;
-      A.a.token[m] = none ? -1 : (int32_t)(uint32_t)first;
-      if (A.a.logprob) A.a.logprob[m] = none ? NAN : 0.f;
-      if (A.a.kept) A.a.kept[m] = none ? 0 : 1;
+      A.a.token[m] = -1;
+      if (A.a.logprob) A.a.logprob[m] = NAN;
+      if (A.a.kept) A.a.kept[m] = 0;
     }
     return;
   }
-  const float mx = value_of((uint32_t)(first >> 32));
+  if (T == 0.f) {  // the first of the largest
+    const uint32_t best0 = mapa_shared(smem_u32(&S.best), 0);
+    each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (y[e] == mx)
+          asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(best0), "r"(4 * k - pad + e) : "memory");
+    });
+    cluster_meet(C);
+    if (rank == 0 && tid == 0) {
+      A.a.token[m] = (int32_t)S.best;
+      if (A.a.logprob) A.a.logprob[m] = 0.f;
+      if (A.a.kept) A.a.kept[m] = 1;
+    }
+    return;
+  }
   float u = A.a.u[m];
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+  const Weigh W{mx, 83.f * T, A.ch, A.cl, &S.table};
 
-  // ---- 2. the histogram.  Bins beyond 31 T below the maximum are one.
+  // ---- 2. the histogram.  Logits further than 31 T below the maximum are in the last
+  // bin; those that cannot be kept are left out.
+  const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
   const float span = fminf(mx - mn, 31.f * T);
   const float scale = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;
-  auto bin_of = [&](float x, float& at) {
-    at = fminf((mx - x) * scale, (float)(kBins - 1));
-    return (int)at;
+  if (!with_k || A.a.top_k > kSaThreads) cut = -INFINITY;  // each thread's maximum reaches the cut
+  const float log_m = with_m ? -logf(A.a.min_p) * T : 0.f;
+  if (with_m && !with_p) cut = fmaxf(cut, mx - log_m * 1.001f - 4.f * span / (float)kBins);
+  auto bin_of = [&](float x, float& at) {  // the nearest bin, and the position less it
+    at = fminf(__fmul_rn(__fsub_rn(mx, x), scale), (float)(kBins - 1));
+    const float mag = __fadd_rn(at, kMagic);
+    at = __fsub_rn(at, __fsub_rn(mag, kMagic));
+    return (int)(__float_as_uint(mag) & (uint32_t)(kBins - 1));
   };
-  each_logit(row, V, pad, c0, c1, [&](float x, int) {
-    float at;
-    const int b = bin_of(x, at);
-    atomicAdd(&S.cnt[b], 1u);
-    atomicAdd(&S.frac[b], (uint32_t)((at - (float)b) * 4096.f));
+  const float means = mx - kMeans * T;
+  each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (y[e] != -INFINITY && y[e] >= cut) {
+        float at;
+        const int b = bin_of(y[e], at);
+        atomicAdd(&S.first.cnt[b], 1u);
+        if (y[e] >= means)  // (at + 1/2) 4096
+          atomicAdd(&S.first.frac[b], __float_as_uint(__fmaf_rn(at, 4096.f, kMagic + 2048.f)) - 0x4B400000u);
+      }
   });
   if (C > 1) {
     cluster_meet(C);
-    // each rank adds up a run of bins of all CTAs and gives each CTA the sums
-    uint32_t n[kBins / 2 / kSaThreads], fr[kBins / 2 / kSaThreads];
-    const int mine = kBins / C;
+    // Each rank adds up a run of bins of all CTAs and gives each CTA the sums; a bin
+    // is read by its own rank alone, so it may be overwritten at once.
+    const int mine = kBins / 2 / C;  // pairs of bins
+#pragma unroll 1
+    for (int i = tid; i < 2 * mine; i += kSaThreads) {
+      const uint32_t at = smem_u32(i < mine ? &S.first.cnt[2 * (rank * mine + i)] : &S.first.frac[2 * (rank * mine + i - mine)]);
+      uint2 n = make_uint2(0u, 0u);
+#pragma unroll 1
+      for (int r0 = 0; r0 < C; r0 += 8) {
+        uint2 x[8];
 #pragma unroll
-    for (int i = 0; i < kBins / 2 / kSaThreads; ++i) {
-      n[i] = fr[i] = 0u;
-      const int b = rank * mine + tid + i * kSaThreads;
-      if (tid + i * kSaThreads < mine)
-        for (int r = 0; r < C; ++r) {
-          n[i] += ld_cluster_u32(mapa_shared(smem_u32(&S.cnt[b]), (uint32_t)r));
-          fr[i] += ld_cluster_u32(mapa_shared(smem_u32(&S.frac[b]), (uint32_t)r));
-        }
-    }
-    // a bin is read by its own rank alone, so it may be overwritten at once
+        for (int r = 0; r < 8; ++r) x[r] = r0 + r < C ? ld_cluster_v2(mapa_shared(at, (uint32_t)(r0 + r))) : make_uint2(0u, 0u);
 #pragma unroll
-    for (int i = 0; i < kBins / 2 / kSaThreads; ++i) {
-      const int b = rank * mine + tid + i * kSaThreads;
-      if (tid + i * kSaThreads < mine)
-        for (int r = 0; r < C; ++r) {
-          st_cluster_u32(mapa_shared(smem_u32(&S.cnt[b]), (uint32_t)r), n[i]);
-          st_cluster_u32(mapa_shared(smem_u32(&S.frac[b]), (uint32_t)r), fr[i]);
-        }
+        for (int r = 0; r < 8; ++r) n.x += x[r].x, n.y += x[r].y;
+      }
+#pragma unroll 4
+      for (int r = 0; r < C; ++r) st_cluster_v2(mapa_shared(at, (uint32_t)r), n);
     }
   }
   cluster_meet(C);
 
-  // The bins where the borders are: this thread's are kBinsPer consecutive ones.
-  const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
-  const bool with_p = A.a.top_p < 1.f, with_m = A.a.min_p > 0.f;
+  // What lies before each bin: tokens, and weights as integers, 2^31 in all, so that
+  // no thread's sums differ from another's.  This thread's bins are kBinsPer
+  // consecutive ones.
   const float per_bin = scale > 0.f ? 1.44269504f / (T * scale) : 0.f;  // octaves
-  uint32_t n0[kBinsPer + 1];
-  unsigned long long f0[kBinsPer + 1];  // counts and sums before each bin
   {
+    uint4* cnt = reinterpret_cast<uint4*>(S.first.cnt) + 2 * tid;
+    uint4* frac = reinterpret_cast<uint4*>(S.first.frac) + 2 * tid;
+    const uint4 k0 = cnt[0], k1 = cnt[1], q0 = frac[0], q1 = frac[1];
+    uint32_t k[kBinsPer] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    uint32_t q[kBinsPer] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    float f[kBinsPer], sum = 0.f;
     uint32_t cn = 0;
-    unsigned long long cf = 0;
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
-      const int b = tid * kBinsPer + i;
-      const uint32_t k = S.cnt[b];
-      n0[i] = cn;
-      f0[i] = cf;
-      cn += k;
-      if (k)
-        cf += (unsigned long long)__float2ll_rn(kOne * (float)k *
-                                                exp2f(-per_bin * ((float)b + (float)S.frac[b] / (4096.f * (float)k))));
+      // the middle where no positions were added (with any, the sum is not 0: bin 0's are 1/2 and more)
+      const float kf = (float)k[i], mean = q[i] ? __fdividef((float)q[i], 4096.f * kf) - 0.5f : 0.f;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f[i]) : "f"(-per_bin * ((float)(tid * kBinsPer + i) + mean)));
+      f[i] *= kf;
+      sum += f[i];
+      cn += k[i];
     }
-    const uint32_t bn = cta_before(cn, S.red32);
-    const unsigned long long bf = cta_before(cf, S.red64);
+    const float part = warp_sum(sum);
+    if (lane == 0) S.redf[0][warp] = part;
+    __syncthreads();
+    const float all = warp_sum(lane < kSaWarps ? S.redf[0][lane] : 0.f);
+    const float per_unit = 2147000000.f / all;  // the roundings of kBins sums stay below 2^31
+    uint32_t cf = 0;
 #pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) n0[i] += bn, f0[i] += bf;
-    n0[kBinsPer] = bn + cn;
-    f0[kBinsPer] = bf + cf;
+    for (int i = 0; i < kBinsPer; ++i) {
+      q[i] = __float2uint_rn(f[i] * per_unit);
+      cf += q[i];
+    }
+    uint32_t xn = warp_upto(cn), xf = warp_upto(cf);
+    if (lane == 31) S.red32[warp] = xn, S.redf[1][warp] = __uint_as_float(xf);
+    __syncthreads();
+    xn += __reduce_add_sync(0xffffffffu, lane < warp ? S.red32[lane & (kSaWarps - 1)] : 0u) - cn;
+    xf += __reduce_add_sync(0xffffffffu, lane < warp ? __float_as_uint(S.redf[1][lane & (kSaWarps - 1)]) : 0u) - cf;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const uint32_t n = k[i], w = q[i];
+      k[i] = xn;
+      q[i] = xf;
+      xn += n;
+      xf += w;
+    }
+    cnt[0] = make_uint4(k[0], k[1], k[2], k[3]);
+    cnt[1] = make_uint4(k[4], k[5], k[6], k[7]);
+    frac[0] = make_uint4(q[0], q[1], q[2], q[3]);
+    frac[1] = make_uint4(q[4], q[5], q[6], q[7]);
+    if (tid == kSaThreads - 1) S.included = xn, S.total = xf;
   }
-  // Sum and count up to and with bin b, which its thread tells all others.
-  auto sum_with = [&](int b, uint32_t& count) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i)
-      if (tid * kBinsPer + i == b) S.redf[0] = (float)f0[i + 1], S.red32[0] = n0[i + 1];
-    __syncthreads();
-    count = S.red32[0];
-    return S.redf[0];
+  __syncthreads();
+  const uint32_t included = S.included, total = S.total;
+  auto sum_before = [&](int b) { return (float)(b < kBins ? S.first.frac[b] : total); };
+  auto count_before = [&](int b) { return b < kBins ? S.first.cnt[b] : included; };
+
+  // The bins where the borders are: ranges [lo, hi] for k, p, m and the token.  Every
+  // thread finds them; lanes 0 and 1 of a pair search the two ends.
+  int lo[4] = {kBins, kBins, kBins, kBins}, hi[4] = {kBins, kBins, kBins, kBins};
+  auto range = [&](float from, float to, int& first, int& last) {
+    const float t = lane & 1 ? to : from;
+    const int b = reach(S.first.frac, t > 1.f ? (uint32_t)t : 1u);
+    first = __shfl_sync(0xffffffffu, b, 0);
+    last = __shfl_sync(0xffffffffu, b, 1);
   };
-  uint32_t count;
-  const float total = sum_with(kBins - 1, count);
-  // The first bin whose sums reach t (the last where none does).
-  auto reach = [&](float t, int* out) {
-    const unsigned long long target = t > 1.f ? (unsigned long long)t : 1ull;
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i)
-      if (f0[i] < target && f0[i + 1] >= target) *out = tid * kBinsPer + i;
-    if (tid == kSaThreads - 1 && f0[kBinsPer] < target) *out = kBins - 1;
-  };
-  float s_lo = total, s_hi = total;  // the kept weights, within kSlack
-  uint32_t n_hi = finite;            // tokens up to the last bin that may hold the last kept one
-  int b_hi = kBins - 1;
+  float s_lo = (float)total, s_hi = s_lo;  // the kept weights, within kSlack
+  int b_hi = kBins - 1;                    // the last bin that may hold the last kept token
   if (with_k) {
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i)
-      if (n0[i] < (uint32_t)A.a.top_k && n0[i + 1] >= (uint32_t)A.a.top_k) S.lo[0] = S.hi[0] = tid * kBinsPer + i;
-    __syncthreads();
-    b_hi = S.hi[0];
-    s_hi = sum_with(b_hi, n_hi);
-    s_lo = b_hi > 0 ? sum_with(b_hi - 1, count) : 0.f;
+    lo[0] = hi[0] = b_hi = reach(S.first.cnt, (uint32_t)A.a.top_k);
+    s_lo = sum_before(b_hi);
+    s_hi = sum_before(b_hi + 1);
   }
   if (with_p) {
-    const float slack = kSlack * s_hi;
-    reach(A.a.top_p * s_lo - slack, &S.lo[1]);
-    reach(A.a.top_p * s_hi + slack, &S.hi[1]);
-    __syncthreads();
-    const int b = S.hi[1];
-    const float with = sum_with(b, count);
+    const float slack = kSlack * s_hi + 8.f;
+    range(A.a.top_p * s_lo - slack, A.a.top_p * s_hi + slack, lo[1], hi[1]);
     s_lo *= A.a.top_p;
-    if (b < b_hi) {
-      b_hi = b;
-      s_hi = with;
-      n_hi = count;
+    if (hi[1] < b_hi) {
+      b_hi = hi[1];
+      s_hi = sum_before(b_hi + 1);
     }
   }
   if (with_m) {
-    const int b = (int)fminf(-logf(A.a.min_p) * T * scale, (float)(kBins - 1));
-    const int b1 = min(kBins - 1, b + 1);
-    if (tid == 0) S.lo[2] = max(0, b - 1), S.hi[2] = b1;
-    s_lo = fminf(s_lo, b >= 2 ? sum_with(b - 2, count) : 0.f);
-    const float with = sum_with(b1, count);
-    if (b1 < b_hi) {
-      b_hi = b1;
-      s_hi = with;
-      n_hi = count;
+    const int b = (int)fminf(log_m * scale, (float)(kBins - 1));
+    lo[2] = max(0, b - 1);
+    hi[2] = min(kBins - 1, b + 2);
+    s_lo = fminf(s_lo, sum_before(lo[2]));
+    if (hi[2] < b_hi) {
+      b_hi = hi[2];
+      s_hi = sum_before(b_hi + 1);
     }
   }
-  if (n_hi <= kWhole) {
-    if (tid == 0) S.lo[3] = 0, S.hi[3] = b_hi;
+  if (count_before(b_hi + 1) <= kWhole) {
+    lo[3] = 0;
+    hi[3] = b_hi;
   } else {
-    const float slack = kSlack * total;
-    reach(u * s_lo - slack, &S.lo[3]);
-    reach(u * s_hi + slack, &S.hi[3]);
+    const float slack = kSlack * (float)total + 8.f;
+    range(u * s_lo - slack, u * s_hi + slack, lo[3], hi[3]);
   }
-  __syncthreads();
-  // Classes of the bins: 255 for the candidates', else how many of the ranges end before.
-  uint32_t listed = 0;
-#pragma unroll
-  for (int i = 0; i < kBinsPer; ++i) {
-    const int b = tid * kBinsPer + i;
-    int seg = 0;
-    bool in = false;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      in = in || (b >= S.lo[r] && b <= S.hi[r]);
-      seg += S.hi[r] < b ? 1 : 0;
-    }
-    S.cls[b] = in ? 255 : (uint8_t)seg;
-    if (in) listed += n0[i + 1] - n0[i];
-  }
-  listed = cta_sum(listed, S.red32);
-  int last = 0;  // the last bin that matters
-  const bool all = !with_k && (with_p || !with_m);
+  // Classes of the bins: 255 for the candidates', else how many of the ranges end
+  // before.
+  const bool all = !with_k && (with_p || !with_m);  // every weight counts
+  int last = all ? kBins - 1 : -1;                  // the last bin that matters
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (S.hi[r] < kBins) last = max(last, S.hi[r]);
-  if (all) last = kBins - 1;
-  const bool fits = listed <= kCap;
+    if (hi[r] < kBins) last = max(last, hi[r]);
+  auto seg_of = [&](int b) { return (hi[0] < b) + (hi[1] < b) + (hi[2] < b) + (hi[3] < b); };
+#pragma unroll 1
+  for (int b = tid; b < kBins; b += kSaThreads) {
+    bool in = false;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) in = in || (b >= lo[r] && b <= hi[r]);
+    S.cls[b] = in ? 255 : (uint8_t)seg_of(b);
+  }
+  // Lane s: the tokens of class s, whose bins are those behind the s-th range to end
+  // and before the first of the ranges that end later.
+  uint32_t seg_cnt = 0;
+  if (lane < kSegs) {
+    int from = lane ? kBins : 0, to = kBins;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (lane && hi[r] < kBins && seg_of(hi[r]) < lane && seg_of(hi[r] + 1) >= lane) from = hi[r] + 1;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (hi[r] >= from) to = min(to, lo[r]);
+    if (from < to && seg_of(from) == lane) seg_cnt = count_before(to) - count_before(from);
+  }
+  const int n = (int)(included - __reduce_add_sync(0xffffffffu, seg_cnt));  // candidates
+  const bool fits = n <= kCap;
+  const int segs = last < 0 ? 0 : seg_of(last) + 1;  // classes whose sums are wanted
+  seg_cnt = warp_upto(seg_cnt);
+  if (warp == 0 && lane < kSegs) S.base_cnt[lane] = seg_cnt;
+#pragma unroll 1
+  for (int s = 0; s < segs; ++s) S.second.acc[s][tid] = make_float2(0.f, 0.f);
+  __syncthreads();
 
   // ---- 3. exact sums, candidates
   if (fits) {
-    Pair sum[kSegs];
-    uint32_t n[kSegs] = {0u, 0u, 0u, 0u, 0u};
     const uint32_t cand0 = mapa_shared(smem_u32(&S.cand[0]), 0), count0 = mapa_shared(smem_u32(&S.ncand), 0);
-    each_logit(row, V, pad, c0, c1, [&](float x, int v) {
-      float at;
-      const int b = bin_of(x, at);
-      if (b > last) return;
-      const int cls = S.cls[b];
-      if (cls == 255) {
-        const uint32_t i = atom_cluster_add(count0, 1u);
-        if (i < kCap) st_cluster_u64(cand0 + 8 * i, ((unsigned long long)key_of(x) << 32) | (uint32_t)v);
-      } else {
-        const float2 w = weight(x, mx, A.ch, A.cl, S.table);
+    auto add = [&](int cls, float2 w) {
+      const float2 a = S.second.acc[cls][tid];
+      Pair p;
+      p.h = a.x;
+      p.l = a.y;
+      p.add(w);
+      S.second.acc[cls][tid] = make_float2(p.h, p.l);
+    };
+    each_chunk(row, V, pad, c0, c1, S.first.ring, [&](const float(&y)[4], int k) {
+      int cls[4];
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s)
-          if (cls == s) sum[s].add(w.x, w.y), ++n[s];
+      for (int e = 0; e < 4; ++e) {
+        cls[e] = kSegs;  // of no account
+        if (y[e] != -INFINITY && y[e] >= cut) {
+          float at;
+          const int b = bin_of(y[e], at);
+          if (b <= last) cls[e] = S.cls[b];
+        }
+      }
+      if (max(max(cls[0], cls[1]), max(cls[2], cls[3])) == 255) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const int c = e < 2 ? (e ? cls[1] : cls[0]) : (e == 2 ? cls[2] : cls[3]);
+          const float x = e < 2 ? (e ? y[1] : y[0]) : (e == 2 ? y[2] : y[3]);
+          if (c != 255) continue;
+          const uint32_t j = atom_cluster_add(count0, 1u);
+          if (j < kCap) st_cluster_u64(cand0 + 8 * j, ((unsigned long long)key_of(x) << 32) | (uint32_t)(4 * k - pad + e));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int a = h ? cls[2] : cls[0], b = h ? cls[3] : cls[1];
+        if (a < kSegs || b < kSegs) {
+          float2 w0, w1;
+          weights(W, a < kSegs ? (h ? y[2] : y[0]) : mx, b < kSegs ? (h ? y[3] : y[1]) : mx, w0, w1);
+          if (a < kSegs) add(a, w0);
+          if (b < kSegs) add(b, w1);
+        }
       }
     });
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s) {
-      const unsigned long long w = cta_sum(sum[s].fixed(), S.red64);
-      const uint32_t k = cta_sum(n[s], S.red32);
-      if (tid == 0) {
-        st_cluster_u64(mapa_shared(smem_u32(&S.seg_sum[rank][s]), 0), w);
-        st_cluster_u32(mapa_shared(smem_u32(&S.seg_cnt[rank][s]), 0), k);
-      }
+#pragma unroll 1
+    for (int s = 0; s < segs; ++s) {
+      Pair p;
+      p.h = S.second.acc[s][tid].x;
+      p.l = S.second.acc[s][tid].y;
+      const unsigned long long w = warp_sum(p.fixed());
+      if (lane == 0) S.red64[s][warp] = w;
+    }
+    __syncthreads();
+    if (tid < kSegs) {
+      unsigned long long w = 0;
+      if (tid < segs)
+#pragma unroll 4
+        for (int i = 0; i < kSaWarps; ++i) w += S.red64[tid][i];
+      st_cluster_u64(mapa_shared(smem_u32(&S.seg_sum[rank][tid]), 0), w);
     }
   }
   cluster_meet(C);
@@ -628,128 +841,142 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
 
   // ---- rank 0: the candidates in order, and the answers
   bool done = false;
-  if (fits) {
-    const int n = (int)listed;
-    int size = 32;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kSaThreads) S.cand[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < size; i += kSaThreads) {
-          const int o = i ^ j;
-          if (o > i) {
-            const unsigned long long a = S.cand[i], b = S.cand[o];
-            if ((a > b) == ((i & k) == 0)) S.cand[i] = b, S.cand[o] = a;
+  if (fits && S.ncand == (uint32_t)n) {
+    const unsigned long long* sorted = S.second.sorted;
+    if (n <= kSaThreads) {  // each finds its place by counting
+      if (tid < n) {
+        const unsigned long long own = S.cand[tid];
+        int place = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) place += S.cand[i] < own ? 1 : 0;
+        S.second.sorted[place] = own;
+      }
+    } else {
+      int size = kSaThreads;
+      while (size < n) size *= 2;
+      for (int i = n + tid; i < size; i += kSaThreads) S.cand[i] = ~0ull;
+      __syncthreads();
+      for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+          for (int i = tid; i < size / 2; i += kSaThreads) {
+            const int x = 2 * i - (i & (j - 1)), y = x + j;  // pairs j apart
+            const unsigned long long a = S.cand[x], b = S.cand[y];
+            if ((a > b) == ((x & k) == 0)) S.cand[x] = b, S.cand[y] = a;
           }
+          __syncthreads();
         }
-        __syncthreads();
-      }
-    unsigned long long base_w[kSegs];
-    uint32_t base_n[kSegs];
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s) {
-      base_w[s] = s ? base_w[s - 1] : 0ull;
-      base_n[s] = s ? base_n[s - 1] : 0u;
-      for (int r = 0; r < C; ++r) {
-        base_w[s] += S.seg_sum[r][s];
-        base_n[s] += S.seg_cnt[r][s];
-      }
+      sorted = S.cand;
     }
-    auto seg_of = [&](int b) {
-      int seg = 0;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) seg += S.hi[r] < b ? 1 : 0;
-      return seg;
-    };
-    // this thread's candidates: kCapPer consecutive ones
-    unsigned long long w[kCapPer], upto[kCapPer];
-    uint32_t place[kCapPer];
+    if (tid < kSegs) {
+      unsigned long long w = 0;
+#pragma unroll 1
+      for (int r = 0; r < C; ++r)
+        for (int i = 0; i <= tid; ++i) w += S.seg_sum[r][i];
+      S.base[tid] = w;
+    }
+    __syncthreads();
+    // This thread's candidates are `per` consecutive ones.
+    const int per = n <= kSaThreads ? 1 : kCapPer, j0 = tid * per, j1 = min(n, j0 + per);
     unsigned long long own = 0;
-#pragma unroll
-    for (int i = 0; i < kCapPer; ++i) {
-      const int j = tid * kCapPer + i;
-      w[i] = j < n ? weight_fixed(value_of((uint32_t)(S.cand[j] >> 32)), mx, A, S.table) : 0ull;
-      own += w[i];
-      upto[i] = own;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      const float2 f = weight(W, value_of(sorted[j]));
+      Pair p;
+      p.h = f.x;
+      p.l = f.y;
+      const unsigned long long w = p.fixed();
+      S.first.w[j] = w;
+      S.second.place[j] = with_m && at_least(f, A.a.min_p) ? 0x80000000u : 0u;
+      own += w;
     }
-    const unsigned long long before = cta_before(own, S.red64);
-    const unsigned long long listed_w = cta_sum(own, S.red64);
-#pragma unroll
-    for (int i = 0; i < kCapPer; ++i) {
-      const int j = tid * kCapPer + i;
-      place[i] = 0;
-      if (j < n) {
-        float at;
-        const int seg = seg_of(bin_of(value_of((uint32_t)(S.cand[j] >> 32)), at));
-        unsigned long long bw = 0;
-        uint32_t bn = 0;
-#pragma unroll
-        for (int s = 0; s < kSegs; ++s)
-          if (s == seg) bw = base_w[s], bn = base_n[s];
-        upto[i] += before + bw;
-        place[i] = bn + (uint32_t)j + 1u;
-      }
+    unsigned long long c = warp_upto(own);
+    if (lane == 31) S.red64[0][warp] = c;
+    __syncthreads();
+    c += warp_sum(lane < warp ? S.red64[0][lane & (kSaWarps - 1)] : 0ull) - own;
+    const unsigned long long listed = warp_sum(lane < kSaWarps ? S.red64[0][lane] : 0ull);
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      c += S.first.w[j];
+      float at;
+      const int seg = seg_of(bin_of(value_of(sorted[j]), at));
+      S.first.upto[j] = S.base[seg] + c;
+      S.second.place[j] |= S.base_cnt[seg] + (uint32_t)j + 1u;
     }
+    __syncthreads();
     uint32_t n_keep = finite;
-    unsigned long long s_keep = base_w[kSegs - 1] + listed_w;  // of all, where `all`
-    bool ok = true;
+    unsigned long long s_keep = S.base[kSegs - 1] + listed;  // of all, where `all`
+    bool ok = true, rest;
     if (with_k) {
-#pragma unroll
-      for (int i = 0; i < kCapPer; ++i)
-        if (place[i] == (uint32_t)A.a.top_k) S.s_k = upto[i], S.found[0] = 1;
+#pragma unroll 1
+      for (int j = tid; j < n; j += kSaThreads)
+        if ((S.second.place[j] & 0x7FFFFFFFu) == (uint32_t)A.a.top_k) S.s_k = S.first.upto[j], S.found[0] = 1;
       __syncthreads();
       ok = S.found[0] != 0;
       n_keep = (uint32_t)A.a.top_k;
       s_keep = S.s_k;
     }
     if (with_p && ok) {
-      const double t = (double)A.a.top_p * (double)s_keep;
-#pragma unroll
-      for (int i = 0; i < kCapPer; ++i)
-        if (place[i] > 0 && (double)upto[i] >= t && (place[i] == 1 || (double)(upto[i] - w[i]) < t))
-          S.n_p = place[i], S.s_p = upto[i], S.found[1] = 1;
+      unsigned long long t = times(s_keep, A.a.top_p, rest);
+      t += rest ? 1u : 0u;
+#pragma unroll 1
+      for (int j = tid; j < n; j += kSaThreads) {
+        const unsigned long long to = S.first.upto[j];
+        const uint32_t place = S.second.place[j] & 0x7FFFFFFFu;
+        if (to >= t && (place == 1u || to - S.first.w[j] < t)) S.n_p = place, S.s_p = to, S.found[1] = 1;
+      }
       __syncthreads();
       ok = S.found[1] != 0;
       if (S.n_p < n_keep) n_keep = S.n_p, s_keep = S.s_p;
     }
     if (with_m && ok) {
       // those before the range in the bins are all large enough
-      uint32_t c = 0;
-      unsigned long long cw = 0;
-#pragma unroll
-      for (int i = 0; i < kCapPer; ++i)
-        if (place[i] > 0 && at_least(weight(value_of((uint32_t)(S.cand[tid * kCapPer + i] >> 32)), mx, A.ch, A.cl, S.table),
-                                     A.a.min_p))
-          ++c, cw += w[i];
-      c = cta_sum(c, S.red32);
-      cw = cta_sum(cw, S.red64);
-      const int seg = seg_of(S.lo[2]);
-#pragma unroll
-      for (int s = 0; s < kSegs; ++s)
-        if (s == seg) c += base_n[s], cw += base_w[s];
-      if (c < n_keep) n_keep = c, s_keep = cw;
+      uint32_t large = 0;
+      unsigned long long sum = 0;
+#pragma unroll 1
+      for (int j = tid; j < n; j += kSaThreads)
+        if (S.second.place[j] >> 31) ++large, sum += S.first.w[j];
+      large = cta_sum(large, S.red32) + S.base_cnt[seg_of(lo[2])];
+      sum = cta_sum(sum, S.red64[0]) + S.base[seg_of(lo[2])];
+      if (large < n_keep) n_keep = large, s_keep = sum;
     }
     if (ok) {
-      const double t = (double)u * (double)s_keep;
-#pragma unroll
-      for (int i = 0; i < kCapPer; ++i)
-        if (place[i] > 0 && place[i] <= n_keep && (double)upto[i] > t && (double)(upto[i] - w[i]) <= t) {
-          A.a.token[m] = (int32_t)(uint32_t)S.cand[tid * kCapPer + i];
-          if (A.a.logprob) A.a.logprob[m] = (float)log((double)w[i] / (double)s_keep);
+      const unsigned long long t = times(s_keep, u, rest);
+#pragma unroll 1
+      for (int j = tid; j < n; j += kSaThreads) {
+        const unsigned long long to = S.first.upto[j];
+        if ((S.second.place[j] & 0x7FFFFFFFu) <= n_keep && to > t && to - S.first.w[j] <= t) {
+          const unsigned long long order = sorted[j];
+          A.a.token[m] = (int32_t)(uint32_t)order;
+          if (A.a.logprob) A.a.logprob[m] = share_log(value_of(order), mx, T, s_keep);
           if (A.a.kept) A.a.kept[m] = (int32_t)n_keep;
           S.found[3] = 1;
         }
+      }
       __syncthreads();
       done = S.found[3] != 0;
     }
   }
-  if (!done) sample_slowly(A, S, row, pad, mx, finite, u, m);
+  if (!done) sample_slowly(A, S, Row{row, V, pad, W}, finite, u, m);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
+  static const SaTable table = [] {  // made once for the process
+    SaTable t;
+    for (int i = 0; i < 256; ++i) {
+      const double x = std::exp2(-i / 256.0);
+      t.h[i] = (float)x;
+      t.l[i] = (float)(x - (double)t.h[i]);
+    }
+    return t;
+  }();
+  SaArgs A;
+  A.a = a;
+  const double c = a.temperature > 0.f ? 256.0 * 1.4426950408889634 / (double)a.temperature : 0.0;
+  A.ch = (float)c;
+  A.cl = (float)(c - (double)A.ch);
+  A.table = table;
   static PerDeviceFlag attr_set;
   const int dev = current_device();
   if (!attr_set.done(dev)) {
@@ -758,24 +985,8 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
-  SaArgs A;
-  A.a = a;
-  const double c = a.temperature > 0.f ? 256.0 * 1.4426950408889634 / (double)a.temperature : 0.0;
-  A.ch = (float)c;
-  A.cl = (float)(c - (double)A.ch);
-  static const SaTable table = [] {
-    SaTable t;
-    for (int i = 0; i < 256; ++i) {
-      const double x = std::exp2(-i / 256.0);
-      t.t[i].x = (float)x;
-      t.t[i].y = (float)(x - (double)t.t[i].x);
-    }
-    return t;
-  }();
-  A.table = table;
-  // CTAs for two on every SM at most, with a few thousand logits each at least.
   int C = 1;
-  while (C < kSaMaxCluster && a.M * 2 * C <= 2 * (int64_t)device_sms() && a.V >= 2048 * 2 * C) C *= 2;
+  while (C < kSaMaxCluster && a.M * 2 * C <= (C < 8 ? 2 * (int64_t)device_sms() : 64) && a.V >= 2048 * 2 * C) C *= 2;
   A.C = C;
   return launch_dependent(sample_kernel, dim3((unsigned)(a.M * C)), kSaThreads, sizeof(SaShared), (unsigned)C, s, A);
 }
