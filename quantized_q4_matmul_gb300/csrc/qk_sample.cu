@@ -52,6 +52,7 @@ constexpr int kCap = 2048;  // candidates
 constexpr int kCapPer = kCap / kSaThreads;
 constexpr int kWhole = kSaThreads;  // a kept set of at most so many is listed whole
 constexpr int kSegs = 5;
+constexpr int kNone = kSegs, kListed = kSegs + 1;  // classes of logits of no account, and of candidates
 constexpr float kOne = 17592186044416.f;  // 2^44: the largest weight
 constexpr float kMagic = 12582912.f;      // 1.5 2^23: adding it rounds to an integer in the low bits
 constexpr float kSlack = 6e-5f;           // of the histogram's sums, relative
@@ -92,7 +93,7 @@ union SaFirst {
 };
 union SaSecond {
   float4 ring[kRing][kSaThreads];  // until the sums
-  float2 acc[kSegs][kSaThreads];   // sums of weights
+  float2 acc[kSegs + 2][kSaThreads];  // sums of weights; those of kNone and kListed are not used
   struct {                         // answers: the candidates in order, their places; bit 31 is min_p's
     unsigned long long sorted[kCap];
     uint32_t place[kCap];
@@ -120,7 +121,7 @@ static_assert(sizeof(SaShared) % 16 == 0 && kBinsPer == 8, "16-byte accesses");
 
 // Ascending in the order of the tokens: by the logit from the largest, then by the token.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));  // -0 is 0
   return (b >> 31) ? b : ~(b | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
@@ -278,18 +279,21 @@ __device__ __forceinline__ T warp_upto(T x) {
 
 // Calls f(four logits, chunk) for this thread's chunks c0 + threadIdx.x, ... below c1
 // of a row.  A chunk is 16 aligned bytes; the first has `pad` values before the row.
-// Where there is no logit it has -inf; -0 is 0.  Chunks come through the thread's
+// Where there is no logit it has -inf.  Chunks come through the thread's
 // places in `ring`, kRing - 1 of them on their way.  Past its last one a thread's
 // logits are -inf.
 template <typename F>
 __device__ __forceinline__ void each_chunk(const float* row, int V, int pad, int c0, int c1,
                                            float4 (*ring)[kSaThreads], F f) {
   const int tid = threadIdx.x;
-  auto fetch = [&](int k, int slot) {
+  const int whole = (V + pad) / 4;  // chunks 1 .. whole - 1 lie within the row
+  const float* at = row - pad + 4 * (int64_t)(c0 + tid);
+  const uint32_t to = smem_u32(&ring[0][tid]);
+  int k = c0 + tid;  // the next chunk to fetch
+  auto fetch = [&](int slot) {
     if (k < c1) {
-      float4* to = &ring[slot][tid];
-      if (k > 0 && 4 * k + 3 - pad < V) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(row - pad + 4 * (int64_t)k)
+      if ((unsigned)(k - 1) < (unsigned)(whole - 1)) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (uint32_t)(slot * kSaThreads * 16)), "l"(at)
                      : "memory");
       } else {  // the row's ends
         const int v = 4 * k - pad;
@@ -298,23 +302,25 @@ __device__ __forceinline__ void each_chunk(const float* row, int V, int pad, int
         if (v + 1 >= 0 && v + 1 < V) x.y = __ldg(row + v + 1);
         if (v + 2 >= 0 && v + 2 < V) x.z = __ldg(row + v + 2);
         if (v + 3 >= 0 && v + 3 < V) x.w = __ldg(row + v + 3);
-        *to = x;
+        ring[slot][tid] = x;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    k += kSaThreads;
+    at += 4 * kSaThreads;
   };
   int c = c0 + tid;
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) fetch(c + i * kSaThreads, i);
+  for (int i = 0; i < kRing - 1; ++i) fetch(i);
   int slot = 0;
 #pragma unroll 1
   for (; c - (tid & 31) < c1; c += kSaThreads) {  // as often for all lanes
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
     float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     if (c < c1) x = ring[slot][tid];
-    fetch(c + (kRing - 1) * kSaThreads, (slot + kRing - 1) & (kRing - 1));
+    fetch((slot + kRing - 1) & (kRing - 1));
     slot = (slot + 1) & (kRing - 1);
-    const float y[4] = {__fadd_rn(x.x, 0.f), __fadd_rn(x.y, 0.f), __fadd_rn(x.z, 0.f), __fadd_rn(x.w, 0.f)};
+    const float y[4] = {x.x, x.y, x.z, x.w};
     f(y, c);
     __syncwarp();  // lanes that f parted go on together
   }
@@ -465,12 +471,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // The bin of the histogram in which sums from the first token on reach `target`, at
-// least 1: the last one with less before it.
+// least 1: the last one with less before it.  By a warp.
 __device__ __forceinline__ int reach(const uint32_t* before, uint32_t target) {
+  const int lane = threadIdx.x & 31;
   int b = 0;
-#pragma unroll 1
-  for (int step = kBins / 2; step > 0; step /= 2)
-    if (before[b + step] < target) b += step;
+#pragma unroll
+  for (int step = kBins / 32; step > 0; step = step == 4 ? 1 : step / 32)  // 128, 4, 1
+    b += step * (__popc(__ballot_sync(0xffffffffu, (step > 1 || lane < 4) && before[b + step * lane] < target)) - 1);
   return b;
 }
 
@@ -597,7 +604,9 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
   const float span = fminf(mx - mn, 31.f * T);
   const float scale = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;
-  if (!with_k || A.a.top_k > kSaThreads) cut = -INFINITY;  // each thread's maximum reaches the cut
+  // Logits below the cut, -inf among them, are of no account; each thread's maximum reaches it.
+  if (!with_k || A.a.top_k > kSaThreads) cut = -INFINITY;
+  cut = fmaxf(cut, -3.4028235e38f);
   const float log_m = with_m ? -logf(A.a.min_p) * T : 0.f;
   if (with_m && !with_p) cut = fmaxf(cut, mx - log_m * 1.001f - 4.f * span / (float)kBins);
   auto bin_of = [&](float x, float& at) {  // the nearest bin, and the position less it
@@ -610,7 +619,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (y[e] != -INFINITY && y[e] >= cut) {
+      if (y[e] >= cut) {
         float at;
         const int b = bin_of(y[e], at);
         atomicAdd(&S.first.cnt[b], 1u);
@@ -698,13 +707,11 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   auto count_before = [&](int b) { return b < kBins ? S.first.cnt[b] : included; };
 
   // The bins where the borders are: ranges [lo, hi] for k, p, m and the token.  Every
-  // thread finds them; lanes 0 and 1 of a pair search the two ends.
+  // warp finds them.
   int lo[4] = {kBins, kBins, kBins, kBins}, hi[4] = {kBins, kBins, kBins, kBins};
   auto range = [&](float from, float to, int& first, int& last) {
-    const float t = lane & 1 ? to : from;
-    const int b = reach(S.first.frac, t > 1.f ? (uint32_t)t : 1u);
-    first = __shfl_sync(0xffffffffu, b, 0);
-    last = __shfl_sync(0xffffffffu, b, 1);
+    first = reach(S.first.frac, from > 1.f ? (uint32_t)from : 1u);
+    last = reach(S.first.frac, to > 1.f ? (uint32_t)to : 1u);
   };
   float s_lo = (float)total, s_hi = s_lo;  // the kept weights, within kSlack
   int b_hi = kBins - 1;                    // the last bin that may hold the last kept token
@@ -739,8 +746,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     const float slack = kSlack * (float)total + 8.f;
     range(u * s_lo - slack, u * s_hi + slack, lo[3], hi[3]);
   }
-  // Classes of the bins: 255 for the candidates', else how many of the ranges end
-  // before.
+  // Classes of the bins: kListed for the candidates', else how many of the ranges
+  // end before.
   const bool all = !with_k && (with_p || !with_m);  // every weight counts
   int last = all ? kBins - 1 : -1;                  // the last bin that matters
 #pragma unroll
@@ -752,7 +759,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     bool in = false;
 #pragma unroll
     for (int r = 0; r < 4; ++r) in = in || (b >= lo[r] && b <= hi[r]);
-    S.cls[b] = in ? 255 : (uint8_t)seg_of(b);
+    S.cls[b] = (uint8_t)(in ? kListed : seg_of(b));
   }
   // Lane s: the tokens of class s, whose bins are those behind the s-th range to end
   // and before the first of the ranges that end later.
@@ -791,31 +798,30 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       int cls[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        cls[e] = kSegs;  // of no account
-        if (y[e] != -INFINITY && y[e] >= cut) {
+        cls[e] = kNone;
+        if (y[e] >= cut) {
           float at;
           const int b = bin_of(y[e], at);
           if (b <= last) cls[e] = S.cls[b];
         }
       }
-      if (max(max(cls[0], cls[1]), max(cls[2], cls[3])) == 255) {
+      if (max(max(cls[0], cls[1]), max(cls[2], cls[3])) == kListed) {
 #pragma unroll 1
         for (int e = 0; e < 4; ++e) {
           const int c = e < 2 ? (e ? cls[1] : cls[0]) : (e == 2 ? cls[2] : cls[3]);
           const float x = e < 2 ? (e ? y[1] : y[0]) : (e == 2 ? y[2] : y[3]);
-          if (c != 255) continue;
+          if (c != kListed) continue;
           const uint32_t j = atom_cluster_add(count0, 1u);
           if (j < kCap) st_cluster_u64(cand0 + 8 * j, ((unsigned long long)key_of(x) << 32) | (uint32_t)(4 * k - pad + e));
         }
       }
+      if (min(min(cls[0], cls[1]), min(cls[2], cls[3])) < kSegs) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int a = h ? cls[2] : cls[0], b = h ? cls[3] : cls[1];
-        if (a < kSegs || b < kSegs) {
+        for (int e = 0; e < 4; e += 2) {  // the weight of a logit that is not wanted goes to a sum that is not either
           float2 w0, w1;
-          weights(W, a < kSegs ? (h ? y[2] : y[0]) : mx, b < kSegs ? (h ? y[3] : y[1]) : mx, w0, w1);
-          if (a < kSegs) add(a, w0);
-          if (b < kSegs) add(b, w1);
+          weights(W, y[e], y[e + 1], w0, w1);
+          add(cls[e], w0);
+          add(cls[e + 1], w1);
         }
       }
     });
@@ -867,12 +873,12 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
         }
       sorted = S.cand;
     }
-    if (tid < kSegs) {
+    if (warp < kSegs) {
       unsigned long long w = 0;
 #pragma unroll 1
-      for (int r = 0; r < C; ++r)
-        for (int i = 0; i <= tid; ++i) w += S.seg_sum[r][i];
-      S.base[tid] = w;
+      for (int i = 0; i <= warp; ++i) w += lane < C ? S.seg_sum[lane][i] : 0ull;
+      w = warp_sum(w);
+      if (lane == 0) S.base[warp] = w;
     }
     __syncthreads();
     // This thread's candidates are `per` consecutive ones.
