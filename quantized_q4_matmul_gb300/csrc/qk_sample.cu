@@ -19,11 +19,14 @@
 //
 // A cluster of C CTAs has a row and goes over it three times (it stays in L2; kept
 // in shared memory it was no faster):
-//   1. its maximum and minimum, and whether it can be sampled from;
+//   1. its maximum and minimum, and whether it can be sampled from.  Where top_k (up
+//      to 512) or min_p alone bounds what is kept, a second pass lists the tokens
+//      above a cut, the least of the CTAs' top_k / C-th largest of their threads'
+//      maxima (so that top_k tokens lie above it, and few more) or min_p's border
+//      with a margin: they are the candidates, and nothing else is needed.  Otherwise, or where they are many:
 //   2. a histogram over (max - x) of counts and mean positions within a bin, from
 //      which the bins that hold the three borders and the token follow, the sums
-//      being known to some 1e-5.  With top_k, logits below the least of the
-//      threads' maxima are left out;
+//      being known to some 1e-5.  Logits below the cut are left out;
 //   3. the exact sums of what lies before, between and behind those bins, and a
 //      list of the tokens in them (candidates).
 // Rank 0 sorts the candidates, adds their weights up and answers the questions in
@@ -75,7 +78,7 @@ struct SaArgs {
 struct SaStat {
   float mx;         // largest logit; NaN where one is
   float mn;         // least finite logit
-  float cut;        // least of the threads' maxima
+  float cut;        // the top_k / C-th largest of the threads' maxima
   uint32_t finite;  // logits but -inf
 };
 
@@ -93,6 +96,7 @@ union SaFirst {
 };
 union SaSecond {
   float4 ring[kRing][kSaThreads];  // until the sums
+  float maxima[kSaThreads];        // the threads'
   float2 acc[kSegs + 2][kSaThreads];  // sums of weights; those of kNone and kListed are not used
   struct {                         // answers: the candidates in order, their places; bit 31 is min_p's
     unsigned long long sorted[kCap];
@@ -115,7 +119,8 @@ struct alignas(16) SaShared {
   float redf[3][kSaWarps];
   uint32_t base_cnt[kSegs];  // tokens of the classes up to each
   int found[4];
-  uint32_t ncand, n_p, best, included, total;
+  uint32_t ncand, n_p, best, included, total, listed;
+  uint32_t listed_by[kSaMaxCluster];
 };
 static_assert(sizeof(SaShared) % 16 == 0 && kBinsPer == 8, "16-byte accesses");
 
@@ -505,11 +510,11 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     S.table.l[tid] = A.table.l[tid];
   }
   if (tid < 4) S.found[tid] = 0;
-  if (tid == 0) S.ncand = 0u, S.best = 0xFFFFFFFFu;
+  if (tid == 0) S.ncand = S.listed = 0u, S.best = 0xFFFFFFFFu;
   dependent_wait();
 
   // ---- 1. the largest and the least finite logit
-  float mx = -INFINITY, mn = INFINITY, cut;
+  float mx = -INFINITY, mn = INFINITY, cut = -INFINITY;
   uint32_t finite = 0;
   each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
 #pragma unroll
@@ -520,19 +525,35 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       finite += is ? 1u : 0u;
     }
   });
-  cut = mx;
+  const bool by_k = A.a.top_k > 0 && A.a.top_k <= kSaThreads;
+  const float own = mx;
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
   }
   finite = __reduce_add_sync(0xffffffffu, finite);
   if (lane == 0) {
     S.redf[0][warp] = mx;
     S.redf[1][warp] = mn;
-    S.redf[2][warp] = cut;
     S.red32[warp] = finite;
+  }
+  if (by_k) {  // the share-th largest of this CTA's maxima: the least that fewer than `share` are larger than
+    const int share = (A.a.top_k + C - 1) / C;  // C CTAs' together are top_k logits at least
+    __syncthreads();  // the rings are idle
+    S.second.maxima[tid] = own;
+    __syncthreads();
+    int larger = 0;
+    const float4* maxima = reinterpret_cast<const float4*>(S.second.maxima);
+#pragma unroll 4
+    for (int i = 0; i < kSaThreads / 4; ++i) {
+      const float4 x = maxima[i];
+      larger += (x.x > own) + (x.y > own) + (x.z > own) + (x.w > own);
+    }
+    float least = larger < share ? own : INFINITY;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) S.redf[2][warp] = least;
   }
   __syncthreads();  // also: the histogram is clear
   if (C > 1) {
@@ -543,7 +564,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     const int i = lane & (kSaWarps - 1);
     mx = S.redf[0][i];
     mn = S.redf[1][i];
-    cut = S.redf[2][i];
+    cut = by_k ? S.redf[2][i] : -INFINITY;
     finite = lane < kSaWarps ? S.red32[i] : 0u;
 #pragma unroll 1
     for (int o = kSaWarps / 2; o > 0; o >>= 1) {
@@ -558,7 +579,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   }
   cluster_meet(C);
   {
-    SaStat st{-INFINITY, INFINITY, -INFINITY, 0u};
+    SaStat st{-INFINITY, INFINITY, INFINITY, 0u};
     if (lane < C) st = S.stat[lane];
     mx = st.mx;
     mn = st.mn;
@@ -567,7 +588,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     for (int o = 16; o > 0; o >>= 1) {
       mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+      cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
     }
     finite = __reduce_add_sync(0xffffffffu, st.finite);
   }
@@ -599,255 +620,297 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
   const Weigh W{mx, 83.f * T, A.ch, A.cl, &S.table};
 
-  // ---- 2. the histogram.  Logits further than 31 T below the maximum are in the last
-  // bin; those that cannot be kept are left out.
   const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
   const float span = fminf(mx - mn, 31.f * T);
   const float scale = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;
-  // Logits below the cut, -inf among them, are of no account; each thread's maximum reaches it.
-  if (!with_k || A.a.top_k > kSaThreads) cut = -INFINITY;
+  // Logits below the cut, -inf among them, are of no account.
+  if (!with_k || !by_k) cut = -INFINITY;
   cut = fmaxf(cut, -3.4028235e38f);
   const float log_m = with_m ? -logf(A.a.min_p) * T : 0.f;
-  if (with_m && !with_p) cut = fmaxf(cut, mx - log_m * 1.001f - 4.f * span / (float)kBins);
+  if (with_m && !with_p && !with_k) cut = fmaxf(cut, mx - log_m * 1.001f - 4.f * span / (float)kBins);
   auto bin_of = [&](float x, float& at) {  // the nearest bin, and the position less it
     at = fminf(__fmul_rn(__fsub_rn(mx, x), scale), (float)(kBins - 1));
     const float mag = __fadd_rn(at, kMagic);
     at = __fsub_rn(at, __fsub_rn(mag, kMagic));
     return (int)(__float_as_uint(mag) & (uint32_t)(kBins - 1));
   };
-  const float means = mx - kMeans * T;
-  each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (y[e] >= cut) {
-        float at;
-        const int b = bin_of(y[e], at);
-        atomicAdd(&S.first.cnt[b], 1u);
-        if (y[e] >= means)  // (at + 1/2) 4096
-          atomicAdd(&S.first.frac[b], __float_as_uint(__fmaf_rn(at, 4096.f, kMagic + 2048.f)) - 0x4B400000u);
-      }
-  });
-  if (C > 1) {
-    cluster_meet(C);
-    // Each rank adds up a run of bins of all CTAs and gives each CTA the sums; a bin
-    // is read by its own rank alone, so it may be overwritten at once.
-    const int mine = kBins / 2 / C;  // pairs of bins
-#pragma unroll 1
-    for (int i = tid; i < 2 * mine; i += kSaThreads) {
-      const uint32_t at = smem_u32(i < mine ? &S.first.cnt[2 * (rank * mine + i)] : &S.first.frac[2 * (rank * mine + i - mine)]);
-      uint2 n = make_uint2(0u, 0u);
-#pragma unroll 1
-      for (int r0 = 0; r0 < C; r0 += 8) {
-        uint2 x[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) x[r] = r0 + r < C ? ld_cluster_v2(mapa_shared(at, (uint32_t)(r0 + r))) : make_uint2(0u, 0u);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) n.x += x[r].x, n.y += x[r].y;
-      }
-#pragma unroll 4
-      for (int r = 0; r < C; ++r) st_cluster_v2(mapa_shared(at, (uint32_t)r), n);
-    }
-  }
-  cluster_meet(C);
-
-  // What lies before each bin: tokens, and weights as integers, 2^31 in all, so that
-  // no thread's sums differ from another's.  This thread's bins are kBinsPer
-  // consecutive ones.
-  const float per_bin = scale > 0.f ? 1.44269504f / (T * scale) : 0.f;  // octaves
-  {
-    uint4* cnt = reinterpret_cast<uint4*>(S.first.cnt) + 2 * tid;
-    uint4* frac = reinterpret_cast<uint4*>(S.first.frac) + 2 * tid;
-    const uint4 k0 = cnt[0], k1 = cnt[1], q0 = frac[0], q1 = frac[1];
-    uint32_t k[kBinsPer] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-    uint32_t q[kBinsPer] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-    float f[kBinsPer], sum = 0.f;
-    uint32_t cn = 0;
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) {
-      // the middle where no positions were added (with any, the sum is not 0: bin 0's are 1/2 and more)
-      const float kf = (float)k[i], mean = q[i] ? __fdividef((float)q[i], 4096.f * kf) - 0.5f : 0.f;
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f[i]) : "f"(-per_bin * ((float)(tid * kBinsPer + i) + mean)));
-      f[i] *= kf;
-      sum += f[i];
-      cn += k[i];
-    }
-    const float part = warp_sum(sum);
-    if (lane == 0) S.redf[0][warp] = part;
-    __syncthreads();
-    const float all = warp_sum(lane < kSaWarps ? S.redf[0][lane] : 0.f);
-    const float per_unit = 2147000000.f / all;  // the roundings of kBins sums stay below 2^31
-    uint32_t cf = 0;
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) {
-      q[i] = __float2uint_rn(f[i] * per_unit);
-      cf += q[i];
-    }
-    uint32_t xn = warp_upto(cn), xf = warp_upto(cf);
-    if (lane == 31) S.red32[warp] = xn, S.redf[1][warp] = __uint_as_float(xf);
-    __syncthreads();
-    xn += __reduce_add_sync(0xffffffffu, lane < warp ? S.red32[lane & (kSaWarps - 1)] : 0u) - cn;
-    xf += __reduce_add_sync(0xffffffffu, lane < warp ? __float_as_uint(S.redf[1][lane & (kSaWarps - 1)]) : 0u) - cf;
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) {
-      const uint32_t n = k[i], w = q[i];
-      k[i] = xn;
-      q[i] = xf;
-      xn += n;
-      xf += w;
-    }
-    cnt[0] = make_uint4(k[0], k[1], k[2], k[3]);
-    cnt[1] = make_uint4(k[4], k[5], k[6], k[7]);
-    frac[0] = make_uint4(q[0], q[1], q[2], q[3]);
-    frac[1] = make_uint4(q[4], q[5], q[6], q[7]);
-    if (tid == kSaThreads - 1) S.included = xn, S.total = xf;
-  }
-  __syncthreads();
-  const uint32_t included = S.included, total = S.total;
-  auto sum_before = [&](int b) { return (float)(b < kBins ? S.first.frac[b] : total); };
-  auto count_before = [&](int b) { return b < kBins ? S.first.cnt[b] : included; };
-
-  // The bins where the borders are: ranges [lo, hi] for k, p, m and the token.  Every
-  // warp finds them.
   int lo[4] = {kBins, kBins, kBins, kBins}, hi[4] = {kBins, kBins, kBins, kBins};
-  auto range = [&](float from, float to, int& first, int& last) {
-    first = reach(S.first.frac, from > 1.f ? (uint32_t)from : 1u);
-    last = reach(S.first.frac, to > 1.f ? (uint32_t)to : 1u);
-  };
-  float s_lo = (float)total, s_hi = s_lo;  // the kept weights, within kSlack
-  int b_hi = kBins - 1;                    // the last bin that may hold the last kept token
-  if (with_k) {
-    lo[0] = hi[0] = b_hi = reach(S.first.cnt, (uint32_t)A.a.top_k);
-    s_lo = sum_before(b_hi);
-    s_hi = sum_before(b_hi + 1);
-  }
-  if (with_p) {
-    const float slack = kSlack * s_hi + 8.f;
-    range(A.a.top_p * s_lo - slack, A.a.top_p * s_hi + slack, lo[1], hi[1]);
-    s_lo *= A.a.top_p;
-    if (hi[1] < b_hi) {
-      b_hi = hi[1];
-      s_hi = sum_before(b_hi + 1);
-    }
-  }
-  if (with_m) {
-    const int b = (int)fminf(log_m * scale, (float)(kBins - 1));
-    lo[2] = max(0, b - 1);
-    hi[2] = min(kBins - 1, b + 2);
-    s_lo = fminf(s_lo, sum_before(lo[2]));
-    if (hi[2] < b_hi) {
-      b_hi = hi[2];
-      s_hi = sum_before(b_hi + 1);
-    }
-  }
-  if (count_before(b_hi + 1) <= kWhole) {
-    lo[3] = 0;
-    hi[3] = b_hi;
-  } else {
-    const float slack = kSlack * (float)total + 8.f;
-    range(u * s_lo - slack, u * s_hi + slack, lo[3], hi[3]);
-  }
-  // Classes of the bins: kListed for the candidates', else how many of the ranges
-  // end before.
-  const bool all = !with_k && (with_p || !with_m);  // every weight counts
-  int last = all ? kBins - 1 : -1;                  // the last bin that matters
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (hi[r] < kBins) last = max(last, hi[r]);
   auto seg_of = [&](int b) { return (hi[0] < b) + (hi[1] < b) + (hi[2] < b) + (hi[3] < b); };
+  const uint32_t cand0 = mapa_shared(smem_u32(&S.cand[0]), 0), count0 = mapa_shared(smem_u32(&S.ncand), 0);
+  auto list = [&](float x, int v) {  // a candidate, to rank 0; false where there is no room
+    const uint32_t j = atom_cluster_add(count0, 1u);
+    if (j < kCap) st_cluster_u64(cand0 + 8 * j, ((unsigned long long)key_of(x) << 32) | (uint32_t)v);
+    return j < kCap;
+  };
+  int n = kCap + 1;  // candidates
+  const bool direct = (with_k && by_k) || (with_m && !with_p && !with_k);
+  if (direct) {
+    uint32_t mine = 0;
+    bool room = true;
+    each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int k) {
+      if (fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) < cut) return;
 #pragma unroll 1
-  for (int b = tid; b < kBins; b += kSaThreads) {
-    bool in = false;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) in = in || (b >= lo[r] && b <= hi[r]);
-    S.cls[b] = (uint8_t)(in ? kListed : seg_of(b));
-  }
-  // Lane s: the tokens of class s, whose bins are those behind the s-th range to end
-  // and before the first of the ranges that end later.
-  uint32_t seg_cnt = 0;
-  if (lane < kSegs) {
-    int from = lane ? kBins : 0, to = kBins;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (lane && hi[r] < kBins && seg_of(hi[r]) < lane && seg_of(hi[r] + 1) >= lane) from = hi[r] + 1;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (hi[r] >= from) to = min(to, lo[r]);
-    if (from < to && seg_of(from) == lane) seg_cnt = count_before(to) - count_before(from);
-  }
-  const int n = (int)(included - __reduce_add_sync(0xffffffffu, seg_cnt));  // candidates
-  const bool fits = n <= kCap;
-  const int segs = last < 0 ? 0 : seg_of(last) + 1;  // classes whose sums are wanted
-  seg_cnt = warp_upto(seg_cnt);
-  if (warp == 0 && lane < kSegs) S.base_cnt[lane] = seg_cnt;
-#pragma unroll 1
-  for (int s = 0; s < segs; ++s) S.second.acc[s][tid] = make_float2(0.f, 0.f);
-  __syncthreads();
-
-  // ---- 3. exact sums, candidates
-  if (fits) {
-    const uint32_t cand0 = mapa_shared(smem_u32(&S.cand[0]), 0), count0 = mapa_shared(smem_u32(&S.ncand), 0);
-    auto add = [&](int cls, float2 w) {
-      const float2 a = S.second.acc[cls][tid];
-      Pair p;
-      p.h = a.x;
-      p.l = a.y;
-      p.add(w);
-      S.second.acc[cls][tid] = make_float2(p.h, p.l);
-    };
-    each_chunk(row, V, pad, c0, c1, S.first.ring, [&](const float(&y)[4], int k) {
-      int cls[4];
-#pragma unroll
       for (int e = 0; e < 4; ++e) {
-        cls[e] = kNone;
+        const float x = e < 2 ? (e ? y[1] : y[0]) : (e == 2 ? y[2] : y[3]);
+        if (x < cut) continue;
+        ++mine;
+        if (room) room = list(x, 4 * k - pad + e);
+      }
+    });
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0 && mine) atomicAdd(&S.listed, mine);
+    __syncthreads();
+    if (tid < C)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S.listed_by[rank]), (uint32_t)tid)),
+                   "r"(S.listed)
+                   : "memory");
+    cluster_meet(C);
+    n = (int)min(__reduce_add_sync(0xffffffffu, lane < C ? S.listed_by[lane] : 0u), (uint32_t)kCap + 1u);
+  }
+  const bool listed_all = n <= kCap;  // everything from the cut on
+  int segs = 0;
+  if (listed_all) {
+    if (rank != 0) return;
+    if (tid < kSegs) S.base[tid] = 0ull, S.base_cnt[tid] = 0u;
+  } else {
+    // ---- 2. the histogram.  Logits further than 31 T below the maximum are in the last
+    // bin; those that cannot be kept are left out.
+    const float means = mx - kMeans * T;
+    if (rank == 0 && tid == 0) S.ncand = 0u;  // what did not fit is listed again
+    each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
         if (y[e] >= cut) {
           float at;
           const int b = bin_of(y[e], at);
-          if (b <= last) cls[e] = S.cls[b];
+          atomicAdd(&S.first.cnt[b], 1u);
+          if (y[e] >= means)  // (at + 1/2) 4096
+            atomicAdd(&S.first.frac[b], __float_as_uint(__fmaf_rn(at, 4096.f, kMagic + 2048.f)) - 0x4B400000u);
         }
-      }
-      if (max(max(cls[0], cls[1]), max(cls[2], cls[3])) == kListed) {
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          const int c = e < 2 ? (e ? cls[1] : cls[0]) : (e == 2 ? cls[2] : cls[3]);
-          const float x = e < 2 ? (e ? y[1] : y[0]) : (e == 2 ? y[2] : y[3]);
-          if (c != kListed) continue;
-          const uint32_t j = atom_cluster_add(count0, 1u);
-          if (j < kCap) st_cluster_u64(cand0 + 8 * j, ((unsigned long long)key_of(x) << 32) | (uint32_t)(4 * k - pad + e));
-        }
-      }
-      if (min(min(cls[0], cls[1]), min(cls[2], cls[3])) < kSegs) {
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {  // the weight of a logit that is not wanted goes to a sum that is not either
-          float2 w0, w1;
-          weights(W, y[e], y[e + 1], w0, w1);
-          add(cls[e], w0);
-          add(cls[e + 1], w1);
-        }
-      }
     });
+    if (C > 1) {
+      cluster_meet(C);
+      // Each rank adds up a run of bins of all CTAs and gives each CTA the sums; a bin
+      // is read by its own rank alone, so it may be overwritten at once.
+      const int mine = kBins / 2 / C;  // pairs of bins
 #pragma unroll 1
-    for (int s = 0; s < segs; ++s) {
-      Pair p;
-      p.h = S.second.acc[s][tid].x;
-      p.l = S.second.acc[s][tid].y;
-      const unsigned long long w = warp_sum(p.fixed());
-      if (lane == 0) S.red64[s][warp] = w;
+      for (int i = tid; i < 2 * mine; i += kSaThreads) {
+        const uint32_t at = smem_u32(i < mine ? &S.first.cnt[2 * (rank * mine + i)] : &S.first.frac[2 * (rank * mine + i - mine)]);
+        uint2 n = make_uint2(0u, 0u);
+#pragma unroll 1
+        for (int r0 = 0; r0 < C; r0 += 8) {
+          uint2 x[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) x[r] = r0 + r < C ? ld_cluster_v2(mapa_shared(at, (uint32_t)(r0 + r))) : make_uint2(0u, 0u);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) n.x += x[r].x, n.y += x[r].y;
+        }
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) st_cluster_v2(mapa_shared(at, (uint32_t)r), n);
+      }
+    }
+    cluster_meet(C);
+
+    // What lies before each bin: tokens, and weights as integers, 2^31 in all, so that
+    // no thread's sums differ from another's.  This thread's bins are kBinsPer
+    // consecutive ones.
+    const float per_bin = scale > 0.f ? 1.44269504f / (T * scale) : 0.f;  // octaves
+    {
+      uint4* cnt = reinterpret_cast<uint4*>(S.first.cnt) + 2 * tid;
+      uint4* frac = reinterpret_cast<uint4*>(S.first.frac) + 2 * tid;
+      const uint4 k0 = cnt[0], k1 = cnt[1], q0 = frac[0], q1 = frac[1];
+      uint32_t k[kBinsPer] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+      uint32_t q[kBinsPer] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      float f[kBinsPer], sum = 0.f;
+      uint32_t cn = 0;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        // the middle where no positions were added (with any, the sum is not 0: bin 0's are 1/2 and more)
+        const float kf = (float)k[i], mean = q[i] ? __fdividef((float)q[i], 4096.f * kf) - 0.5f : 0.f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f[i]) : "f"(-per_bin * ((float)(tid * kBinsPer + i) + mean)));
+        f[i] *= kf;
+        sum += f[i];
+        cn += k[i];
+      }
+      const float part = warp_sum(sum);
+      if (lane == 0) S.redf[0][warp] = part;
+      __syncthreads();
+      const float all = warp_sum(lane < kSaWarps ? S.redf[0][lane] : 0.f);
+      const float per_unit = 2147000000.f / all;  // the roundings of kBins sums stay below 2^31
+      uint32_t cf = 0;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        q[i] = __float2uint_rn(f[i] * per_unit);
+        cf += q[i];
+      }
+      uint32_t xn = warp_upto(cn), xf = warp_upto(cf);
+      if (lane == 31) S.red32[warp] = xn, S.redf[1][warp] = __uint_as_float(xf);
+      __syncthreads();
+      xn += __reduce_add_sync(0xffffffffu, lane < warp ? S.red32[lane & (kSaWarps - 1)] : 0u) - cn;
+      xf += __reduce_add_sync(0xffffffffu, lane < warp ? __float_as_uint(S.redf[1][lane & (kSaWarps - 1)]) : 0u) - cf;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        const uint32_t n = k[i], w = q[i];
+        k[i] = xn;
+        q[i] = xf;
+        xn += n;
+        xf += w;
+      }
+      cnt[0] = make_uint4(k[0], k[1], k[2], k[3]);
+      cnt[1] = make_uint4(k[4], k[5], k[6], k[7]);
+      frac[0] = make_uint4(q[0], q[1], q[2], q[3]);
+      frac[1] = make_uint4(q[4], q[5], q[6], q[7]);
+      if (tid == kSaThreads - 1) S.included = xn, S.total = xf;
     }
     __syncthreads();
-    if (tid < kSegs) {
-      unsigned long long w = 0;
-      if (tid < segs)
+    const uint32_t included = S.included, total = S.total;
+    auto sum_before = [&](int b) { return (float)(b < kBins ? S.first.frac[b] : total); };
+    auto count_before = [&](int b) { return b < kBins ? S.first.cnt[b] : included; };
+
+    // The bins where the borders are: ranges [lo, hi] for k, p, m and the token.  Every
+    // warp finds them.
+    auto range = [&](float from, float to, int& first, int& last) {
+      first = reach(S.first.frac, from > 1.f ? (uint32_t)from : 1u);
+      last = reach(S.first.frac, to > 1.f ? (uint32_t)to : 1u);
+    };
+    float s_lo = (float)total, s_hi = s_lo;  // the kept weights, within kSlack
+    int b_hi = kBins - 1;                    // the last bin that may hold the last kept token
+    if (with_k) {
+      lo[0] = hi[0] = b_hi = reach(S.first.cnt, (uint32_t)A.a.top_k);
+      s_lo = sum_before(b_hi);
+      s_hi = sum_before(b_hi + 1);
+    }
+    if (with_p) {
+      const float slack = kSlack * s_hi + 8.f;
+      range(A.a.top_p * s_lo - slack, A.a.top_p * s_hi + slack, lo[1], hi[1]);
+      s_lo *= A.a.top_p;
+      if (hi[1] < b_hi) {
+        b_hi = hi[1];
+        s_hi = sum_before(b_hi + 1);
+      }
+    }
+    if (with_m) {
+      const int b = (int)fminf(log_m * scale, (float)(kBins - 1));
+      lo[2] = max(0, b - 1);
+      hi[2] = min(kBins - 1, b + 2);
+      s_lo = fminf(s_lo, sum_before(lo[2]));
+      if (hi[2] < b_hi) {
+        b_hi = hi[2];
+        s_hi = sum_before(b_hi + 1);
+      }
+    }
+    if (count_before(b_hi + 1) <= kWhole) {
+      lo[3] = 0;
+      hi[3] = b_hi;
+    } else {
+      const float slack = kSlack * (float)total + 8.f;
+      range(u * s_lo - slack, u * s_hi + slack, lo[3], hi[3]);
+    }
+    // Classes of the bins: kListed for the candidates', else how many of the ranges
+    // end before.
+    const bool all = !with_k && (with_p || !with_m);  // every weight counts
+    int last = all ? kBins - 1 : -1;                  // the last bin that matters
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (hi[r] < kBins) last = max(last, hi[r]);
+#pragma unroll 1
+    for (int b = tid; b < kBins; b += kSaThreads) {
+      bool in = false;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) in = in || (b >= lo[r] && b <= hi[r]);
+      S.cls[b] = (uint8_t)(in ? kListed : seg_of(b));
+    }
+    // Lane s: the tokens of class s, whose bins are those behind the s-th range to end
+    // and before the first of the ranges that end later.
+    uint32_t seg_cnt = 0;
+    if (lane < kSegs) {
+      int from = lane ? kBins : 0, to = kBins;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (lane && hi[r] < kBins && seg_of(hi[r]) < lane && seg_of(hi[r] + 1) >= lane) from = hi[r] + 1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (hi[r] >= from) to = min(to, lo[r]);
+      if (from < to && seg_of(from) == lane) seg_cnt = count_before(to) - count_before(from);
+    }
+    n = (int)(included - __reduce_add_sync(0xffffffffu, seg_cnt));
+    segs = last < 0 ? 0 : seg_of(last) + 1;  // classes whose sums are wanted
+    seg_cnt = warp_upto(seg_cnt);
+    if (warp == 0 && lane < kSegs) S.base_cnt[lane] = seg_cnt;
+#pragma unroll 1
+    for (int s = 0; s < segs; ++s) S.second.acc[s][tid] = make_float2(0.f, 0.f);
+    __syncthreads();
+
+    // ---- 3. exact sums, candidates
+    if (n <= kCap) {
+      auto add = [&](int cls, float2 w) {
+        const float2 a = S.second.acc[cls][tid];
+        Pair p;
+        p.h = a.x;
+        p.l = a.y;
+        p.add(w);
+        S.second.acc[cls][tid] = make_float2(p.h, p.l);
+      };
+      each_chunk(row, V, pad, c0, c1, S.first.ring, [&](const float(&y)[4], int k) {
+        int cls[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          cls[e] = kNone;
+          if (y[e] >= cut) {
+            float at;
+            const int b = bin_of(y[e], at);
+            if (b <= last) cls[e] = S.cls[b];
+          }
+        }
+        if (max(max(cls[0], cls[1]), max(cls[2], cls[3])) == kListed) {
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            const int c = e < 2 ? (e ? cls[1] : cls[0]) : (e == 2 ? cls[2] : cls[3]);
+            const float x = e < 2 ? (e ? y[1] : y[0]) : (e == 2 ? y[2] : y[3]);
+            if (c == kListed) list(x, 4 * k - pad + e);
+          }
+        }
+        if (min(min(cls[0], cls[1]), min(cls[2], cls[3])) < kSegs) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {  // the weight of a logit that is not wanted goes to a sum that is not either
+            float2 w0, w1;
+            weights(W, y[e], y[e + 1], w0, w1);
+            add(cls[e], w0);
+            add(cls[e + 1], w1);
+          }
+        }
+      });
+#pragma unroll 1
+      for (int s = 0; s < segs; ++s) {
+        Pair p;
+        p.h = S.second.acc[s][tid].x;
+        p.l = S.second.acc[s][tid].y;
+        const unsigned long long w = warp_sum(p.fixed());
+        if (lane == 0) S.red64[s][warp] = w;
+      }
+      __syncthreads();
+      if (tid < kSegs) {
+        unsigned long long w = 0;
+        if (tid < segs)
 #pragma unroll 4
-        for (int i = 0; i < kSaWarps; ++i) w += S.red64[tid][i];
-      st_cluster_u64(mapa_shared(smem_u32(&S.seg_sum[rank][tid]), 0), w);
+          for (int i = 0; i < kSaWarps; ++i) w += S.red64[tid][i];
+        st_cluster_u64(mapa_shared(smem_u32(&S.seg_sum[rank][tid]), 0), w);
+      }
+    }
+    cluster_meet(C);
+    if (rank != 0) return;
+    if (warp < kSegs) {
+      unsigned long long w = 0;
+#pragma unroll 1
+      for (int i = 0; i <= warp; ++i) w += lane < C ? S.seg_sum[lane][i] : 0ull;
+      w = warp_sum(w);
+      if (lane == 0) S.base[warp] = w;
     }
   }
-  cluster_meet(C);
-  if (rank != 0) return;
 
   // ---- rank 0: the candidates in order, and the answers
   bool done = false;
-  if (fits && S.ncand == (uint32_t)n) {
+  if (n <= kCap && S.ncand == (uint32_t)n) {
     const unsigned long long* sorted = S.second.sorted;
     if (n <= kSaThreads) {  // each finds its place by counting
       if (tid < n) {
@@ -872,13 +935,6 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
           __syncthreads();
         }
       sorted = S.cand;
-    }
-    if (warp < kSegs) {
-      unsigned long long w = 0;
-#pragma unroll 1
-      for (int i = 0; i <= warp; ++i) w += lane < C ? S.seg_sum[lane][i] : 0ull;
-      w = warp_sum(w);
-      if (lane == 0) S.base[warp] = w;
     }
     __syncthreads();
     // This thread's candidates are `per` consecutive ones.

@@ -93,7 +93,7 @@ def _rows(seed, M, V, spread=2.5, banned=0.0):
 
 SETTINGS = [(1.0, 0, 1.0, 0.0), (0.8, 40, 0.95, 0.05), (1.0, 0, 0.9, 0.0), (1.3, 0, 0.999, 0.0), (0.6, 0, 1.0, 0.02),
             (1.5, 300, 1.0, 0.0), (2.0, 3000, 0.97, 0.001), (1.0, 1, 1.0, 0.0), (3.0, 0, 0.5, 0.3), (0.3, 7, 0.3, 0.9),
-            (0.0, 5, 0.5, 0.5), (5.0, 0, 0.99, 0.0), (1.0, 0, 0.0, 0.0), (1.0, 0, 1.0, 1.0), (100.0, 0, 0.7, 0.0)]
+            (0.0, 5, 0.5, 0.5), (1.1, 90, 1.0, 0.003), (1.5, 512, 0.9, 0.0), (1.5, 513, 1.0, 0.01), (5.0, 0, 0.99, 0.0), (1.0, 0, 0.0, 0.0), (1.0, 0, 1.0, 1.0), (100.0, 0, 0.7, 0.0)]
 
 
 @pytest.mark.parametrize("T,k,p,mp", SETTINGS)
