@@ -12,15 +12,19 @@
 //   m = fp16(min x),  d = fp16(max(max x - m, 0) / 15),
 //   q = (x - m) / d rounded to the nearest of 0 .. 15 (0 where d = 0).
 //
-// HBM-bound for a prompt: each input is read once.  A CTA has one token and
-// computes its n_rot / 2 sines and cosines once, while its first rows are on
-// their way.  A head is 8 dimensions a lane: the sum of squares and a group's
-// extremes meet by shuffles, and every lane keeps gamma and the turns of its
-// dimensions in registers for all of its heads; the half layout's mates, which
-// other lanes hold, pass through shared memory.  Few tokens: their heads are
-// spread over several CTAs.
+// HBM-bound for a prompt: each input is read once.  A CTA has a few tokens and
+// computes their sines and cosines together, while its first rows are on their way;
+// a row is a head of a token, 8 dimensions a lane, and the next rows load while one
+// is computed.  The sum of squares and a group's extremes meet by shuffles.  Where a
+// whole head of the half layout turns, a lane has two runs of four dimensions, each
+// other's mates; otherwise a run of eight, and the half layout's mates, which other
+// lanes hold, pass through shared memory (2047 tokens of 32 + 4 + 4 heads of 128:
+// 20.1 us so).  Few tokens:
+// their heads are spread over several CTAs.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
@@ -32,26 +36,27 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrMaxD = 512;
+constexpr int kNrTokens = 4;  // of a CTA, where there are many
 
 __device__ __forceinline__ uint32_t pack2h(float a, float b) {
   const __half2 x = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// 8 values of a group of 32 that four lanes hold: their nibbles in order, and
-// (d, m) as two fp16.  Every lane of the warp takes part.
-__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], uint32_t& dm) {
-  float lo = y[0], hi = y[0];
-  bool bad = false;
+// kN of the 32 values of a group, which 32 / kN lanes hold: their nibbles in order,
+// and (d, m) as two fp16.  Every lane of the warp takes part.
+template <int kN>
+__device__ __forceinline__ uint32_t quantize(const float* y, uint32_t& dm) {
+  float lo = y[0], hi = y[0], far = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < kN; ++e) {
     lo = fminf(lo, y[e]);
     hi = fmaxf(hi, y[e]);
-    bad |= !(fabsf(y[e]) < INFINITY);
+    far = fmaf(y[e], 0.f, far);  // NaN where a value is not finite
   }
-  if (bad) hi = INFINITY;
+  if (far != 0.f) hi = INFINITY;
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
+  for (int o = 1; o < 32 / kN; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
@@ -61,113 +66,153 @@ __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], uint32_t& dm)
   // infinite then, or NaN where m is: infinity less infinity)
   const bool fine = fabsf(m) < INFINITY && d <= 4366.f;
   uint32_t q = 0;
-  if (d > 0.f)
+  if (d > 0.f) {
+    // (y - m) / d by the reciprocal is within 2^-22 of the quotient, 2^-18 at most
+    // here; a quotient nearer to a border than that is divided
+    constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer in the low bits
+    const float r = 1.0f / d;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q |= (uint32_t)fminf(fmaxf(rintf((y[e] - m) / d), 0.f), 15.f) << (4 * e);
+    for (int e = 0; e < kN; ++e) {
+      const float n = y[e] - m, t = n * r;
+      float k = __fadd_rn(t, kMagic);
+      if (fabsf(t - __fsub_rn(k, kMagic)) > 0.4999f) k = __fadd_rn(n / d, kMagic);
+      q |= (uint32_t)min(max((int)__float_as_uint(k) - 0x4B400000, 0), 15) << (4 * e);
+    }
+  }
   dm = fine ? pack2h(d, m) : 0x7FFF7FFFu;
   return fine ? q : 0u;
 }
 
-// A CTA: one token, heads blockIdx.y, blockIdx.y + gridDim.y ... of its H + 2 Hkv
-// in turns of slots; a slot is 2^lph_log2 lanes.  kPer: runs of 8 dimensions of a
-// head that one lane holds (2 where D > 256).
-template <bool kQ4, int kPer>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs N, int lph_log2) {
-  constexpr int kBatch = kPer == 1 ? 3 : 1;  // heads of a slot in flight: 48 of 128 at once
-  __shared__ float2 cs[kNrMaxD / 2];
+// The rows of a CTA: heads first .. first + count - 1 of its tokens, token by token.
+// A slot of 2^lph_log2 lanes takes every slots-th row.  kPer: 8s of dimensions of a
+// row that one lane holds (2 where D > 256).  kMates: they are two runs of 4, half a
+// head apart (half layout, all of a head turns, D <= 256 a multiple of 64).
+template <bool kQ4, int kPer, bool kMates>
+__global__ void __launch_bounds__(kNrThreads, kPer == 1 ? 4 : 2)
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs N, int lph_log2, int tokens, int per_cta) {
+  __shared__ __align__(16) float cosines[kNrTokens][kNrMaxD / 2], sines[kNrTokens][kNrMaxD / 2];
   __shared__ __align__(16) float rows[kNrThreads / 32][kNrMaxD];
   const RopeArgs& A = N.rope;
-  const int64_t i = blockIdx.x, p = A.pos0 + i;
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  const int nt = (int)min((int64_t)tokens, A.M - t0);
   const int lph = 1 << lph_log2, slots = kNrThreads >> lph_log2;
   const int c = threadIdx.x & (lph - 1), slot = threadIdx.x >> lph_log2;
-  const int heads = A.H + 2 * A.Hkv, step = gridDim.y * slots;
+  const int heads = A.H + 2 * A.Hkv, first = blockIdx.y * per_cta, count = min(per_cta, heads - first);
   float* row = &rows[threadIdx.x >> 5][((threadIdx.x & 31) >> lph_log2) * A.D];
   const int h2 = A.n_rot / 2;
-  float tc[kPer][8], ts[kPer][8];  // y = x tc + mate ts
-  uint4 gq[kPer], gk[kPer];
-  bool ready = false;
+  const float per_d = 1.0f / (float)A.D;
+  const bool vec = A.half ? h2 % 8 == 0 : true;  // this lane's turns lie together
   dependent_wait();
-  for (int h0 = blockIdx.y * slots; h0 < heads; h0 += kBatch * step) {
-    uint4 x[kBatch][kPer][2];
+
+  // This CTA's part of each tensor; offsets within it fit 32 bits.
+  const float *q_in = A.q + t0 * A.H * A.D, *k_in = A.k + t0 * A.Hkv * A.D, *v_in = A.v + t0 * A.Hkv * A.D;
+  uint16_t* q_to = A.q_out + t0 * A.H * A.D;
+  struct Row {  // a head of a token (tok >= nt: none), on its way
+    int tok, hd;
+    uint4 v[kPer][2];
+  };
+  const int tok_step = slots / count, hd_step = slots - tok_step * count;
+  int tok_next = slot / count, hd_next = first + slot - tok_next * count;
+  const bool whole = 8 * lph * kPer == A.D;  // every lane has dimensions
+  auto load = [&](Row& x) {  // past the last row: the last token's again
+    x.tok = tok_next;
+    x.hd = hd_next;
+    const bool is_q = x.hd < A.H, is_k = x.hd < A.H + A.Hkv;
+    const float* base = is_q ? q_in : is_k ? k_in : v_in;
+    const int h = x.hd - (is_q ? 0 : is_k ? A.H : A.H + A.Hkv);
+    const float* in = base + (min(x.tok, nt - 1) * (is_q ? A.H : A.Hkv) + h) * A.D;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int hd = h0 + b * step + slot;
-      const float* in = hd < A.H           ? A.q + (i * A.H + hd) * A.D
-                        : hd < A.H + A.Hkv ? A.k + (i * A.Hkv + hd - A.H) * A.D
-                                           : A.v + (i * A.Hkv + hd - A.H - A.Hkv) * A.D;
-#pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const int d0 = 8 * (c + r * lph);
-        x[b][r][0] = x[b][r][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (hd < heads && d0 < A.D) {
-          x[b][r][0] = ldg_stream16(in + d0);
-          x[b][r][1] = ldg_stream16(in + d0 + 4);
-        }
-      }
+    for (int r = 0; r < kPer; ++r) {
+      const int d0 = 8 * (c + r * lph), d = whole || d0 < A.D ? (kMates ? d0 / 2 : d0) : 0;
+      x.v[r][0] = ldg_stream16(in + d);
+      x.v[r][1] = ldg_stream16(in + d + (kMates ? h2 : 4));
     }
-    if (!ready) {
-      fill_table(A, p, cs, kNrThreads);
-      __syncthreads();
-      ready = true;
+    tok_next += tok_step;
+    hd_next += hd_step;
+    if (hd_next >= first + count) hd_next -= count, ++tok_next;
+  };
+  Row x0, x1;  // two rows on their way
+  load(x0);
+  load(x1);
+  for (int j = threadIdx.x; j < nt * h2; j += kNrThreads) {
+    const int t = j / h2, i = j - t * h2;
+    const float2 cs = turn(A, A.pos0 + t0 + t, i);
+    cosines[t][i] = cs.x;
+    sines[t][i] = cs.y;
+  }
+  uint4 gq[kPer], gk[kPer];
 #pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const int d0 = 8 * (c + r * lph);
-        gq[r] = gk[r] = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);  // ones
-        if (d0 < A.D) {
-          if (N.q_gamma) gq[r] = *reinterpret_cast<const uint4*>(N.q_gamma + d0);
-          if (N.k_gamma) gk[r] = *reinterpret_cast<const uint4*>(N.k_gamma + d0);
-        }
+  for (int r = 0; r < kPer; ++r) {
+    const int d0 = 8 * (c + r * lph);
+    gq[r] = gk[r] = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);  // ones
+    if (d0 < A.D) {
+      auto gamma = [&](const uint16_t* from) {
+        if (!kMates) return *reinterpret_cast<const uint4*>(from + d0);
+        const uint2 a = *reinterpret_cast<const uint2*>(from + d0 / 2);
+        const uint2 b = *reinterpret_cast<const uint2*>(from + d0 / 2 + h2);
+        return make_uint4(a.x, a.y, b.x, b.y);
+      };
+      if (N.q_gamma) gq[r] = gamma(N.q_gamma);
+      if (N.k_gamma) gk[r] = gamma(N.k_gamma);
+    }
+  }
+  __syncthreads();
+
+  auto compute = [&](Row& x) {
+    const int tok = x.tok, hd = x.hd;
+    float y[kPer][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          tc[r][e] = 1.f;
-          ts[r][e] = 0.f;
-          if (d < A.n_rot) {
-            const bool second = A.half ? d >= h2 : (e & 1) != 0;
-            const float2 t = cs[A.half ? (second ? d - h2 : d) : d >> 1];
-            tc[r][e] = t.x;
-            ts[r][e] = second ? t.y : -t.y;
+    for (int r = 0; r < kPer; ++r) {
+      const uint4 lo = x.v[r][0], hi = x.v[r][1];
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[r][e] = __uint_as_float(w[e]);
+      if (!whole && 8 * (c + r * lph) >= A.D)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[r][e] = 0.f;
+    }
+    load(x);
+    const bool on = tok < nt, is_q = hd < A.H, turns = hd < A.H + A.Hkv;
+    // every lane takes the same path through the shuffles: a head without a norm (v,
+    // or no gamma) only drops the result
+    if (N.q_gamma || N.k_gamma) {
+      float ss = 0.f;
+#pragma unroll
+      for (int r = 0; r < kPer; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[r][e], y[r][e], ss);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+        if (o < lph) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (is_q ? N.q_gamma != nullptr : turns && N.k_gamma != nullptr) {
+        const float inv = rsqrtf(fmaf(ss, per_d, N.eps));
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const uint4 g4 = is_q ? gq[r] : gk[r];
+          const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 gg = __half22float2(*reinterpret_cast<const __half2*>(&g[e]));
+            y[r][2 * e] = y[r][2 * e] * inv * gg.x;
+            y[r][2 * e + 1] = y[r][2 * e + 1] * inv * gg.y;
           }
         }
       }
     }
+    if (kMates) {
+      if (turns && on && 8 * c < A.D) {
+        const float4 cc = *reinterpret_cast<const float4*>(cosines[tok] + 4 * c);
+        const float4 ss = *reinterpret_cast<const float4*>(sines[tok] + 4 * c);
+        const float tc[4] = {cc.x, cc.y, cc.z, cc.w}, ts[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int hd = h0 + b * step + slot;
-      const bool is_q = hd < A.H, turns = hd < A.H + A.Hkv;
-      float y[kPer][8];
-#pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const uint32_t w[8] = {x[b][r][0].x, x[b][r][0].y, x[b][r][0].z, x[b][r][0].w,
-                               x[b][r][1].x, x[b][r][1].y, x[b][r][1].z, x[b][r][1].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[r][e] = __uint_as_float(w[e]);
-      }
-      // every lane takes the same path through the shuffles: a head without a
-      // norm (v, or no gamma) only drops the result
-      if (N.q_gamma || N.k_gamma) {
-        float ss = 0.f;
-#pragma unroll
-        for (int r = 0; r < kPer; ++r)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(y[r][e], y[r][e], ss);
-        for (int o = 1; o < lph; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (is_q ? N.q_gamma != nullptr : turns && N.k_gamma != nullptr) {
-          const float inv = 1.0f / sqrtf(ss / (float)A.D + N.eps);
-#pragma unroll
-          for (int r = 0; r < kPer; ++r) {
-            const uint4 g4 = is_q ? gq[r] : gk[r];
-            const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 gg = __half22float2(*reinterpret_cast<const __half2*>(&g[e]));
-              y[r][2 * e] = y[r][2 * e] * inv * gg.x;
-              y[r][2 * e + 1] = y[r][2 * e + 1] * inv * gg.y;
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float a = y[0][e], b = y[0][4 + e];
+          y[0][e] = a * tc[e] - b * ts[e];
+          y[0][4 + e] = b * tc[e] + a * ts[e];
         }
       }
-      if (A.half && A.n_rot > 0) {  // the mates are other lanes'
+    } else if (h2 > 0 && __any_sync(0xffffffffu, turns && on)) {
+      if (A.half) {  // the mates are other lanes'
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < kPer; ++r) {
@@ -179,46 +224,94 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
         }
         __syncwarp();
       }
-      if (turns) {
+      if (turns && on) {
+        const float *cosine = cosines[tok], *sine = sines[tok];
 #pragma unroll
         for (int r = 0; r < kPer; ++r) {
           const int d0 = 8 * (c + r * lph);
-          float mate[8];
-          if (A.half) {
+          if (d0 >= A.n_rot) continue;
+          if (!A.half) {
+            const float4 cc = *reinterpret_cast<const float4*>(cosine + d0 / 2);
+            const float4 ss = *reinterpret_cast<const float4*>(sine + d0 / 2);
+            const float tc[4] = {cc.x, cc.y, cc.z, cc.w}, ts[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int d = d0 + e;
-              mate[e] = d < A.n_rot ? row[d < h2 ? d + h2 : d - h2] : 0.f;
+            for (int e = 0; e < 4; ++e)
+              if (d0 + 2 * e < A.n_rot) {
+                const float a = y[r][2 * e], b = y[r][2 * e + 1];
+                y[r][2 * e] = a * tc[e] - b * ts[e];
+                y[r][2 * e + 1] = b * tc[e] + a * ts[e];
+              }
+          } else if (vec) {  // all 8 dimensions turn, on the same side of their mates
+            const bool second = d0 >= h2;
+            const int p0 = second ? d0 - h2 : d0, m0 = second ? p0 : d0 + h2;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 cc = *reinterpret_cast<const float4*>(cosine + p0 + 4 * q);
+              const float4 ss = *reinterpret_cast<const float4*>(sine + p0 + 4 * q);
+              const float4 mm = *reinterpret_cast<const float4*>(row + m0 + 4 * q);
+              const float tc[4] = {cc.x, cc.y, cc.z, cc.w}, ts[4] = {ss.x, ss.y, ss.z, ss.w};
+              const float mate[4] = {mm.x, mm.y, mm.z, mm.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[r][4 * q + e] = y[r][4 * q + e] * tc[e] + mate[e] * (second ? ts[e] : -ts[e]);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mate[e] = y[r][e ^ 1];
+            for (int e = 0; e < 8; ++e) {
+              const int d = d0 + e;
+              if (d >= A.n_rot) continue;
+              const bool second = d >= h2;
+              const int p = second ? d - h2 : d;
+              y[r][e] = y[r][e] * cosine[p] + row[second ? p : d + h2] * (second ? sine[p] : -sine[p]);
+            }
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (d0 + e < A.n_rot) y[r][e] = y[r][e] * tc[r][e] + mate[e] * ts[r][e];
-        }
-      }
-      const int g = hd - A.H - (turns ? 0 : A.Hkv);  // key/value head
-#pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const int d0 = 8 * (c + r * lph);
-        uint32_t q = 0, dm = 0;
-        if (kQ4) q = quantize8(y[r], dm);
-        if (hd >= heads || d0 >= A.D) continue;
-        if (!kQ4 || is_q) {
-          uint16_t* out = is_q ? A.q_out + (i * A.H + hd) * A.D
-                               : (turns ? A.k_cache : A.v_cache) + ((int64_t)g * A.Lmax + p) * A.D;
-          *reinterpret_cast<uint4*>(out + d0) =
-              make_uint4(pack2h(y[r][0], y[r][1]), pack2h(y[r][2], y[r][3]), pack2h(y[r][4], y[r][5]),
-                         pack2h(y[r][6], y[r][7]));
-        } else {
-          const int64_t at = ((int64_t)g * A.Lmax + p) * (A.D / 8) + d0 / 8;
-          (turns ? N.k_q4 : N.v_q4)[at] = q;
-          if ((c & 3) == 0) (turns ? N.k_dm : N.v_dm)[at >> 2] = dm;
         }
       }
     }
+    const int g = hd - A.H - (turns ? 0 : A.Hkv);  // key/value head
+    const int64_t at = (int64_t)g * A.Lmax + A.pos0 + t0 + tok;  // its row of the cache
+    const bool packs = kQ4 && __any_sync(0xffffffffu, on && !is_q);
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int d0 = 8 * (c + r * lph);
+      uint32_t q = 0, dm = 0, dm2 = 0;
+      if (packs && !kMates) q = quantize<8>(y[r], dm);
+      if (packs && kMates) {
+        // lanes of a pair: the even one gets 8 dimensions of the first run, the odd one of the second
+        const uint32_t a = quantize<4>(y[r], dm), b = quantize<4>(y[r] + 4, dm2);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, c & 1 ? a : b, 1);
+        q = c & 1 ? other | (b << 16) : a | (other << 16);
+      }
+      if (!on || d0 >= A.D) continue;
+      if (!kQ4 || is_q) {
+        uint16_t* out = is_q ? q_to + (tok * A.H + hd) * A.D : (turns ? A.k_cache : A.v_cache) + at * A.D;
+        const uint4 h = make_uint4(pack2h(y[r][0], y[r][1]), pack2h(y[r][2], y[r][3]), pack2h(y[r][4], y[r][5]),
+                                   pack2h(y[r][6], y[r][7]));
+        if (!kMates) {
+          *reinterpret_cast<uint4*>(out + d0) = h;
+        } else {
+          *reinterpret_cast<uint2*>(out + d0 / 2) = make_uint2(h.x, h.y);
+          *reinterpret_cast<uint2*>(out + d0 / 2 + h2) = make_uint2(h.z, h.w);
+        }
+      } else {
+        uint32_t* q_row = (turns ? N.k_q4 : N.v_q4) + at * (A.D / 8);
+        uint32_t* dm_row = (turns ? N.k_dm : N.v_dm) + at * (A.D / 32);
+        if (!kMates) {
+          q_row[d0 / 8] = q;
+          if ((c & 3) == 0) dm_row[d0 / 32] = dm;
+        } else {
+          q_row[(c & 1 ? h2 / 8 : 0) + c / 2] = q;
+          if ((c & 7) == 0) dm_row[c / 8] = dm;
+          if ((c & 7) == 1) dm_row[h2 / 32 + c / 8] = dm2;
+        }
+      }
+    }
+  };
+  const int total = (nt * count + slots - 1) / slots;  // rows of the longest slot
+#pragma unroll 1
+  for (int step = 0; step < total; step += 2) {
+    compute(x0);
+    if (step + 1 < total) compute(x1);
   }
 }
 
@@ -228,11 +321,16 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t s) {
   const bool two = r.D > 256;
   int lph_log2 = 0;
   while (lph_log2 < 5 && (8 << lph_log2) < r.D) ++lph_log2;
-  const int slots = kNrThreads >> lph_log2;
-  const int split = r.M <= 2 * (int64_t)device_sms() ? (r.H + 2 * r.Hkv + slots - 1) / slots : 1;
-  const dim3 grid((unsigned)r.M, (unsigned)split);
-  return launch_dependent(two ? norm_rope_kernel<kQ4, 2> : norm_rope_kernel<kQ4, 1>, grid, kNrThreads, 0, 1, s, a,
-                          lph_log2);
+  const int slots = kNrThreads >> lph_log2, heads = r.H + 2 * r.Hkv;
+  // Few tokens: one a CTA, its heads over several; many: kNrTokens a CTA.
+  const bool few = r.M <= 2 * (int64_t)device_sms();
+  const int tokens = few ? 1 : kNrTokens, per_cta = few ? std::min(slots, heads) : heads;
+  const dim3 grid((unsigned)((r.M + tokens - 1) / tokens), (unsigned)((heads + per_cta - 1) / per_cta));
+  const bool mates = r.half && r.n_rot == r.D && !two && r.D % 64 == 0;
+  return launch_dependent(two     ? norm_rope_kernel<kQ4, 2, false>
+                          : mates ? norm_rope_kernel<kQ4, 1, true>
+                                  : norm_rope_kernel<kQ4, 1, false>,
+                          grid, kNrThreads, 0, 1, s, a, lph_log2, tokens, per_cta);
 }
 
 }  // namespace

@@ -53,12 +53,13 @@ def _append_case(qk, cuda, M, H, Hkv, Dh, n_rot, pos0, L, half, qn, kn, mag=1.0,
     sizes = (M, H, Hkv, Dh, n_rot, pos0, L)
 
     def exact(x, gamma):
-        """(64-bit values, what fp32 may be off by): a sum of squares of D / 256 + 12
-        steps, halved by the root, and five more operations, 2^-24 each; sine and
-        cosine within 2^-21, two products and a sum of 2^-24."""
+        """(64-bit values, what fp32 may be off by), in steps of 2^-24: a lane adds 8 (D > 256:
+        16) squares and shuffles 5 more, halved by the root; the mean and eps one half each;
+        rsqrtf 4; two products 2.  Sine and cosine within 2^-21, two products and a sum of
+        2^-24.  A rotated value has two such parts."""
         y = ref4.head_norm(x, gamma, EPS)
         most = np.abs(y).max(-1, keepdims=True) * 2 * max(1.0, abs(mag))
-        return ref4.rotate(y, angle, n_rot, half, mag), most * (2.0 ** -20.5 + (Dh / 256 + 22) / 2 * 2.0 ** -24)
+        return ref4.rotate(y, angle, n_rot, half, mag), most * (2.0 ** -20.5 + ((21 if Dh > 256 else 13) / 2 + 7) * 2.0 ** -24)
 
     eq, dq = exact(q, gq)
     ek, dk = exact(k, gk)
