@@ -456,7 +456,7 @@ qk_status qk_gqa_attention_window(const uint16_t *q_f16, const uint16_t *k_cache
  * qk_norm_rope_kv_append_q4; d q + m and 15 d must be finite fp16 numbers, or d
  * or m NaN).  Up to 32 columns, M * H / H_kv (a decode step, or a few drafted
  * tokens), read the 4-bit rows directly: over a cluster of CTAs per key/value
- * head, or, from 32768 positions of all key/value heads on, over all SMs, joined
+ * head, or, from 65536 positions of all key/value heads on, over all SMs, joined
  * by a second kernel through `scratch`.  More tokens have the rows that their
  * queries see written to `scratch` as fp16 first (512 bytes a position and
  * key/value head).  scratch is a caller-owned device buffer of at least

@@ -6,36 +6,51 @@
 //
 // A row of one position and key/value head holds groups of 32 values as v = d q + m
 // (q in 0 .. 15, d and m fp16): 64 bytes of quants and 16 of (d, m) for 128
-// values, 80 bytes where fp16 takes 256.  Every path uses fp16(d q + m), one
-// rounding, so that they agree with the rows that qk_dequant_kv_q4 gives.
+// values, 80 bytes where fp16 takes 256.
 //
 // Few tokens (a decode step, or drafted tokens: M * H / H_kv <= 32 columns, a
-// column being a query head of one token).  A cluster of up to 16 CTAs per
-// key/value head splits the visible positions; a warp takes 16 of them at a time
-// through a ring of its own in shared memory (a lane has one whole group of 32
-// key and value quants of a position, 16 bytes), three more 16s on their way.
-// mma.sync, whose 8-wide N side
-// holds the columns, multiplies:
-//   S^T = K Q^T  (16 positions x 8 columns): the product's k axis is permuted to
-//     what the lanes hold, so nothing is exchanged;
-//   O^T = V^T P  (dimensions x columns): movmatrix transposes 8 positions of 4
-//     nibbles each, which are four dimensions' k pairs.
+// column being a query head of one token).  A warp takes 16 positions at a time
+// through a ring of its own in shared memory, three more 16s on their way.
+// mma.sync, whose 8-wide N side holds the columns, multiplies:
+//   S^T = K Q^T (16 positions x 8 columns), a group of the dimensions at a time:
+//     the sum over the groups of d (q . Q) + m (sum of Q), d applied to the fp32
+//     products.  The quants are exact operands, so K is not rounded at all;
+//   O^T = V^T P (dimensions x columns): fp16(d (q - 8)) P, and 8 d + m of the groups
+//     through one more product, whose other rows add up the weights.  movmatrix
+//     transposes 8 positions of 4 nibbles each, which are four dimensions' k pairs.
 // A nibble becomes an fp16 by OR with an exponent (1024 + q, or 64 + q where it
-// sits 4 bits higher), a subtraction and one fused multiply-add for its pair.
+// sits 4 bits higher); for K the offsets come off with the product of (d, m).
+// Rounded to fp16: weights (against a reference 7 below the largest, so that those
+// down to 2^-32 of it count), d (q - 8), and the outputs.  The 2-norm of the error is
+// 2.7e-4 of the output's after 500 positions, 3.3e-4 after 65536; the output's own
+// rounding is 2.1e-4 of it.  With fp16(d q + m) for K and fp16(d q) for V it was 6.0e-4
+// and 7.4e-4 (in 3.8 and 21.8 us instead of 4.0 and 22.4).
 // Every warp keeps its own running maximum, sums and O; the warps of a CTA join
-// in order through shared memory, the CTAs through distributed shared memory,
-// each writing a share of the outputs.
+// in order through shared memory.  The CTAs of a key/value head join
+//   - as a cluster of up to 16 through distributed shared memory, each writing a
+//     share of the outputs; or,
+//   - from 65536 positions of all heads on, through the scratch and a second kernel
+//     (attn_q4_join_kernel): a GPC takes few clusters of 16, so that 8 heads' leave
+//     SMs idle, while this split uses all of them.  24 heads over 8, clusters / all
+//     SMs, us: 2048 positions 5.7 / 7.2, 4096 6.8 / 8.0, 8192 9.0 / 8.9, 16384 13.3 /
+//     10.9, 32768 21.5 / 15.9, 131072 69 / 35; 32 over 4: 4096 5.6 / 8.7.
 //
-// More tokens: the visible rows are written as fp16 to the caller's scratch once
-// and the windowed prefill runs over them: a query tile's 128 rows would unpack
-// each key again.
+// One token, 24 heads over 8, 65536 positions (84 MB: 12.4 us at a copy's rate): 22.4 us.
+// Bound by instructions at long lengths (410 for a warp's 16 positions, issued in
+// 57 % of the cycles, the ends included; the DRAM is 45 % busy) and by the latency of
+// a launch, or two, at short ones.
 //
-// The kernel has no waits but the cluster barriers, which every thread reaches.
+// More tokens: the visible rows are written as fp16(d q + m) to the caller's scratch
+// once and the windowed prefill runs over them: a query tile's 128 rows would unpack
+// each key again.  1023 tokens after 7001, 24 heads over 8: 117 us, 9 of them for
+// the rows; 104 CTAs of two query tiles each on 152 SMs.  (Clusters of 2, 4 and 8 that
+// share the keys of a pair of tiles: 134, 118, 171.)
+//
+// The kernels have no waits but the cluster barriers, which every thread reaches.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 #include <atomic>
 
 #include "qk_attn.cuh"
@@ -49,7 +64,7 @@ namespace {
 constexpr int kQMaxCluster = 16;
 constexpr int kQMaxCols = 32;
 constexpr int kQMaxSplit = 160;   // CTAs of a call that join through the scratch
-constexpr int64_t kQSplitFrom = 8 * 4096;  // positions of all key/value heads from which they do
+constexpr int64_t kQSplitFrom = 8 * 8192;  // positions of all key/value heads from which they do
 constexpr int kUnit = 16;  // positions of a warp's step
 
 // The shape of a CTA for NT tiles of 8 columns and W warps.
@@ -116,28 +131,6 @@ __device__ __forceinline__ void unpack_pairs(uint32_t w, __half2 (&q)[4]) {
   for (int i = 0; i < 4; ++i) q[i] = __hsub2(as_h2(u[i]), as_h2(i & 1 ? 0x54005400u : 0x64006400u));
 }
 
-// fp16(d q) of a word's nibbles, one rounding each.  Where |d| < 60 the offsets
-// go with the product, d (1024 + q) - 1024 d, whose last term is exact.
-struct Scaled {
-  __half2 d, c1024, c64;
-  __device__ __forceinline__ explicit Scaled(uint32_t pair)
-      : d(as_h2(pair)), c1024(__hmul2(as_h2(pair), as_h2(0xE400E400u))), c64(__hmul2(as_h2(pair), as_h2(0xD400D400u))) {}
-  template <bool kWide>
-  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&v)[4]) const {
-    if (kWide) {
-      __half2 q[4];
-      unpack_pairs(w, q);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hmul2(q[i], d));
-    } else {
-      spread(w, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hfma2(as_h2(v[i]), d, i & 1 ? c64 : c1024));
-    }
-  }
-};
-constexpr uint32_t kWideD = 0x5380u;  // 60 as fp16
-
 // Transposes an 8 x 8 matrix of 16-bit values: lane 4 r + c holds row r, columns 2 c and 2 c + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
@@ -195,9 +188,10 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
   auto fetch = [&](int at, int stage) {
     if (at < unit1) {
       Q4Stage& R = ring[stage];
+      const int kl = 4 * grp + (tq ^ ((grp >> 1) & 3));
       const int64_t j0 = 4 * position(kUnit * at + grp), j1 = 4 * position(kUnit * at + grp + 8);
-      copy16(&R.k[lane], kq + j0);
-      copy16(&R.k[lane + 32], kq + j1);
+      copy16(&R.k[kl], kq + j0);
+      copy16(&R.k[kl + 32], kq + j1);
       copy16((lane < 16 ? R.ks : R.vs) + (lane & 15), dm + position(kUnit * at + (lane & 15)));
       copy16(&R.v[lane], vq + j0);
       copy16(&R.v[lane + 32], vq + j1);
@@ -207,21 +201,24 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(unit + i * Sh::kWarps, i);
 
-  // Q: the product's k axis in step (word j, half h) is dims 32 tq + 8 j + 2 h and + 4
-  // (first register), and those + 1 (second), of this lane's tq.
+  // Q: the product's k axis in step (group j, half h) is dims 32 j + 8 tq + 2 h and + 4
+  // (first register), and those + 1 (second).
   uint2 qb[NT][4][2];
+  uint32_t kb[NT][2];  // of column grp and group tq: (what takes the offsets off the product, the sum of Q) 2^-k, high and low parts
+  float kup[NT][2];    // 2^k of this lane's columns
   int cpos[NT][2];    // the positions of this lane's columns
   float o[NT][8][4];  // [column tile][2 j + h]: dims 32 (grp / 2) + 8 j + 4 (grp % 2) + 2 h (+ 1: elements 2, 3), columns 2 tq (+ 1)
-  float om[NT][4];    // elements 0, 1: what their group's m adds to all of these; 2, 3: the columns' sums of weights
+  float om[NT][4];    // elements 0, 1: weights times d (even grp) or m (odd) of group grp / 2; 2, 3: the columns' sums of weights
   float m[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int col = 8 * n + grp;
     const int token = kMulti ? col / A.G : 0;
-    const uint4* qr = reinterpret_cast<const uint4*>(A.q + ((int64_t)token * A.H + g * A.G + (col - token * A.G)) * kD) + 4 * tq;
+    const uint4* qr = reinterpret_cast<const uint4*>(A.q + ((int64_t)token * A.H + g * A.G + (col - token * A.G)) * kD) + tq;
+    float even[4] = {0.f, 0.f, 0.f, 0.f}, odd[4] = {0.f, 0.f, 0.f, 0.f};  // of the nibbles with the offsets 1024 and 64
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint4 y = col < A.M * A.G ? qr[j] : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 y = col < A.M * A.G ? qr[4 * j] : make_uint4(0u, 0u, 0u, 0u);
       const uint2 b0 = make_uint2(prmt(y.x, y.z, 0x5410), prmt(y.x, y.z, 0x7632));
       const uint2 b1 = make_uint2(prmt(y.y, y.w, 0x5410), prmt(y.y, y.w, 0x7632));
       if (!Sh::kSharedQ) {
@@ -231,7 +228,33 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
         S.q[8 * n + 2 * j][lane] = b0;
         S.q[8 * n + 2 * j + 1][lane] = b1;
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = __half22float2(as_h2(i ? b1.x : b0.x)), b = __half22float2(as_h2(i ? b1.y : b0.y));
+        even[j] += a.x + a.y;
+        odd[j] += b.x + b.y;
+      }
     }
+    // lane tq gets the sums of group tq, of its column
+#pragma unroll
+    for (int x = 2; x > 0; x >>= 1)
+#pragma unroll
+      for (int j = 0; j < x; ++j) {
+        const bool up = (tq & x) != 0;
+        even[j] = (up ? even[j + x] : even[j]) + __shfl_xor_sync(0xffffffffu, up ? even[j] : even[j + x], x);
+        odd[j] = (up ? odd[j + x] : odd[j]) + __shfl_xor_sync(0xffffffffu, up ? odd[j] : odd[j + x], x);
+      }
+    const float off = -fmaf(1024.f, even[0], 64.f * odd[0]), sum = even[0] + odd[0];
+    float most = fmaxf(fabsf(off), fabsf(sum));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const uint32_t ex = max(__float_as_uint(most) >> 23, 64u);  // the largest becomes 2^13 .. 2^14
+    const float down = __uint_as_float((267u - ex) << 23), up = __uint_as_float((ex - 13u) << 23);
+    const __half2 hi = __floats2half2_rn(off * down, sum * down);
+    kb[n][0] = as_u32(hi);
+    kb[n][1] = as_u32(__floats2half2_rn(off * down - __low2float(hi), sum * down - __high2float(hi)));
+    kup[n][0] = __shfl_sync(0xffffffffu, up, 8 * tq);
+    kup[n][1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       cpos[n][e] = (int)A.pos0 + (kMulti ? min((8 * n + 2 * tq + e) / A.G, A.M - 1) : 0);
@@ -250,42 +273,55 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
     __syncwarp();  // the scales are other lanes' copies; and all lanes are done with the stage before
     fetch(unit + (kStages - 1) * Sh::kWarps, stage == 0 ? kStages - 1 : stage - 1);
     const Q4Stage& R = ring[stage];
-    const uint4 k0 = R.k[lane], k1 = R.k[lane + 32], v0 = R.v[lane], v1 = R.v[lane + 32];
-    const uint32_t* sk = reinterpret_cast<const uint32_t*>(R.ks) + lane;
+    const uint4 v0 = R.v[lane], v1 = R.v[lane + 32];
     const uint32_t* sv = reinterpret_cast<const uint32_t*>(R.vs) + lane;
-    const uint32_t ks0 = sk[0], ks1 = sk[32], vs0 = sv[0], vs1 = sv[32];
+    const uint32_t vs0 = sv[0], vs1 = sv[32];
     const int u = kUnit * unit, rows = total - u;  // rows past them are copies
-    // ---- scores: rows grp and grp + 8, this lane's group of the dimensions
+    // ---- scores of rows grp and grp + 8: the sum over the groups of d (q . Q) + m (sum of Q),
+    // without a rounding of K.  The quants go to the tensor core with their offsets, a
+    // group at a time; one more product of the rows' (d, m) takes those off and adds m.
     float sc[NT][4];
     {
-      float part[NT][2][4];
+      const uint32_t* sk = reinterpret_cast<const uint32_t*>(R.ks) + lane;
+      const uint32_t dm[4] = {sk[0], sk[32], sk[0], sk[32]};
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[n][0][e] = part[n][1][e] = 0.f;
-      const __half2 d0 = as_h2(prmt(ks0, ks0, 0x1010)), m0 = as_h2(prmt(ks0, ks0, 0x3232));
-      const __half2 d1 = as_h2(prmt(ks1, ks1, 0x1010)), m1 = as_h2(prmt(ks1, ks1, 0x3232));
-      const uint32_t a0[4] = {k0.x, k0.y, k0.z, k0.w}, a1[4] = {k1.x, k1.y, k1.z, k1.w};
+        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+        mma16816(sc[n], dm, kb[n][0], kb[n][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] *= kup[n][e & 1];
+      }
+      // lane l gives the address of row l % 8 of group l / 8
+      uint32_t k0[4], k1[4];
+      const uint32_t at = smem_u32(&R.k[4 * (lane & 7) + ((lane >> 3) ^ ((lane >> 1) & 3))]);
+      ldsm_x4(at, k0);
+      ldsm_x4(at + 512u, k1);
+      const uint4 ks0 = R.ks[grp], ks1 = R.ks[grp + 8];
+      const uint32_t dm0[4] = {ks0.x, ks0.y, ks0.z, ks0.w}, dm1[4] = {ks1.x, ks1.y, ks1.z, ks1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        __half2 p0[4], p1[4];
-        unpack_pairs(a0[j], p0);
-        unpack_pairs(a1[j], p1);
+        uint32_t p0[4], p1[4];
+        spread(k0[j], p0);
+        spread(k1[j], p1);
+        const float d0 = __low2float(as_h2(dm0[j])), d1 = __low2float(as_h2(dm1[j]));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a[4] = {as_u32(__hfma2(p0[2 * h], d0, m0)), as_u32(__hfma2(p1[2 * h], d1, m1)),
-                                 as_u32(__hfma2(p0[2 * h + 1], d0, m0)), as_u32(__hfma2(p1[2 * h + 1], d1, m1))};
+        for (int n = 0; n < NT; ++n) {
+          float dot[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {p0[2 * h], p1[2 * h], p0[2 * h + 1], p1[2 * h + 1]};
             const uint2 b = Sh::kSharedQ ? S.q[8 * n + 2 * j + h][lane] : qb[n][j][h];
-            mma16816(part[n][h], a, b.x, b.y);
+            mma16816(dot, a, b.x, b.y);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] = fmaf(e < 2 ? d0 : d1, dot[e], sc[n][e]);
         }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = (part[n][0][e] + part[n][1][e]) * A.scale_log2e;
+        for (int e = 0; e < 4; ++e) sc[n][e] *= A.scale_log2e;
     }
     // ---- hidden positions; none where every column sees all 16
     const int j0 = u + (u < sink_rows ? 0 : gap), j1 = u + kUnit - 1 + (u + kUnit - 1 < sink_rows ? 0 : gap);
@@ -350,34 +386,38 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
     }
     // ---- O^T += V^T P: after transposing, this lane has group grp / 2 of the
     // dimensions and rows 2 tq, 2 tq + 1 (and those + 8)
-    uint32_t dv[2], mv[2];
+    uint32_t dv[2], dm[2];
     bool odd = false;  // a row has a value that is not finite
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // even lanes' rows get d, odd ones m, of the pair of positions
-      const uint32_t mine = transpose8(grp + 8 * i < rows ? (i ? vs1 : vs0) : 0u);
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
-      dv[i] = grp & 1 ? other : mine;
-      mv[i] = grp & 1 ? mine : other;
+      dm[i] = transpose8(grp + 8 * i < rows ? (i ? vs1 : vs0) : 0u);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, dm[i], 4);
+      dv[i] = grp & 1 ? other : dm[i];
       if (kMulti) {
         // infinity and NaN have the exponent's bits all set
-        const uint32_t top = as_u32(__hmul2(__float2half2_rn(15.f), as_h2(dv[i])));
-        const bool b0 = (top & 0x7C00u) == 0x7C00u || (mv[i] & 0x7C00u) == 0x7C00u;
-        const bool b1 = (top & 0x7C000000u) == 0x7C000000u || (mv[i] & 0x7C000000u) == 0x7C000000u;
+        const uint32_t top = as_u32(__hmul2(__float2half2_rn(15.f), as_h2(dv[i]))), mv = grp & 1 ? dm[i] : other;
+        const bool b0 = (top & 0x7C00u) == 0x7C00u || (mv & 0x7C00u) == 0x7C00u;
+        const bool b1 = (top & 0x7C000000u) == 0x7C000000u || (mv & 0x7C000000u) == 0x7C000000u;
         const uint32_t keep = (b0 ? 0u : 0xFFFFu) | (b1 ? 0u : 0xFFFF0000u);
         dv[i] &= keep;
-        mv[i] &= keep;
+        dm[i] &= keep;
         odd = odd || b0 || b1;
       }
     }
-    const Scaled s0(dv[0]), s1(dv[1]);
-    const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
-    auto values = [&](auto wide) {
+    {
+      const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t p0[4], p1[4];
-        s0.template operator()<decltype(wide)::value>(transpose8(a0[j]), p0);
-        s1.template operator()<decltype(wide)::value>(transpose8(a1[j]), p1);
+        spread(transpose8(a0[j]), p0);
+        spread(transpose8(a1[j]), p1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 off = as_h2(i & 1 ? 0x54805480u : 0x64086408u);  // 72, 1032
+          p0[i] = as_u32(__hmul2(__hsub2(as_h2(p0[i]), off), as_h2(dv[0])));
+          p1[i] = as_u32(__hmul2(__hsub2(as_h2(p1[i]), off), as_h2(dv[1])));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t a[4] = {p0[2 * h], p0[2 * h + 1], p1[2 * h], p1[2 * h + 1]};
@@ -385,13 +425,7 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
           for (int n = 0; n < NT; ++n) mma16816(o[n][2 * j + h], a, pb[n][0], pb[n][1]);
         }
       }
-    };
-    if (__any_sync(0xffffffffu, max(vs0 & 0x7FFFu, vs1 & 0x7FFFu) > kWideD))
-      values(std::true_type{});
-    else
-      values(std::false_type{});
-    {
-      const uint32_t a[4] = {mv[0], 0x3C003C00u, mv[1], 0x3C003C00u};
+      const uint32_t a[4] = {dm[0], 0x3C003C00u, dm[1], 0x3C003C00u};
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma16816(om[n], a, pb[n][0], pb[n][1]);
     }
@@ -415,6 +449,14 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
   }
   copy_wait<0>();
   __syncwarp();
+  // What 8 d + m of their group adds to this lane's values.
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float other = __shfl_xor_sync(0xffffffffu, om[n][e], 4);
+      om[n][e] = grp & 1 ? fmaf(8.f, other, om[n][e]) : fmaf(8.f, om[n][e], other);
+    }
   // The warp's references and sums of weights.
 #pragma unroll
   for (int n = 0; n < NT; ++n)

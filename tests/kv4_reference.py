@@ -16,6 +16,13 @@ def values(q4, dm):
         return (q * np.repeat(d, 32, -1) + np.repeat(m, 32, -1)).astype(np.float16)
 
 
+def exact(q4, dm):
+    """d q + m in 64 bits."""
+    q, d, m = unpack(q4, dm)
+    with np.errstate(invalid="ignore"):
+        return q * np.repeat(d, 32, -1) + np.repeat(m, 32, -1)
+
+
 def pack(x):
     """Packed rows of fp32 values [..., D], in fp32 as the library defines them."""
     b = x.reshape(*x.shape[:-1], -1, 32)
@@ -63,7 +70,7 @@ def seen(p, window, sinks):
 
 
 def attention(q, k, v, H, Hkv, pos0, window, sinks, scale, rows=None):
-    """64-bit attention of fp16 q [M][H][128] over fp16 rows k, v [Hkv][L][128]."""
+    """64-bit attention of fp16 q [M][H][128] over rows k, v [Hkv][L][128]."""
     rows = np.arange(q.shape[0]) if rows is None else rows
     out = np.zeros((len(rows), H, q.shape[2]))
     G = H // Hkv

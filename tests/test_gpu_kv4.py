@@ -216,16 +216,18 @@ def _attn(qk, cuda, q, cache, H, Hkv, pos0, window, sinks, scratch=None):
 def _check(qk, cuda, seed, M, H, Hkv, pos0, window, sinks, slack=3, rows=None):
     """Weights rounded to fp16 2^-11 relative each, those below 2^-24 of the largest flushed
     (2^-25 each, 2^13 of them in a warp at most), scores in fp32 (2^-12 of a weight in
-    all), the output's rounding 2^-11: against the largest |v|."""
+    all), the output's rounding 2^-11: against the largest |v|.  Few tokens have the
+    exact values d q + m, whose d (q - 8) is rounded, 2^-11 of 8 d; chunks those of fp16."""
     q, cache = _attn_inputs(seed, M, H, Hkv, pos0, pos0 + M + slack, window, sinks)
-    k, v = ref4.values(*cache[:2]), ref4.values(*cache[2:])
+    few = M * (H // Hkv) <= 32
+    k, v = ((ref4.exact if few else ref4.values)(*c) for c in (cache[:2], cache[2:]))
     got = _attn(qk, cuda, q, cache, H, Hkv, pos0, window, sinks)
     assert np.isfinite(got).all()
     vmax = np.abs(v[np.isfinite(v)].astype(np.float64)).max()
     if rows is not None:
         got = got[rows]
     _within(got, ref4.attention(q, k, v, H, Hkv, pos0, window, sinks, SCALE, rows),
-            vmax * (2.0 ** -10 + 2.0 ** -12 + 2.0 ** -12), "attention")
+            vmax * (2.0 ** -10 + 2.0 ** -12 + 2.0 ** -12) + few * 8 * 0.35 * 2.0 ** -11, "attention")
 
 
 NONE = 10 ** 9
@@ -250,7 +252,7 @@ def test_attention_group_sizes(qk_lib, cuda, H, Hkv):
 @pytest.mark.parametrize("M,pos0,window,sinks,H,Hkv", [
     (2, 0, NONE, 0, 8, 8), (8, 0, NONE, 0, 8, 8), (8, 0, 3, 2, 8, 8), (9, 1000, NONE, 0, 8, 8), (16, 3000, NONE, 0, 8, 8),
     (17, 3000, 1000, 5, 8, 8), (32, 5000, NONE, 0, 4, 4), (32, 0, 7, 3, 4, 4), (5, 20000, 8192, 4, 24, 8), (10, 77, NONE, 0, 24, 8),
-    (4, 4000, 0, 900, 16, 2), (4, 3, 0, 5, 16, 2), (8, 500, 1, 0, 12, 3), (31, 100, 50, 60, 2, 2), (2, 40, 20, 10 ** 7, 6, 2)])
+    (10, 9000, NONE, 0, 24, 8), (4, 4000, 0, 900, 16, 2), (4, 3, 0, 5, 16, 2), (8, 500, 1, 0, 12, 3), (31, 100, 50, 60, 2, 2), (2, 40, 20, 10 ** 7, 6, 2)])
 def test_attention_few_tokens(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
     """Several tokens in one to four tiles of columns; each its own window."""
     _check(qk_lib, cuda, 405, M, H, Hkv, pos0, window, sinks)
@@ -275,6 +277,35 @@ def test_attention_long_cache(qk_lib, cuda):
     """100000 positions.  A warp's share of 391 rounds its small weights to fp16 one by one:
     2^-25 each of the largest, 2^-16 in all; the tolerance above holds."""
     _check(qk_lib, cuda, 409, 1, 4, 2, 99999, NONE, 0)
+
+
+@pytest.mark.parametrize("M,pos0,H,Hkv", [(1, 500, 32, 8), (1, 40000, 8, 2), (1, 60000, 8, 8), (5, 3000, 24, 8), (10, 700, 24, 8),
+                                          (4, 50000, 8, 4)])
+def test_attention_few_tokens_precision(qk_lib, cuda, M, pos0, H, Hkv):
+    """Three roundings to fp16 (weights, d (q - 8), outputs) of at most half a step, evenly
+    spread: 2^-11 / sqrt(3) of a value each, at random.  Of random values, whose mean nearly
+    vanishes, d (q - 8) is as large as d q + m: together 2^-11 in the 2-norm.  Scores are off by
+    2^-21 of sums of 1024 |Q| d 32, 2^-11 / sqrt(3) less by far."""
+    q, cache = _attn_inputs(419, M, H, Hkv, pos0, pos0 + M, NONE, 0)
+    want = ref4.attention(q, ref4.exact(*cache[:2]), ref4.exact(*cache[2:]), H, Hkv, pos0, NONE, 0, SCALE)
+    got = _attn(qk_lib, cuda, q, cache, H, Hkv, pos0, NONE, 0).astype(np.float64)
+    assert np.linalg.norm(got - want) <= 2.0 ** -11 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("M,sizes", [(1, (1e-3, 1.0, 300.0, 2e-4)), (3, (1e-3, 1.0, 300.0, 2e-4)), (10, (1.0, 1e-3, 3.0, 0.1))])
+def test_attention_heads_of_very_different_sizes(qk_lib, cuda, M, sizes):
+    """Queries of one key/value head whose sizes lie far apart: each as exact as alone.  Of
+    the largest, whose scores are beyond what fp32 holds to 2^-12, only that they are finite."""
+    q, cache = _attn_inputs(420, M, 8, 2, 900, 900 + M, NONE, 0)
+    size = np.array(sizes * 2)[None, :, None]
+    q = (q * size).astype(np.float16)
+    k, v = ref4.exact(*cache[:2]), ref4.exact(*cache[2:])
+    want = ref4.attention(q, k, v, 8, 2, 900, NONE, 0, SCALE)
+    got = _attn(qk_lib, cuda, q, cache, 8, 2, 900, NONE, 0)
+    assert np.isfinite(got).all()
+    fine = np.flatnonzero(size[0, :, 0] < 100)
+    vmax = np.abs(v).max()
+    _within(got[:, fine], want[:, fine], vmax * (2.0 ** -10 + 2.0 ** -11) + 8 * 0.35 * 2.0 ** -11, "heads")
 
 
 def test_attention_sees_nothing(qk_lib, cuda):

@@ -80,9 +80,9 @@ def test_attention_q4_scratch(qk_lib):
     assert f(9, 8, 2, 128, 1000, 100, 30) == 512 * 2 * (100 + 8 + 30)
     assert f(9, 8, 2, 128, 1000, 100, none) == 512 * 2 * 1009
     assert f(9, 8, 2, 128, 1000, 0) == 0 and f(9, 8, 2, 128, 1000, 0, 7) == 512 * 2 * 7
-    # few: from 32768 positions of all heads on, partial results of the CTAs
-    assert f(1, 8, 2, 128, 16382, none) == 0
-    assert 0 < f(1, 8, 2, 128, 16383, none) <= 1 << 20 and 0 < f(8, 8, 2, 128, 10 ** 6, none) <= 4 << 20
+    # few: from 65536 positions of all heads on, partial results of the CTAs
+    assert f(1, 8, 2, 128, 32766, none) == 0
+    assert 0 < f(1, 8, 2, 128, 32767, none) <= 1 << 20 and 0 < f(8, 8, 2, 128, 10 ** 6, none) <= 4 << 20
     assert f(1, 8, 2, 128, 10 ** 6, 4096, 4) == 0
     for bad in ((-1, 8, 2, 128, 0, 1), (1, 8, 3, 128, 0, 1), (1, 8, 2, 64, 0, 1), (1, 8, 2, 128, -1, 1), (1, 8, 2, 128, 0, -1),
                 (1, 8, 2, 128, 0, 1, -1), (1, 8, 2, 128, 1 << 30, 1), (1, 18, 2, 128, 0, 1)):
