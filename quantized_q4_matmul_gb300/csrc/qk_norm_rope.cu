@@ -12,15 +12,21 @@
 //   m = fp16(min x),  d = fp16(max(max x - m, 0) / 15),
 //   q = (x - m) / d rounded to the nearest of 0 .. 15 (0 where d = 0).
 //
-// HBM-bound for a prompt: each input is read once.  A CTA has a few tokens and
-// computes their sines and cosines together, while its first rows are on their way;
-// a row is a head of a token, 8 dimensions a lane, and the next rows load while one
-// is computed.  The sum of squares and a group's extremes meet by shuffles.  Where a
-// whole head of the half layout turns, a lane has two runs of four dimensions, each
-// other's mates; otherwise a run of eight, and the half layout's mates, which other
-// lanes hold, pass through shared memory (2047 tokens of 32 + 4 + 4 heads of 128:
-// 20.1 us so).  Few tokens:
-// their heads are spread over several CTAs.
+// A CTA has a few tokens and computes their sines and cosines together, while its
+// first rows are on their way; a row is a head of a token, 8 dimensions a lane, and two
+// rows load while one is computed.  The sum of squares and a group's extremes
+// meet by shuffles.  Where a whole head of the half layout turns, a lane has two runs of
+// four dimensions, each other's mates; otherwise a run of eight, and the half layout's
+// mates, which other lanes hold, pass through shared memory (2047 tokens of 32 + 4 + 4
+// heads of 128 in the half layout: 14.7 us with mates in a lane, 20.1 through shared
+// memory; the interleaved layout 15.7).  A value's level comes from a reciprocal, and from
+// a division where that is near a border between two levels: a division for each took
+// twice as long.
+//
+// Every input is read once: 4095 tokens of 24 + 8 + 8 heads of 128 into 4 bits move 115
+// MB (17 us at a copy's rate) in 25 us, bound by instructions (178 for a row and warp,
+// issue slots 79 % busy); into fp16 25.3 us.  Four CTAs an SM: three took 18.7 us where four
+// took 15.9 (2047 tokens into fp16).  One token 2.1 us, latency.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -36,7 +42,7 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrMaxD = 512;
-constexpr int kNrTokens = 4;  // of a CTA, where there are many
+constexpr int kNrTokens = 4;  // of a CTA at most
 
 __device__ __forceinline__ uint32_t pack2h(float a, float b) {
   const __half2 x = __floats2half2_rn(a, b);
@@ -322,9 +328,12 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t s) {
   int lph_log2 = 0;
   while (lph_log2 < 5 && (8 << lph_log2) < r.D) ++lph_log2;
   const int slots = kNrThreads >> lph_log2, heads = r.H + 2 * r.Hkv;
-  // Few tokens: one a CTA, its heads over several; many: kNrTokens a CTA.
-  const bool few = r.M <= 2 * (int64_t)device_sms();
-  const int tokens = few ? 1 : kNrTokens, per_cta = few ? std::min(slots, heads) : heads;
+  // Few tokens: one a CTA, its heads over several CTAs.  us with 1, 2, 4 tokens a CTA,
+  // 24 + 8 + 8 heads of 128 into fp16: 152 tokens 3.7, 4.3, 6.6; 304: 5.2, 4.3, 6.7; 1216:
+  // 17.2, 8.4, 8.8; 2047: 27.7, 13.8, 15.0; 4095: 54.2, 26.2, 25.3; 8190: 106, 49.9, 47.5.
+  const int64_t sms = device_sms();
+  const int tokens = 2 * r.M <= 3 * sms ? 1 : r.M <= 16 * sms ? 2 : kNrTokens;
+  const int per_cta = tokens == 1 ? std::min(slots, heads) : heads;
   const dim3 grid((unsigned)((r.M + tokens - 1) / tokens), (unsigned)((heads + per_cta - 1) / per_cta));
   const bool mates = r.half && r.n_rot == r.D && !two && r.D % 64 == 0;
   return launch_dependent(two     ? norm_rope_kernel<kQ4, 2, false>
