@@ -12,27 +12,34 @@
 //
 // Every decision compares sums of up to 2^19 weights with a border, and a row of
 // 10^5 tokens has 10^5 borders: sums in fp32 would choose another token in some
-// percent of the rows.  Weights are therefore computed in pairs of fp32 to about
-// 2^-42 (a difference without error, a table of 2^(-i / 256) and a polynomial of
+// percent of the rows.  Weights are therefore computed in pairs of fp32 to 2^-38 of
+// themselves (a difference without error, a table of 2^(-i / 256) and a polynomial of
 // degree 4) and summed in pairs within a thread and in 64-bit integers, multiples
 // of 2^-44 of the largest weight, between threads: no order changes a result.
 //
-// A cluster of C CTAs has a row and goes over it three times (it stays in L2; kept
-// in shared memory it was no faster):
-//   1. its maximum and minimum, and whether it can be sampled from.  Where top_k (up
-//      to 512) or min_p alone bounds what is kept, a second pass lists the tokens
-//      above a cut, the least of the CTAs' top_k / C-th largest of their threads'
-//      maxima (so that top_k tokens lie above it, and few more) or min_p's border
-//      with a margin: they are the candidates, and nothing else is needed.  Otherwise, or where they are many:
-//   2. a histogram over (max - x) of counts and mean positions within a bin, from
-//      which the bins that hold the three borders and the token follow, the sums
-//      being known to some 1e-5.  Logits below the cut are left out;
-//   3. the exact sums of what lies before, between and behind those bins, and a
-//      list of the tokens in them (candidates).
+// A cluster of C CTAs has a row and goes over it two or three times (it stays in L2;
+// kept in shared memory it was no faster):
+//   1. its maximum and minimum, and whether it can be sampled from;
+//   2. where top_k (up to 512) or min_p alone bounds what is kept, a list of the tokens
+//      above a cut: the least of the CTAs' top_k / C-th largest of their threads' (or
+//      warps') maxima, so that top_k tokens lie above it, and few more, or min_p's
+//      border with a margin.  They are the candidates, and nothing else is needed.
+//      Otherwise, or where they are many, a histogram over (max - x) of counts and
+//      mean positions within a bin, from which the bins that hold the borders and
+//      the token follow, the sums being known to 1e-5;
+//   3. with the histogram, the exact sums of what lies before, between and behind
+//      those bins, and a list of the tokens in them (candidates).
 // Rank 0 sorts the candidates, adds their weights up and answers the questions in
 // turn, checking for each that the border lies where it was expected.  Where it
 // does not, or the candidates are too many (equal logits), it searches the order
 // bit by bit instead, with an exact sum over the row at each step.
+//
+// Bound by latency for one row (9.3 us for 128256 logits with top_k 40: two passes of
+// 1 us, two cluster barriers, then a dozen short steps of one CTA whose code is
+// fetched once), and by instructions where all weights count: 512 rows of 128256
+// without bounds 323 us, issue slots 77 % busy, 128 instructions a logit and warp, most
+// of them the weights' pairs (packed two at a time; one at a time 387 us where packed took
+// 363); HBM 25 %.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -58,11 +65,15 @@ constexpr int kSegs = 5;
 constexpr int kNone = kSegs, kListed = kSegs + 1;  // classes of logits of no account, and of candidates
 constexpr float kOne = 17592186044416.f;  // 2^44: the largest weight
 constexpr float kMagic = 12582912.f;      // 1.5 2^23: adding it rounds to an integer in the low bits
-constexpr float kSlack = 6e-5f;           // of the histogram's sums, relative
+constexpr float kSlack = 3e-5f;           // of the histogram's sums, relative: twice what they may be off
+// The histogram ends this many T below the maximum, where weights are 2^-45 of the
+// largest; with a top_k, whose last token may lie anywhere, where they are 0 in
+// every sum (the bins are wider then: 2^-16 of a bin's weight is lost).
+constexpr float kSpan = 31.f, kSpanK = 83.f;
 // Bins further than this many T below the maximum go without mean positions: of
 // tokens of weight w that hold the whole sum, an error of a bin's 12th root each
-// leaves sqrt(w) of one, 1.5e-5 of the sum at 10 T.
-constexpr float kMeans = 10.f;
+// leaves sqrt(w) of one, 1.5e-5 of the sum at 10 T, and at 14 T of the wider bins.
+constexpr float kMeans = 10.f, kMeansK = 14.f;
 
 struct SaTable {
   float h[256], l[256];  // 2^(-i / 256) as a pair
@@ -504,7 +515,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     __syncwarp();
     cluster_arrive();  // its wait is before the first write to another CTA
   }
-  for (int i = tid; i < kBins / 2; i += kSaThreads) reinterpret_cast<uint4*>(S.first.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < kBins / 2; i += kSaThreads)
+    reinterpret_cast<uint4*>(S.first.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid < 256) {
     S.table.h[tid] = A.table.h[tid];
     S.table.l[tid] = A.table.l[tid];
@@ -633,7 +645,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   const Weigh W{mx, 83.f * T, A.ch, A.cl, &S.table};
 
   const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
-  const float span = fminf(mx - mn, 31.f * T);
+  const float span = fminf(mx - mn, (with_k ? kSpanK : kSpan) * T);
   const float scale = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;
   // Logits below the cut, -inf among them, are of no account.
   if (!with_k || !by_k) cut = -INFINITY;
@@ -679,15 +691,16 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     cluster_meet(C);
     n = (int)min(__reduce_add_sync(0xffffffffu, lane < C ? S.listed_by[lane] : 0u), (uint32_t)kCap + 1u);
   }
+  bool k_far = false;  // the last of the top_k has the weight 0 in every sum
   const bool listed_all = n <= kCap;  // everything from the cut on
   int segs = 0;
   if (listed_all) {
     if (rank != 0) return;
     if (tid < kSegs) S.base[tid] = 0ull, S.base_cnt[tid] = 0u;
   } else {
-    // ---- 2. the histogram.  Logits further than 31 T below the maximum are in the last
+    // ---- 2. the histogram.  Logits further below the maximum than `span` are in the last
     // bin; those that cannot be kept are left out.
-    const float means = mx - kMeans * T;
+    const float means = mx - (with_k ? kMeansK : kMeans) * T;
     if (rank == 0 && tid == 0) S.ncand = 0u;  // what did not fit is listed again
     each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int) {
 #pragma unroll
@@ -707,13 +720,15 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       const int mine = kBins / 2 / C;  // pairs of bins
 #pragma unroll 1
       for (int i = tid; i < 2 * mine; i += kSaThreads) {
-        const uint32_t at = smem_u32(i < mine ? &S.first.cnt[2 * (rank * mine + i)] : &S.first.frac[2 * (rank * mine + i - mine)]);
+        const uint32_t at =
+            smem_u32(i < mine ? &S.first.cnt[2 * (rank * mine + i)] : &S.first.frac[2 * (rank * mine + i - mine)]);
         uint2 n = make_uint2(0u, 0u);
 #pragma unroll 1
         for (int r0 = 0; r0 < C; r0 += 8) {
           uint2 x[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) x[r] = r0 + r < C ? ld_cluster_v2(mapa_shared(at, (uint32_t)(r0 + r))) : make_uint2(0u, 0u);
+          for (int r = 0; r < 8; ++r)
+            x[r] = r0 + r < C ? ld_cluster_v2(mapa_shared(at, (uint32_t)(r0 + r))) : make_uint2(0u, 0u);
 #pragma unroll
           for (int r = 0; r < 8; ++r) n.x += x[r].x, n.y += x[r].y;
         }
@@ -781,21 +796,32 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
 
     // The bins where the borders are: ranges [lo, hi] for k, p, m and the token.  Every
     // warp finds them.
-    auto range = [&](float from, float to, int& first, int& last) {
+    // A share f of a sum S is found within 2 kSlack f (1 - f) S, as the errors of what
+    // lies before it and behind it are relative to these: towards the end of a row,
+    // where thousands of tokens share 1e-4 of the sum, that is a few of them.  (8 times
+    // that, for single tokens' places in their bins.)
+    auto range = [&](float f, float from, float to, int& first, int& last) {
+      const float slack = kSlack * to * fminf(16.f * (1.f - f), 1.f) + 256.f;
+      from = f * from - slack;
+      to = f * to + slack;
       first = reach(S.first.frac, from > 1.f ? (uint32_t)from : 1u);
-      last = reach(S.first.frac, to > 1.f ? (uint32_t)to : 1u);
+      last = reach(S.first.frac, to > 1.f ? min((uint32_t)to, total) : 1u);
+      return slack;
     };
     float s_lo = (float)total, s_hi = s_lo;  // the kept weights, within kSlack
     int b_hi = kBins - 1;                    // the last bin that may hold the last kept token
     if (with_k) {
-      lo[0] = hi[0] = b_hi = reach(S.first.cnt, (uint32_t)A.a.top_k);
-      s_lo = sum_before(b_hi);
-      s_hi = sum_before(b_hi + 1);
+      const int b = reach(S.first.cnt, (uint32_t)A.a.top_k);
+      k_far = b == kBins - 1 && span < mx - mn;
+      if (!k_far) {
+        lo[0] = hi[0] = b_hi = b;
+        s_lo = sum_before(b);
+        s_hi = sum_before(b + 1);
+      }
     }
     if (with_p) {
-      const float slack = kSlack * s_hi + 8.f;
-      range(A.a.top_p * s_lo - slack, A.a.top_p * s_hi + slack, lo[1], hi[1]);
-      s_lo *= A.a.top_p;
+      const float slack = range(A.a.top_p, s_lo, s_hi, lo[1], hi[1]);
+      s_lo = A.a.top_p * s_lo - slack;
       if (hi[1] < b_hi) {
         b_hi = hi[1];
         s_hi = sum_before(b_hi + 1);
@@ -815,12 +841,11 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       lo[3] = 0;
       hi[3] = b_hi;
     } else {
-      const float slack = kSlack * (float)total + 8.f;
-      range(u * s_lo - slack, u * s_hi + slack, lo[3], hi[3]);
+      range(u, s_lo, s_hi, lo[3], hi[3]);
     }
     // Classes of the bins: kListed for the candidates', else how many of the ranges
     // end before.
-    const bool all = !with_k && (with_p || !with_m);  // every weight counts
+    const bool all = (!with_k || k_far) && (with_p || !with_m);  // every weight counts
     int last = all ? kBins - 1 : -1;                  // the last bin that matters
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -980,10 +1005,10 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       S.second.place[j] |= S.base_cnt[seg] + (uint32_t)j + 1u;
     }
     __syncthreads();
-    uint32_t n_keep = finite;
+    uint32_t n_keep = k_far ? (uint32_t)A.a.top_k : finite;
     unsigned long long s_keep = S.base[kSegs - 1] + listed;  // of all, where `all`
     bool ok = true, rest;
-    if (with_k) {
+    if (with_k && !k_far) {
 #pragma unroll 1
       for (int j = tid; j < n; j += kSaThreads)
         if ((S.second.place[j] & 0x7FFFFFFFu) == (uint32_t)A.a.top_k) S.s_k = S.first.upto[j], S.found[0] = 1;
@@ -1057,13 +1082,23 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   static PerDeviceFlag attr_set;
   const int dev = current_device();
   if (!attr_set.done(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SaShared));
+    cudaError_t e =
+        cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SaShared));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
+  // CTAs for each row: as many as fill two CTAs an SM, up to 8; 16 for four rows at
+  // most.  Where a long row's sums are needed, which keep the SMs busy, some SMs may
+  // have more.  us with 1, 2, 4, 8, 16 CTAs, 128256 logits: one row, top_k 40: 29.8, 21.4,
+  // 16.8, 10.2, 9.3; 8 rows 30.6, 21.7, 17.9, 12.1, 12.9; 64 rows, top_p 0.9: 137, 98, 62, 79,
+  // 125; 80 rows 129, 99, 89; 160 rows 179, 151, 145; 512 rows 341, 333, 394.
+  const bool sums = a.temperature > 0.f && (a.top_k == 0 ? a.top_p < 1.f || a.min_p == 0.f : a.top_k > kSaThreads);
+  const int64_t fill = (sums && a.V >= 65536 ? 5 : 4) * (int64_t)device_sms() / 2;
   int C = 1;
-  while (C < kSaMaxCluster && a.M * 2 * C <= (C < 8 ? 2 * (int64_t)device_sms() : 64) && a.V >= 2048 * 2 * C) C *= 2;
+  while (C < kSaMaxCluster && a.M * 2 * C <= (C < 4 ? fill : C < 8 ? 2 * (int64_t)device_sms() : 64) &&
+         a.V >= 2048 * 2 * C)
+    C *= 2;
   A.C = C;
   return launch_dependent(sample_kernel, dim3((unsigned)(a.M * C)), kSaThreads, sizeof(SaShared), (unsigned)C, s, A);
 }
