@@ -204,17 +204,21 @@ __global__ void __launch_bounds__(Q4Shape<NT, W>::kThreads, Q4Shape<NT, W>::kPer
   // Q: the product's k axis in step (group j, half h) is dims 32 j + 8 tq + 2 h and + 4
   // (first register), and those + 1 (second).
   uint2 qb[NT][4][2];
-  uint32_t kb[NT][2];  // of column grp and group tq: (what takes the offsets off the product, the sum of Q) 2^-k, high and low parts
+  // of column grp and group tq: (what takes the offsets off the product, the sum of Q) 2^-k, as high and low parts
+  uint32_t kb[NT][2];
   float kup[NT][2];    // 2^k of this lane's columns
   int cpos[NT][2];    // the positions of this lane's columns
-  float o[NT][8][4];  // [column tile][2 j + h]: dims 32 (grp / 2) + 8 j + 4 (grp % 2) + 2 h (+ 1: elements 2, 3), columns 2 tq (+ 1)
-  float om[NT][4];    // elements 0, 1: weights times d (even grp) or m (odd) of group grp / 2; 2, 3: the columns' sums of weights
+  // [column tile][2 j + h]: dims 32 (grp / 2) + 8 j + 4 (grp % 2) + 2 h (+ 1: elements 2, 3), columns 2 tq (+ 1)
+  float o[NT][8][4];
+  // elements 0, 1: weights times d (even grp) or m (odd) of group grp / 2; 2, 3: the columns' sums of weights
+  float om[NT][4];
   float m[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int col = 8 * n + grp;
     const int token = kMulti ? col / A.G : 0;
-    const uint4* qr = reinterpret_cast<const uint4*>(A.q + ((int64_t)token * A.H + g * A.G + (col - token * A.G)) * kD) + tq;
+    const int64_t row = (int64_t)token * A.H + g * A.G + (col - token * A.G);
+    const uint4* qr = reinterpret_cast<const uint4*>(A.q + row * kD) + tq;
     float even[4] = {0.f, 0.f, 0.f, 0.f}, odd[4] = {0.f, 0.f, 0.f, 0.f};  // of the nibbles with the offsets 1024 and 64
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -563,7 +567,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_q4_join_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = A.M * A.G, g = blockIdx.x / cols, col = blockIdx.x - g * cols;
   const float4* o = reinterpret_cast<const float4*>(A.part) + (int64_t)blockIdx.x * A.C * (kD / 4) + lane;
-  const float2* st = reinterpret_cast<const float2*>(A.part + (int64_t)A.Hkv * cols * A.C * kD) + (int64_t)blockIdx.x * A.C;
+  const float2* st =
+      reinterpret_cast<const float2*>(A.part + (int64_t)A.Hkv * cols * A.C * kD) + (int64_t)blockIdx.x * A.C;
   dependent_wait();
   float M = -INFINITY;
   for (int r = lane; r < A.C; r += 32) M = fmaxf(M, st[r].x);
