@@ -517,14 +517,15 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * temperature 0 gives the first token in the order, a logprob of 0 and kept 1.  A
  * row that holds NaN or +inf, or nothing but -inf, gives token -1, a NaN logprob
  * and kept 0.  u below 0 or NaN counts as 0, u of 1 or more as the largest fp32
- * number below 1.  The sums are exact to about 2^-40 of the largest weight a
- * token (weights below 2^-45 of the largest count as 0 in them), so that a token
- * follows from the definition rather than from the order of a sum; the same call
- * repeats its bits, whatever M.  temperature is 0 or 1e-6 .. 1e6, top_p 0 .. 1, min_p
- * 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need not be 16-byte aligned
- * (any V), the buffers do.  No output may overlap another or an input.  Thousands
- * of equal logits around the last kept token, or around the chosen one, make a
- * row slow (0.1 to 1 ms).  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
+ * number below 1.  A weight enters the sums within 2^-38 of itself and 2^-45 of the
+ * largest, so that a token follows from the definition, but where a border lies
+ * closer than 2^-30 of the sum to a decision, rather than from the order of a sum.
+ * How many CTAs share a row follows M and the device, and with it the sums' last
+ * bits; the same call repeats its bits.  temperature is 0 or 1e-6 .. 1e6, top_p
+ * 0 .. 1, min_p 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need
+ * not be 16-byte aligned (any V), the buffers do.  No output may overlap another or
+ * an input.  Thousands of equal logits around the last kept token, or around the
+ * chosen one, make a row slow (0.1 to 2 ms).  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
  */
 qk_status qk_sample(const float *logits, const float *u, int32_t *token, float *logprob, int32_t *kept, int64_t M,
                     int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream);

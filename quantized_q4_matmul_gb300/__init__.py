@@ -147,8 +147,8 @@ def lib():
         L.qk_norm_rope_kv_append.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64,
                                              i32, f32, vp]
         L.qk_norm_rope_kv_append_q4.restype = i32
-        L.qk_norm_rope_kv_append_q4.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64,
-                                                i64, i64, i32, f32, vp]
+        L.qk_norm_rope_kv_append_q4.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
+                                                i64, i64, i64, i32, f32, vp]
         L.qk_dequant_kv_q4.restype = i32
         L.qk_dequant_kv_q4.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, vp]
         L.qk_gqa_attention_q4.restype = i32
@@ -450,16 +450,18 @@ def qk_norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_fr
     cn = 2 * _size(H_kv, L_max, D)
     w = "qk_norm_rope_kv_append: %s"
     a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
-    _check(lib().qk_norm_rope_kv_append(*a, _buf(k_cache, cn, (w, "k_cache"), _F16), _buf(v_cache, cn, (w, "v_cache"), _F16),
-                                        M, H, H_kv, D, int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
-                                        _stream(stream)), "qk_norm_rope_kv_append")
+    _check(lib().qk_norm_rope_kv_append(*a, _buf(k_cache, cn, (w, "k_cache"), _F16),
+                                        _buf(v_cache, cn, (w, "v_cache"), _F16), M, H, H_kv, D, int(n_rot),
+                                        int(pos0), L_max, int(layout), float(magnitude), _stream(stream)),
+           "qk_norm_rope_kv_append")
 
 
 def _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot):
     qn, kn = _size(M, H, D), _size(M, H_kv, D)
     return (_buf(q, 4 * qn, (w, "q"), _F32), _buf(k, 4 * kn, (w, "k"), _F32), _buf(v, 4 * kn, (w, "v"), _F32),
-            _buf(q_gamma_f16, 2 * _n(D), (w, "q_gamma_f16"), _F16), _buf(k_gamma_f16, 2 * _n(D), (w, "k_gamma_f16"), _F16),
-            float(eps), _buf(inv_freq, 4 * _n(n_rot), (w, "inv_freq"), _F64), _buf(q_f16, 2 * qn, (w, "q_f16"), _F16))
+            _buf(q_gamma_f16, 2 * _n(D), (w, "q_gamma_f16"), _F16),
+            _buf(k_gamma_f16, 2 * _n(D), (w, "k_gamma_f16"), _F16), float(eps),
+            _buf(inv_freq, 4 * _n(n_rot), (w, "inv_freq"), _F64), _buf(q_f16, 2 * qn, (w, "q_f16"), _F16))
 
 
 def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_freq, q_f16, k_q4, k_dm, v_q4, v_dm,
@@ -471,18 +473,22 @@ def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv
     cn = _size(H_kv, L_max, D)
     w = "qk_norm_rope_kv_append_q4: %s"
     a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
-    _check(lib().qk_norm_rope_kv_append_q4(*a, _buf(k_q4, cn // 2, (w, "k_q4"), _U8), _buf(k_dm, cn // 8, (w, "k_dm"), _F16),
-                                           _buf(v_q4, cn // 2, (w, "v_q4"), _U8), _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
+    _check(lib().qk_norm_rope_kv_append_q4(*a, _buf(k_q4, cn // 2, (w, "k_q4"), _U8),
+                                           _buf(k_dm, cn // 8, (w, "k_dm"), _F16),
+                                           _buf(v_q4, cn // 2, (w, "v_q4"), _U8),
+                                           _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
                                            M, H, H_kv, D, int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
                                            _stream(stream)), "qk_norm_rope_kv_append_q4")
 
 
 def qk_dequant_kv_q4(q4, dm, out_f16, H_kv: int, D: int, pos0: int, M: int, L_max: int, stream=None) -> None:
     """Rows pos0 .. pos0 + M - 1 of one tensor of a 4-bit cache as fp16 [H_kv][M][D] (see include/qk.h)."""
-    cn = _size(int(H_kv), int(L_max), int(D))
-    _check(lib().qk_dequant_kv_q4(_buf(q4, cn // 2, "qk_dequant_kv_q4: q4", _U8), _buf(dm, cn // 8, "qk_dequant_kv_q4: dm", _F16),
-                                  _buf(out_f16, 2 * _size(int(H_kv), int(M), int(D)), "qk_dequant_kv_q4: out_f16", _F16),
-                                  int(H_kv), int(D), int(pos0), int(M), int(L_max), _stream(stream)), "qk_dequant_kv_q4")
+    H_kv, D, M, L_max = int(H_kv), int(D), int(M), int(L_max)
+    cn = _size(H_kv, L_max, D)
+    _check(lib().qk_dequant_kv_q4(_buf(q4, cn // 2, "qk_dequant_kv_q4: q4", _U8),
+                                  _buf(dm, cn // 8, "qk_dequant_kv_q4: dm", _F16),
+                                  _buf(out_f16, 2 * _size(H_kv, M, D), "qk_dequant_kv_q4: out_f16", _F16), H_kv, D,
+                                  int(pos0), M, L_max, _stream(stream)), "qk_dequant_kv_q4")
 
 
 def qk_rmsnorm_scratch_bytes(qtype, M: int, K: int, gateup: bool = False) -> int:
@@ -619,14 +625,15 @@ def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_
 
 def qk_gqa_attention_q4_scratch_bytes(M: int, H: int, H_kv: int, D: int, pos0: int, window: int, sinks: int = 0) -> int:
     """Scratch bytes that qk_gqa_attention_q4 needs (0: none); host only."""
-    r = int(lib().qk_gqa_attention_q4_scratch_bytes(int(M), int(H), int(H_kv), int(D), int(pos0), int(window), int(sinks)))
+    r = int(lib().qk_gqa_attention_q4_scratch_bytes(int(M), int(H), int(H_kv), int(D), int(pos0), int(window),
+                                                    int(sinks)))
     if r < 0:
         raise ValueError("qk_gqa_attention_q4_scratch_bytes: invalid sizes")
     return r
 
 
-def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, H_kv: int, D: int, pos0: int, L_max: int,
-                        scale: float, window: int, sinks: int = 0, scratch=None, stream=None) -> None:
+def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, H_kv: int, D: int, pos0: int,
+                        L_max: int, scale: float, window: int, sinks: int = 0, scratch=None, stream=None) -> None:
     """qk_gqa_attention_window over a cache held in 4 bits (see include/qk.h); scratch:
     qk_gqa_attention_q4_scratch_bytes of device memory where that is not 0."""
     M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
@@ -636,8 +643,8 @@ def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, 
     w = "qk_gqa_attention_q4: %s"
     _check(lib().qk_gqa_attention_q4(_buf(q_f16, 2 * qn, (w, "q_f16"), _F16), _buf(k_q4, cn // 2, (w, "k_q4"), _U8),
                                      _buf(k_dm, cn // 8, (w, "k_dm"), _F16), _buf(v_q4, cn // 2, (w, "v_q4"), _U8),
-                                     _buf(v_dm, cn // 8, (w, "v_dm"), _F16), _buf(out_f16, 2 * qn, (w, "out_f16"), _F16), M,
-                                     H, H_kv, D, pos0, L_max, float(scale), window, sinks,
+                                     _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
+                                     _buf(out_f16, 2 * qn, (w, "out_f16"), _F16), M, H, H_kv, D, pos0, L_max, float(scale), window, sinks,
                                      _buf(scratch, need, (w, "scratch"), _F16 + _U8) if need else 0, _stream(stream)),
            "qk_gqa_attention_q4")
 

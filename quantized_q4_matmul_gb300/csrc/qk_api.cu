@@ -764,8 +764,8 @@ qk_status qk_gqa_attention_q4(const uint16_t* q_f16, const uint8_t* k_q4, const 
   if (st == QK_OK) st = check_spans_device(b, n);
   if (st != QK_OK) return st;
   const qk::Q4Cache c{k_q4, v_q4, k_dm, v_dm};
-  return map_cuda(qk::launch_gqa_attention_q4(q_f16, c, out_f16, M, (int)H, (int)H_kv, pos0, L_max, scale, window, sinks,
-                                              scratch, reinterpret_cast<cudaStream_t>(stream)));
+  return map_cuda(qk::launch_gqa_attention_q4(q_f16, c, out_f16, M, (int)H, (int)H_kv, pos0, L_max, scale, window,
+                                              sinks, scratch, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 qk_status qk_rope_inv_freq(const qk_rope_config* c, int64_t n_rot, double* out) {
@@ -827,7 +827,8 @@ qk_status qk_logprobs(const float* logits, const int32_t* tokens, float* logprob
 qk_status qk_sample(const float* logits, const float* u, int32_t* token, float* logprob, int32_t* kept, int64_t M,
                     int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream) {
   if (M < 0 || M >= kMaxDim || V <= 0 || V > ((int64_t)1 << 19) || top_k < 0 || !(top_p >= 0.f && top_p <= 1.f) ||
-      !(min_p == 0.f || (min_p >= 1e-12f && min_p <= 1.f)) || !(temperature == 0.f || (temperature >= 1e-6f && temperature <= 1e6f)))
+      !(min_p == 0.f || (min_p >= 1e-12f && min_p <= 1.f)) ||
+      !(temperature == 0.f || (temperature >= 1e-6f && temperature <= 1e6f)))
     return QK_ERR_SHAPE;
   if (M == 0) return QK_OK;
   Span b[5] = {{logits, 4 * M * V, false}, {u, 4 * M, false}, {token, 4 * M, true}};  // below 2^53

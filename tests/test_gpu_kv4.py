@@ -252,7 +252,8 @@ def test_attention_group_sizes(qk_lib, cuda, H, Hkv):
 @pytest.mark.parametrize("M,pos0,window,sinks,H,Hkv", [
     (2, 0, NONE, 0, 8, 8), (8, 0, NONE, 0, 8, 8), (8, 0, 3, 2, 8, 8), (9, 1000, NONE, 0, 8, 8), (16, 3000, NONE, 0, 8, 8),
     (17, 3000, 1000, 5, 8, 8), (32, 5000, NONE, 0, 4, 4), (32, 0, 7, 3, 4, 4), (5, 20000, 8192, 4, 24, 8), (10, 77, NONE, 0, 24, 8),
-    (10, 9000, NONE, 0, 24, 8), (4, 4000, 0, 900, 16, 2), (4, 3, 0, 5, 16, 2), (8, 500, 1, 0, 12, 3), (31, 100, 50, 60, 2, 2), (2, 40, 20, 10 ** 7, 6, 2)])
+    (10, 9000, NONE, 0, 24, 8), (4, 4000, 0, 900, 16, 2), (4, 3, 0, 5, 16, 2), (8, 500, 1, 0, 12, 3),
+    (31, 100, 50, 60, 2, 2), (2, 40, 20, 10 ** 7, 6, 2)])
 def test_attention_few_tokens(qk_lib, cuda, M, pos0, window, sinks, H, Hkv):
     """Several tokens in one to four tiles of columns; each its own window."""
     _check(qk_lib, cuda, 405, M, H, Hkv, pos0, window, sinks)

@@ -3,7 +3,7 @@
 Tokens and kept counts are whole numbers: they are equal to the definition's
 wherever no border lies closer than 2^-30 of the sum to a decision (the kernel's
 sums are within that: 8192 threads' shares rounded to 2^-45 each, five a thread,
-and weights within 2^-42).  Log probabilities are (x - max) / T less log1p of the
+and weights within 2^-38 of themselves).  Log probabilities are (x - max) / T less log1p of the
 kept sum without its largest weight, both at most 0 in fp32: a difference and a
 quotient of 2^-24 each, log1p within 2^-23, their sum 2^-24, less than 2^-22 in all;
 the sum within 2^-30.
@@ -41,7 +41,7 @@ def reference(x, u, T, k=0, p=1.0, mp=0.0):
         n = min(n, n_p)
     if mp > 0:
         n_m = int((w >= mp).sum())
-        # relative, as a weight is known to 2^-42 of itself; the largest is 1 exactly
+        # relative, as a weight is known to 2^-38 of itself; the largest is 1 exactly
         near += [abs(v - mp) / mp for v in w[max(0, n_m - 1): n_m + 1] if v < 1]
         n = min(n, n_m)
     t = (float(min(max(u, 0.0), 1 - 2.0 ** -24)) if u == u else 0.0) * c[n - 1]
@@ -57,8 +57,8 @@ def _call(qk, cuda, x, u, T, k=0, p=1.0, mp=0.0, offset=0):
     tok = torch.full((M,), -7, dtype=torch.int32, device=cuda)
     kept = torch.full((M,), -7, dtype=torch.int32, device=cuda)
     lp = torch.full((M,), 7.0, device=cuda)
-    qk.qk_sample(torch.from_numpy(np.ascontiguousarray(x)).to(cuda), torch.from_numpy(u.astype(np.float32)).to(cuda), tok, lp,
-                 kept, M, V, temperature=T, top_k=k, top_p=p, min_p=mp)
+    qk.qk_sample(torch.from_numpy(np.ascontiguousarray(x)).to(cuda), torch.from_numpy(u.astype(np.float32)).to(cuda),
+                 tok, lp, kept, M, V, temperature=T, top_k=k, top_p=p, min_p=mp)
     return tok.cpu().numpy(), lp.cpu().numpy(), kept.cpu().numpy()
 
 
@@ -93,7 +93,8 @@ def _rows(seed, M, V, spread=2.5, banned=0.0):
 
 SETTINGS = [(1.0, 0, 1.0, 0.0), (0.8, 40, 0.95, 0.05), (1.0, 0, 0.9, 0.0), (1.3, 0, 0.999, 0.0), (0.6, 0, 1.0, 0.02),
             (1.5, 300, 1.0, 0.0), (2.0, 3000, 0.97, 0.001), (1.0, 1, 1.0, 0.0), (3.0, 0, 0.5, 0.3), (0.3, 7, 0.3, 0.9),
-            (0.0, 5, 0.5, 0.5), (1.1, 90, 1.0, 0.003), (1.5, 512, 0.9, 0.0), (1.5, 513, 1.0, 0.01), (5.0, 0, 0.99, 0.0), (1.0, 0, 0.0, 0.0), (1.0, 0, 1.0, 1.0), (100.0, 0, 0.7, 0.0)]
+            (0.0, 5, 0.5, 0.5), (1.1, 90, 1.0, 0.003), (1.5, 512, 0.9, 0.0), (1.5, 513, 1.0, 0.01), (5.0, 0, 0.99, 0.0),
+            (1.0, 0, 0.0, 0.0), (1.0, 0, 1.0, 1.0), (100.0, 0, 0.7, 0.0)]
 
 
 @pytest.mark.parametrize("T,k,p,mp", SETTINGS)
@@ -176,6 +177,19 @@ def test_random_numbers_out_of_range(qk_lib, cuda):
         tok = _call(qk_lib, cuda, np.tile(x, (len(u), 1)), u, *s)[0]
         assert (tok[:4] == tok[0]).all() and (tok[4:] == tok[7]).all() and tok[0] != tok[7]
         assert tok[0] == x[0].argmax()
+
+
+@pytest.mark.parametrize("T,k,p,mp", [(1.3, 0, 1.0, 0.0), (0.5, 0, 1.0, 0.0), (20.0, 0, 1.0, 0.0), (1.0, 0, 0.9999, 0.0),
+                                      (0.1, 3000, 1.0, 0.0), (0.1, 3000, 0.95, 0.0), (0.3, 2411, 1.0, 0.04),
+                                      (0.05, 15000, 0.999, 0.0), (2.0, 9000, 1.0, 0.0), (0.4, 20001, 0.9, 0.0)])
+def test_the_ends_of_rows(qk_lib, cuda, T, k, p, mp):
+    """Random numbers near 1, where thousands of tokens share a little of the sum, and a
+    top_k among tokens whose weights are 0 in every sum.  Weights there can be as small as the
+    distance that counts as near: by the definition alone 12 of the rows are at T 0.5, one at
+    1.3 and none elsewhere."""
+    x, _ = _rows(512, 40, 20000)
+    u = (1 - 10.0 ** (-0.5 - 6.5 * (np.arange(40) / 40))).astype(np.float32)
+    _check(qk_lib, cuda, x, u, T, k, p, mp, exempt={0.5: 12, 1.3: 1}.get(T, 0))
 
 
 def test_rows_without_an_answer(qk_lib, cuda):
