@@ -36,8 +36,8 @@
 //     10.9, 32768 21.5 / 15.9, 131072 69 / 35; 32 over 4: 4096 5.6 / 8.7.
 //
 // One token, 24 heads over 8, 65536 positions (84 MB: 12.4 us at a copy's rate): 22.4 us.
-// Bound by instructions at long lengths (410 for a warp's 16 positions, issued in
-// 57 % of the cycles, the ends included; the DRAM is 45 % busy) and by the latency of
+// Bound by instructions at long lengths (375 for a warp's 16 positions, issued in
+// 57 % of the cycles, the ends included; the DRAM is 48 % busy) and by the latency of
 // a launch, or two, at short ones.
 //
 // More tokens: the visible rows are written as fp16(d q + m) to the caller's scratch
