@@ -625,13 +625,15 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     return;
   }
   if (T == 0.f) {  // the first of the largest
-    const uint32_t best0 = mapa_shared(smem_u32(&S.best), 0);
+    uint32_t best = 0xFFFFFFFFu;
     each_chunk(row, V, pad, c0, c1, S.second.ring, [&](const float(&y)[4], int k) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (y[e] == mx)
-          asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(best0), "r"(4 * k - pad + e) : "memory");
+      for (int e = 3; e >= 0; --e)
+        if (y[e] == mx) best = min(best, (uint32_t)(4 * k - pad + e));
     });
+    best = __reduce_min_sync(0xffffffffu, best);
+    if (lane == 0)
+      asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&S.best), 0)), "r"(best) : "memory");
     cluster_meet(C);
     if (rank == 0 && tid == 0) {
       A.a.token[m] = (int32_t)S.best;

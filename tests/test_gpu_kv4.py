@@ -429,6 +429,46 @@ def test_overlapping_buffers_are_refused(qk_lib, cuda):
     assert e.value.status == -7
 
 
+def test_offsets_beyond_32_bits(qk_lib, cuda):
+    """A cache whose tensors pass 4 GB: rows at its end are read and written as in a short
+    one, to the bit."""
+    import torch
+    Hkv, H, far, n = 2, 6, 40_000_000, 150
+    rng = synth.rng_for(421, 0)
+    small = [_dev(a, cuda) for a in ref4.random_cache(rng, Hkv, n) + ref4.random_cache(rng, Hkv, n)]
+    big = [torch.empty(Hkv, far + n, *t.shape[2:], dtype=t.dtype, device=cuda) for t in small]
+    assert big[0].numel() > 1 << 32
+    for b, t in zip(big, small):
+        b[:, far:] = t
+    for M, pos0 in ((1, n - 1), (5, n - 5), (40, n - 40)):
+        q = _dev((1.5 * rng.standard_normal((M, H, D))).astype(np.float16), cuda)
+        outs = []
+        for cache, at, L in ((small, pos0, n), (big, far + pos0, far + n)):
+            need = qk_lib.qk_gqa_attention_q4_scratch_bytes(M, H, Hkv, D, at, 64, 0)
+            out = torch.empty_like(q)
+            qk_lib.qk_gqa_attention_q4(q, *cache, out, M, H, Hkv, D, at, L, SCALE, 64, 0,
+                                       scratch=torch.empty(need, dtype=torch.uint8, device=cuda) if need else None)
+            outs.append(out)
+        assert torch.equal(*outs), M
+    rows = [torch.empty(Hkv, n, D, dtype=torch.float16, device=cuda) for _ in range(2)]
+    qk_lib.qk_dequant_kv_q4(*small[:2], rows[0], Hkv, D, 0, n, n)
+    qk_lib.qk_dequant_kv_q4(*big[:2], rows[1], Hkv, D, far, n, far + n)
+    assert torch.equal(*rows)
+    x = [_dev(rng.standard_normal((3, h, D)).astype(np.float32), cuda) for h in (H, Hkv, Hkv)]
+    q16 = torch.empty(3, H, D, dtype=torch.float16, device=cuda)
+    for cache, at, L in ((small, 70, n), (big, far + 70, far + n)):
+        qk_lib.qk_norm_rope_kv_append_q4(*x, None, None, EPS, None, q16, *cache, 3, H, Hkv, D, 0, at, L)
+    for b, t in zip(big, small):
+        assert torch.equal(b[:, far:].contiguous().view(torch.uint8), t.view(torch.uint8))
+    del big
+    wide = [torch.empty(Hkv, far, D, dtype=torch.float16, device=cuda) for _ in range(2)]
+    want = [torch.empty(Hkv, n, D, dtype=torch.float16, device=cuda) for _ in range(2)]
+    qk_lib.qk_norm_rope_kv_append(*x, None, None, EPS, None, q16, *wide, 3, H, Hkv, D, 0, far - 3, far)
+    qk_lib.qk_norm_rope_kv_append(*x, None, None, EPS, None, q16, *want, 3, H, Hkv, D, 0, n - 3, n)
+    for w, t in zip(wide, want):
+        assert torch.equal(w[:, far - 3:], t[:, n - 3:])
+
+
 def test_step_on_a_side_stream_and_in_a_graph(qk_lib, cuda):
     """Append, attention and append again as a decode loop makes them, on a stream of its
     own and replayed from a graph: the same bits as call by call."""

@@ -234,6 +234,27 @@ def test_outputs_that_are_not_wanted(qk_lib, cuda):
     assert (guard[3:] == -9).all()
 
 
+def test_more_than_2_31_logits(qk_lib, cuda):
+    """Rows behind 2^31 logits are as in a call of their own."""
+    import torch
+    M, V = 17000, 128256
+    g = torch.Generator(device=cuda).manual_seed(513)
+    x = torch.empty(M, V, device=cuda)
+    for i in range(0, M, 1000):
+        x[i: i + 1000].normal_(generator=g)
+    u = torch.rand(M, generator=g, device=cuda)
+    tok, kept = (torch.full((M,), -7, dtype=torch.int32, device=cuda) for _ in range(2))
+    lp = torch.empty(M, device=cuda)
+    qk_lib.qk_sample(x, u, tok, lp, kept, M, V, 0.8, 40, 0.95, 0.05)
+    rows = torch.tensor([0, 16743, 16744, 16745, M - 1], device=cuda)
+    t2, k2, lp2 = torch.empty(5, dtype=torch.int32, device=cuda), torch.empty(5, dtype=torch.int32, device=cuda), torch.empty(
+        5, device=cuda)
+    qk_lib.qk_sample(x[rows], u[rows], t2, lp2, k2, 5, V, 0.8, 40, 0.95, 0.05)
+    assert torch.equal(tok[rows], t2) and torch.equal(kept[rows], k2) and (tok >= 0).all()
+    qk_lib.qk_sample(x, u, tok, None, None, M, V, 0.0)
+    assert torch.equal(tok[rows].long(), x[rows].argmax(1))
+
+
 def test_sample_in_a_graph_with_new_numbers(qk_lib, cuda):
     """A captured call follows the logits and the random numbers that its buffers hold."""
     import torch
