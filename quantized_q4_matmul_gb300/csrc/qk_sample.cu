@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
           float at;
           const int b = bin_of(y[e], at);
           atomicAdd(&S.first.cnt[b], 1u);
-          if (y[e] >= means)  // (at + 1/2) 4096
-            atomicAdd(&S.first.frac[b], __float_as_uint(__fmaf_rn(at, 4096.f, kMagic + 2048.f)) - 0x4B400000u);
+          if (y[e] >= means)  // (at + 1/2) 4096 + 1, 1 at least
+            atomicAdd(&S.first.frac[b], __float_as_uint(__fmaf_rn(at, 4096.f, kMagic + 2049.f)) - 0x4B400000u);
         }
     });
     if (C > 1) {
@@ -754,8 +754,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       uint32_t cn = 0;
 #pragma unroll
       for (int i = 0; i < kBinsPer; ++i) {
-        // the middle where no positions were added (with any, the sum is not 0: bin 0's are 1/2 and more)
-        const float kf = (float)k[i], mean = q[i] ? __fdividef((float)q[i], 4096.f * kf) - 0.5f : 0.f;
+        // the middle where no positions were added
+        const float kf = (float)k[i], mean = q[i] ? __fdividef((float)q[i], 4096.f * kf) - 2049.f / 4096.f : 0.f;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f[i]) : "f"(-per_bin * ((float)(tid * kBinsPer + i) + mean)));
         f[i] *= kf;
         sum += f[i];

@@ -152,6 +152,16 @@ def test_ties(qk_lib, cuda, step, T, k, p, mp):
     _check(qk_lib, cuda, x, u, T, k, p, mp, exempt=1)
 
 
+@pytest.mark.parametrize("T,k,p,mp", SETTINGS[:7])
+def test_logits_of_fewer_bits(qk_lib, cuda, T, k, p, mp):
+    """Logits that were fp16 or bf16: many equal ones, and many in the middle between two bins."""
+    x, u = _rows(514, 8, 30000)
+    x[4:] = x[4:].astype(np.float16)
+    bits = x[:4].view(np.uint32)
+    x[:4] = ((bits + 0x7FFF + ((bits >> 16) & 1)) & 0xFFFF0000).view(np.float32)
+    _check(qk_lib, cuda, x, u, T, k, p, mp)
+
+
 def test_zeros_of_both_signs_are_equal(qk_lib, cuda):
     x = np.zeros((1, 64), np.float32)
     x[0, ::2] = -0.0
