@@ -525,7 +525,7 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * 0 .. 1, min_p 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need
  * not be 16-byte aligned (any V), the buffers do.  No output may overlap another or
  * an input.  Thousands of equal logits around the last kept token, or around the
- * chosen one, make a row slow (0.1 to 2 ms).  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
+ * chosen one, make a row slow (0.1 to 4 ms).  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
  */
 qk_status qk_sample(const float *logits, const float *u, int32_t *token, float *logprob, int32_t *kept, int64_t M,
                     int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream);

@@ -355,6 +355,7 @@ struct Sums {
 struct Row {
   const float* x;
   int V, pad;
+  float mn;  // least finite logit
   Weigh weigh;
 };
 
@@ -384,7 +385,7 @@ __device__ __noinline__ unsigned long long first_with(SaShared& S, const Row& R,
                                                       Sums& at) {
   unsigned long long key = 0;
   for (int part = 0; part < 2; ++part) {
-    uint32_t lo = 0u, hi = part ? (uint32_t)R.V - 1u : 0xFFFFFFFFu;
+    uint32_t lo = part ? 0u : key_of(R.weigh.mx), hi = part ? (uint32_t)R.V - 1u : key_of(R.mn);
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo) / 2;
       const Sums s = sums_upto(S, R, part ? key | mid : ((unsigned long long)mid << 32) | 0xFFFFFFFFull);
@@ -1060,7 +1061,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       done = S.found[3] != 0;
     }
   }
-  if (!done) sample_slowly(A, S, Row{row, V, pad, W}, finite, u, m);
+  if (!done) sample_slowly(A, S, Row{row, V, pad, mn, W}, finite, u, m);
 }
 
 }  // namespace
