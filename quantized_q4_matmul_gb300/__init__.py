@@ -204,6 +204,21 @@ def _buf(t, nbytes: int, what, dtypes=None) -> int:
     return t.data_ptr()
 
 
+def _bufs(where: str, *args) -> list:
+    """The addresses of buffer arguments (tensor, bytes, dtypes, name), each checked
+    as by _buf: one loop for all takes 0.1 us less for each of them."""
+    out = []
+    for t, nbytes, dtypes, name in args:
+        try:
+            if _dtype_names[t.dtype] in dtypes and t.nbytes >= nbytes and t.is_contiguous():
+                out.append(t.data_ptr())
+                continue
+        except (AttributeError, KeyError):  # None, an address, or a dtype seen for the first time
+            pass
+        out.append(_buf(t, nbytes, ("%s: %s", where, name), dtypes))
+    return out
+
+
 def _what(what) -> str:
     return what if isinstance(what, str) else what[0] % what[1:]
 
@@ -446,22 +461,21 @@ def qk_norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_fr
                            layout: int = QK_ROPE_INTERLEAVED, magnitude: float = 1.0, stream=None) -> None:
     """qk_rope_kv_append with an RMSNorm of each query and key head in front (see
     include/qk.h): gammas fp16 [D], or None for heads that are not normalized."""
-    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    M, H, H_kv, D, n_rot, L_max = int(M), int(H), int(H_kv), int(D), int(n_rot), int(L_max)
     cn = 2 * _size(H_kv, L_max, D)
-    w = "qk_norm_rope_kv_append: %s"
-    a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
-    _check(lib().qk_norm_rope_kv_append(*a, _buf(k_cache, cn, (w, "k_cache"), _F16),
-                                        _buf(v_cache, cn, (w, "v_cache"), _F16), M, H, H_kv, D, int(n_rot),
-                                        int(pos0), L_max, int(layout), float(magnitude), _stream(stream)),
+    a = _bufs("qk_norm_rope_kv_append",
+              *_append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot),
+              (k_cache, cn, _F16, "k_cache"), (v_cache, cn, _F16, "v_cache"))
+    _check(lib().qk_norm_rope_kv_append(a[0], a[1], a[2], a[3], a[4], float(eps), a[5], a[6], a[7], a[8], M, H, H_kv, D,
+                                        n_rot, int(pos0), L_max, int(layout), float(magnitude), _stream(stream)),
            "qk_norm_rope_kv_append")
 
 
-def _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot):
-    qn, kn = _size(M, H, D), _size(M, H_kv, D)
-    return (_buf(q, 4 * qn, (w, "q"), _F32), _buf(k, 4 * kn, (w, "k"), _F32), _buf(v, 4 * kn, (w, "v"), _F32),
-            _buf(q_gamma_f16, 2 * _n(D), (w, "q_gamma_f16"), _F16),
-            _buf(k_gamma_f16, 2 * _n(D), (w, "k_gamma_f16"), _F16), float(eps),
-            _buf(inv_freq, 4 * _n(n_rot), (w, "inv_freq"), _F64), _buf(q_f16, 2 * qn, (w, "q_f16"), _F16))
+def _append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot):
+    qn, kn, gn = _size(M, H, D), 4 * _size(M, H_kv, D), 2 * D
+    return ((q, 4 * qn, _F32, "q"), (k, kn, _F32, "k"), (v, kn, _F32, "v"), (q_gamma_f16, gn, _F16, "q_gamma_f16"),
+            (k_gamma_f16, gn, _F16, "k_gamma_f16"), (inv_freq, 4 * n_rot, _F64, "inv_freq"),
+            (q_f16, 2 * qn, _F16, "q_f16"))
 
 
 def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_freq, q_f16, k_q4, k_dm, v_q4, v_dm,
@@ -469,15 +483,14 @@ def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv
                               layout: int = QK_ROPE_INTERLEAVED, magnitude: float = 1.0, stream=None) -> None:
     """qk_norm_rope_kv_append into a cache held in 4 bits (see include/qk.h): k_q4, v_q4
     uint8 [H_kv][L_max][D / 2], k_dm, v_dm fp16 [H_kv][L_max][D / 32][2]."""
-    M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    M, H, H_kv, D, n_rot, L_max = int(M), int(H), int(H_kv), int(D), int(n_rot), int(L_max)
     cn = _size(H_kv, L_max, D)
-    w = "qk_norm_rope_kv_append_q4: %s"
-    a = _append_inputs(w, q, k, v, q_gamma_f16, k_gamma_f16, eps, inv_freq, q_f16, M, H, H_kv, D, n_rot)
-    _check(lib().qk_norm_rope_kv_append_q4(*a, _buf(k_q4, cn // 2, (w, "k_q4"), _U8),
-                                           _buf(k_dm, cn // 8, (w, "k_dm"), _F16),
-                                           _buf(v_q4, cn // 2, (w, "v_q4"), _U8),
-                                           _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
-                                           M, H, H_kv, D, int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
+    a = _bufs("qk_norm_rope_kv_append_q4",
+              *_append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot),
+              (k_q4, cn // 2, _U8, "k_q4"), (k_dm, cn // 8, _F16, "k_dm"), (v_q4, cn // 2, _U8, "v_q4"),
+              (v_dm, cn // 8, _F16, "v_dm"))
+    _check(lib().qk_norm_rope_kv_append_q4(a[0], a[1], a[2], a[3], a[4], float(eps), a[5], a[6], a[7], a[8], a[9], a[10],
+                                           M, H, H_kv, D, n_rot, int(pos0), L_max, int(layout), float(magnitude),
                                            _stream(stream)), "qk_norm_rope_kv_append_q4")
 
 
@@ -485,10 +498,9 @@ def qk_dequant_kv_q4(q4, dm, out_f16, H_kv: int, D: int, pos0: int, M: int, L_ma
     """Rows pos0 .. pos0 + M - 1 of one tensor of a 4-bit cache as fp16 [H_kv][M][D] (see include/qk.h)."""
     H_kv, D, M, L_max = int(H_kv), int(D), int(M), int(L_max)
     cn = _size(H_kv, L_max, D)
-    _check(lib().qk_dequant_kv_q4(_buf(q4, cn // 2, "qk_dequant_kv_q4: q4", _U8),
-                                  _buf(dm, cn // 8, "qk_dequant_kv_q4: dm", _F16),
-                                  _buf(out_f16, 2 * _size(H_kv, M, D), "qk_dequant_kv_q4: out_f16", _F16), H_kv, D,
-                                  int(pos0), M, L_max, _stream(stream)), "qk_dequant_kv_q4")
+    a = _bufs("qk_dequant_kv_q4", (q4, cn // 2, _U8, "q4"), (dm, cn // 8, _F16, "dm"),
+              (out_f16, 2 * _size(H_kv, M, D), _F16, "out_f16"))
+    _check(lib().qk_dequant_kv_q4(a[0], a[1], a[2], H_kv, D, int(pos0), M, L_max, _stream(stream)), "qk_dequant_kv_q4")
 
 
 def qk_rmsnorm_scratch_bytes(qtype, M: int, K: int, gateup: bool = False) -> int:
@@ -640,13 +652,11 @@ def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, 
     pos0, window, sinks = int(pos0), int(window), int(sinks)
     qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
     need = max(0, lib().qk_gqa_attention_q4_scratch_bytes(M, H, H_kv, D, pos0, window, sinks))
-    w = "qk_gqa_attention_q4: %s"
-    _check(lib().qk_gqa_attention_q4(_buf(q_f16, 2 * qn, (w, "q_f16"), _F16), _buf(k_q4, cn // 2, (w, "k_q4"), _U8),
-                                     _buf(k_dm, cn // 8, (w, "k_dm"), _F16), _buf(v_q4, cn // 2, (w, "v_q4"), _U8),
-                                     _buf(v_dm, cn // 8, (w, "v_dm"), _F16),
-                                     _buf(out_f16, 2 * qn, (w, "out_f16"), _F16), M, H, H_kv, D, pos0, L_max, float(scale), window, sinks,
-                                     _buf(scratch, need, (w, "scratch"), _F16 + _U8) if need else 0, _stream(stream)),
-           "qk_gqa_attention_q4")
+    a = _bufs("qk_gqa_attention_q4", (q_f16, 2 * qn, _F16, "q_f16"), (k_q4, cn // 2, _U8, "k_q4"),
+              (k_dm, cn // 8, _F16, "k_dm"), (v_q4, cn // 2, _U8, "v_q4"), (v_dm, cn // 8, _F16, "v_dm"),
+              (out_f16, 2 * qn, _F16, "out_f16"), (scratch if need else None, need, _F16 + _U8, "scratch"))
+    _check(lib().qk_gqa_attention_q4(a[0], a[1], a[2], a[3], a[4], a[5], M, H, H_kv, D, pos0, L_max, float(scale),
+                                     window, sinks, a[6], _stream(stream)), "qk_gqa_attention_q4")
 
 
 def qk_logprobs(logits, tokens, logprob, entropy, top_n: int, top_ids, top_logprobs, M: int, V: int,
@@ -669,11 +679,12 @@ def qk_sample(logits, u, token, logprob, kept, M: int, V: int, temperature: floa
               top_p: float = 1.0, min_p: float = 0.0, stream=None) -> None:
     """A token from each row of logits fp32 [M][V] and a given random number u fp32 [M]
     (see include/qk.h): token int32 [M], logprob fp32 [M] and kept int32 [M] or None."""
+    M, V = int(M), int(V)
     m = 4 * _n(M)
-    _check(lib().qk_sample(_buf(logits, m * _n(V), "qk_sample: logits", _F32), _buf(u, m, "qk_sample: u", _F32),
-                           _buf(token, m, "qk_sample: token", _I32), _buf(logprob, m, "qk_sample: logprob", _F32),
-                           _buf(kept, m, "qk_sample: kept", _I32), int(M), int(V), float(temperature), int(top_k),
-                           float(top_p), float(min_p), _stream(stream)), "qk_sample")
+    a = _bufs("qk_sample", (logits, m * _n(V), _F32, "logits"), (u, m, _F32, "u"), (token, m, _I32, "token"),
+              (logprob, m, _F32, "logprob"), (kept, m, _I32, "kept"))
+    _check(lib().qk_sample(a[0], a[1], a[2], a[3], a[4], M, V, float(temperature), int(top_k), float(top_p),
+                           float(min_p), _stream(stream)), "qk_sample")
 
 
 def qk_get_device_status(stream=None) -> None:

@@ -48,7 +48,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // The pointer must be readable by the current device: device or managed
 // memory of this device, or host memory registered with / allocated by CUDA.
-qk_status check_pointer(const void* p) {
+// `dev`: the current device, asked for where it is not given.
+qk_status check_pointer(const void* p, int dev = -1) {
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     cudaGetLastError();
@@ -56,8 +57,7 @@ qk_status check_pointer(const void* p) {
   }
   if (a.type == cudaMemoryTypeUnregistered) return QK_ERR_POINTER;
   if (a.type == cudaMemoryTypeDevice) {
-    int dev = 0;
-    cudaGetDevice(&dev);
+    if (dev < 0) cudaGetDevice(&dev);
     if (a.device != dev) return QK_ERR_POINTER;
   }
   if (a.type == cudaMemoryTypeHost && a.devicePointer == nullptr) return QK_ERR_POINTER;
@@ -113,8 +113,9 @@ qk_status check_spans_host(const Span* s, int n) {
 qk_status check_spans_device(const Span* s, int n) {
   qk_status st = check_device();
   if (st != QK_OK) return st;
+  const int dev = qk::current_device();
   for (int i = 0; i < n; ++i)
-    if ((st = check_pointer(s[i].p)) != QK_OK) return st;
+    if ((st = check_pointer(s[i].p, dev)) != QK_OK) return st;
   for (int i = 0; i < n; ++i)
     for (int j = 0; j < n; ++j)
       if (i != j && s[i].output && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return QK_ERR_ALIAS;
