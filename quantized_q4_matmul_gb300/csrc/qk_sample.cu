@@ -34,10 +34,10 @@
 // does not, or the candidates are too many (equal logits), it searches the order
 // bit by bit instead, with an exact sum over the row at each step.
 //
-// Bound by latency for one row (9.3 us for 128256 logits with top_k 40: two passes of
+// Bound by latency for one row (9.2 us for 128256 logits with top_k 40: two passes of
 // 1 us, two cluster barriers, then a dozen short steps of one CTA whose code is
 // fetched once), and by instructions where all weights count: 512 rows of 128256
-// without bounds 323 us, issue slots 77 % busy, 128 instructions a logit and warp, most
+// without bounds 320 us, issue slots 77 % busy, 126 instructions a logit and warp, most
 // of them the weights' pairs (packed two at a time; one at a time 387 us where packed took
 // 363); HBM 25 %.
 #include <cuda_runtime.h>
