@@ -517,9 +517,10 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * temperature 0 gives the first token in the order, a logprob of 0 and kept 1.  A
  * row that holds NaN or +inf, or nothing but -inf, gives token -1, a NaN logprob
  * and kept 0.  u below 0 or NaN counts as 0, u of 1 or more as the largest fp32
- * number below 1.  A weight enters the sums within 2^-38 of itself and 2^-45 of the
- * largest, so that a token follows from the definition, but where a border lies
- * closer than 2^-30 of the sum to a decision, rather than from the order of a sum.
+ * number below 1.  A weight is within 2^-36 of itself, and an addition rounds 2^-40
+ * of the largest off at most, so that a token follows from the definition, but where
+ * a border lies closer than about 2^-33 of the sum to a decision, rather than from
+ * the order of a sum.
  * How many CTAs share a row follows M and the device, and with it the sums' last
  * bits; the same call repeats its bits.  temperature is 0 or 1e-6 .. 1e6, top_p
  * 0 .. 1, min_p 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need

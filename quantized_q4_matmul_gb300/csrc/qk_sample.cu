@@ -12,9 +12,8 @@
 //
 // Every decision compares sums of up to 2^19 weights with a border, and a row of
 // 10^5 tokens has 10^5 borders: sums in fp32 would choose another token in some
-// percent of the rows.  Weights are therefore computed in pairs of fp32 to 2^-38 of
-// themselves (a difference without error, a table of 2^(-i / 256) and a polynomial of
-// degree 4) and summed in pairs within a thread and in 64-bit integers, multiples
+// percent of the rows.  Weights are therefore computed in pairs of fp32 to 2^-36 of
+// themselves (a difference without error, a table of 2^(-i / 2048) and two powers) and summed in pairs within a thread and in 64-bit integers, multiples
 // of 2^-44 of the largest weight, between threads: no order changes a result.
 //
 // A cluster of C CTAs has a row and goes over it two or three times (it stays in L2;
@@ -37,9 +36,9 @@
 // Bound by latency for one row (9.2 us for 128256 logits with top_k 40: two passes of
 // 1 us, two cluster barriers, then a dozen short steps of one CTA whose code is
 // fetched once), and by instructions where all weights count: 512 rows of 128256
-// without bounds 320 us, issue slots 77 % busy, 126 instructions a logit and warp, most
-// of them the weights' pairs (packed two at a time; one at a time 387 us where packed took
-// 363); HBM 25 %.
+// without bounds 288 us (weights for nothing would leave 235: 21 packed instructions for
+// two, as the table of 2048 spares a polynomial in pairs; with one of 256 it was 321); HBM
+// 28 %.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -75,15 +74,20 @@ constexpr float kSpan = 31.f, kSpanK = 83.f;
 // leaves sqrt(w) of one, 1.5e-5 of the sum at 10 T, and at 14 T of the wider bins.
 constexpr float kMeans = 10.f, kMeansK = 14.f;
 
+constexpr int kTable = 2048;     // 2^(-i / kTable)
+constexpr int kFine = 64;        // it is the product of 2^(-i / 32) and 2^(-j / kTable), j < kFine
+struct SaFactors {
+  float2 coarse[kTable / kFine], fine[kFine];  // as pairs
+};
 struct SaTable {
-  float h[256], l[256];  // 2^(-i / 256) as a pair
+  float h[kTable], l[kTable];  // as a pair
 };
 
 struct SaArgs {
   SampleArgs a;
-  float ch, cl;  // 256 log2(e) / T as a pair
+  float ch, cl;  // kTable log2(e) / T as a pair
   int C;
-  SaTable table;
+  SaFactors factors;
 };
 
 struct SaStat {
@@ -145,18 +149,21 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 __device__ __forceinline__ float value_of(unsigned long long order) { return value_of((uint32_t)(order >> 32)); }
 
-// A sum as a pair of fp32.
-struct Pair {
-  float h = 0.f, l = 0.f;
+// A pair of fp32 in multiples of 1 / kOne.
+__device__ __forceinline__ unsigned long long fixed(float h, float l) {
+  return (unsigned long long)(__float2ll_rn(h * kOne) + __float2ll_rn(l * kOne));
+}
+
+// A sum of weights as a pair of fp32, and 1: as no weight is larger than that, what an
+// addition rounds off is the weight less what was added.
+struct Sum {
+  float h = 1.f, l = 0.f;
   __device__ __forceinline__ void add(float2 w) {
-    const float s = __fadd_rn(h, w.x), b = __fsub_rn(s, h);
-    const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(w.x, b));
+    const float s = __fadd_rn(h, w.x), e = __fsub_rn(w.x, __fsub_rn(s, h));
     h = s;
     l = __fadd_rn(l, __fadd_rn(e, w.y));
   }
-  __device__ __forceinline__ unsigned long long fixed() const {
-    return (unsigned long long)(__float2ll_rn(h * kOne) + __float2ll_rn(l * kOne));
-  }
+  __device__ __forceinline__ unsigned long long value() const { return fixed(h, l) - (1ull << 44); }
 };
 
 // Two numbers in one register pair, for the instructions that take both.
@@ -185,50 +192,46 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
   return d;
 }
 
+constexpr double kPerOctave = kTable * 1.44269504088896340736;  // kTable log2(e)
+constexpr float kPerOctaveH = (float)kPerOctave, kPerOctaveL = (float)(kPerOctave - (double)kPerOctaveH);
+constexpr float kFar = 87.f;  // exp(-87) is 2^-125.5, of the octaves that the exponent holds
+
 // What the weights of a row need.
 struct Weigh {
-  float mx, most;  // differences above `most`, 83 T or 2^-120 of the largest weight, count as it
-  float ch, cl;    // 256 log2(e) / T as a pair
+  float mx, least;  // logits below `least`, whose weight is 0 in every sum, count as it
+  float ch, cl;     // kTable log2(e) / T as a pair
   const SaTable* table;
 };
 
-// exp((x - mx) / T) of two finite logits as pairs, within 2^-38.
+// exp((x - mx) / T) of two finite logits, as pairs, within 2^-36.
+// The table is so fine that only u's first power matters beyond fp32.
 __device__ __forceinline__ void weights(const Weigh& W, float x0, float x1, float2& w0, float2& w1) {
-  constexpr double kLn = 0.69314718055994530942 / 256;
-  constexpr float L = (float)kLn, Ll = (float)(kLn - (double)L);
-  const Two minus(-1.f), mx(W.mx), ch(W.ch), x(x0, x1);
+  constexpr float kLn = (float)(0.69314718055994530942 / kTable);
+  const Two minus(-1.f), mx(W.mx), ch(W.ch), x(fmaxf(x0, W.least), fmaxf(x1, W.least));
   // d + dl = mx - x without error
-  Two d = fma2(x, minus, mx);
+  const Two d = fma2(x, minus, mx);
   const Two b = fma2(mx, minus, d);
   const Two dl = fma2(add2(x, b), minus, fma2(fma2(b, minus, d), minus, mx));
-  float d0, d1, l0, l1;
-  d.get(d0, d1);
-  d = Two(fminf(d0, W.most), fminf(d1, W.most));
-  // th + tl = 256 log2(e) (mx - x) / T, th = m + f with an integer m; tl is 2^-9 at
-  // most, but for differences above `most` (whose dl may be NaN)
+  // th + tl = kTable log2(e) (mx - x) / T, th = m + f with an integer m; tl is 2^-6 at most
   const Two th = mul2(d, ch);
-  Two tl = fma2(dl, ch, fma2(d, Two(W.cl), fma2(d, ch, mul2(d, Two(-W.ch)))));
-  tl.get(l0, l1);
-  tl = Two(fminf(fmaxf(l0, -1.f), 1.f), fminf(fmaxf(l1, -1.f), 1.f));
+  const Two tl = fma2(dl, ch, fma2(d, Two(W.cl), fma2(d, ch, mul2(d, Two(-W.ch)))));
   const Two mag = add2(th, Two(kMagic));
-  const Two f = fma2(add2(mag, Two(-kMagic)), minus, th);
-  // u = (f + tl) ln 2 / 256, at most 2^-9.5; exp(-u) = 1 - uh + s
-  const Two uh = mul2(f, Two(L)), nuh = mul2(f, Two(-L));
-  const Two ul = fma2(tl, Two(L), fma2(f, Two(Ll), fma2(f, Two(L), nuh)));
-  const Two q = mul2(mul2(uh, uh), fma2(nuh, fma2(nuh, Two(1.f / 24.f), Two(1.f / 6.f)), Two(0.5f)));
-  const Two s = fma2(ul, minus, fma2(ul, fma2(q, minus, uh), q));
-  // 2^(-i / 256) (1 - uh + s), i = m modulo 256, times 2^-(m / 256)
+  const Two f = add2(fma2(add2(mag, Two(-kMagic)), minus, th), tl);
+  // u = (f + tl) ln 2 / kTable, at most 2^-12.4; exp(-u) - 1 = u (u / 2 - 1), u^3 / 6 is 2^-40
+  const Two u = mul2(f, Two(kLn));
+  const Two r = mul2(u, fma2(u, Two(0.5f), minus));
+  // 2^(-i / kTable) (1 + r), i = m modulo kTable, times 2^-(m / kTable)
   float m0, m1;
   mag.get(m0, m1);
   const uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);  // m in the low bits
-  const Two t(W.table->h[b0 & 255u], W.table->h[b1 & 255u]), r(W.table->l[b0 & 255u], W.table->l[b1 & 255u]);
-  const Two np = mul2(t, nuh), pl = fma2(r, uh, fma2(t, uh, np));
-  const Two h = add2(t, np), e = add2(fma2(h, minus, t), np);
-  const Two l = add2(e, fma2(pl, minus, fma2(t, s, r)));
-  const Two scale(__uint_as_float((127u << 23) - ((b0 & 0x7F00u) << 15)),
-                  __uint_as_float((127u << 23) - ((b1 & 0x7F00u) << 15)));
-  mul2(h, scale).get(w0.x, w1.x);
-  mul2(l, scale).get(w0.y, w1.y);
+  const uint32_t i0 = b0 & (kTable - 1u), i1 = b1 & (kTable - 1u);
+  const Two h(W.table->h[i0], W.table->h[i1]), l(W.table->l[i0], W.table->l[i1]);
+  constexpr uint32_t kOctaves = 127u * kTable;
+  const Two scale(__uint_as_float((127u << 23) - ((b0 & kOctaves) * ((1u << 23) / kTable))),
+                  __uint_as_float((127u << 23) - ((b1 & kOctaves) * ((1u << 23) / kTable))));
+  const Two low = fma2(h, r, l), sum = add2(h, low);
+  mul2(sum, scale).get(w0.x, w1.x);
+  mul2(fma2(fma2(h, minus, sum), minus, low), scale).get(w0.y, w1.y);
 }
 __device__ __forceinline__ float2 weight(const Weigh& W, float x) {
   float2 a, b;
@@ -361,7 +364,7 @@ struct Row {
 
 // The exact sum over the tokens up to `order`.
 __device__ __noinline__ Sums sums_upto(SaShared& S, const Row& R, unsigned long long order) {
-  Pair sum;
+  Sum sum;
   uint32_t n = 0;
   each_chunk(R.x, R.V, R.pad, 0, (R.V + R.pad + 3) / 4, S.first.ring, [&](const float(&y)[4], int k) {
     const int v = 4 * k - R.pad;
@@ -373,7 +376,7 @@ __device__ __noinline__ Sums sums_upto(SaShared& S, const Row& R, unsigned long 
       }
   });
   Sums r;
-  r.w = cta_sum(sum.fixed(), S.red64[0]);
+  r.w = cta_sum(sum.value(), S.red64[0]);
   r.n = cta_sum(n, S.red32);
   return r;
 }
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   const int pad = (int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3u);
   const int chunks = (V + pad + 3) / 4;
   const int c0 = (int)((int64_t)rank * chunks / C), c1 = (int)((int64_t)(rank + 1) * chunks / C);
-  const float T = A.a.temperature;
+  float T = A.a.temperature;
   const bool with_p = A.a.top_p < 1.f, with_m = A.a.min_p > 0.f;
   if (C > 1) {
     __syncwarp();
@@ -518,9 +521,13 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   }
   for (int i = tid; i < kBins / 2; i += kSaThreads)
     reinterpret_cast<uint4*>(S.first.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid < 256) {
-    S.table.h[tid] = A.table.h[tid];
-    S.table.l[tid] = A.table.l[tid];
+#pragma unroll
+  for (int i = tid; i < kTable; i += kSaThreads) {
+    const float2 a = A.factors.coarse[i / kFine], b = A.factors.fine[i % kFine];
+    const float p = a.x * b.x, e = fmaf(a.x, b.y, fmaf(a.y, b.x, fmaf(a.x, b.x, -p)));
+    const float h = __fadd_rn(p, e);
+    S.table.h[i] = h;
+    S.table.l[i] = __fsub_rn(e, __fsub_rn(h, p));
   }
   if (tid < 4) S.found[tid] = 0;
   if (tid == 0) S.ncand = S.listed = 0u, S.best = 0xFFFFFFFFu;
@@ -645,7 +652,21 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
   }
   float u = A.a.u[m];
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
-  const Weigh W{mx, 83.f * T, A.ch, A.cl, &S.table};
+  // Where the next number below mx is more than 87 T away, all weights but the largest
+  // are 0 in every sum; a larger T says the same.  Otherwise mx - least is between
+  // 43 T and 87 T, or 2^-62 and 2^-125.5.
+  float ch = A.ch, cl = A.cl;
+  {
+    const uint32_t bits = __float_as_uint(mx);
+    const float below = mx > 0.f ? __uint_as_float(bits - 1u) : mx < 0.f ? __uint_as_float(bits + 1u) : 0.f;
+    const float step = fminf(mx - below, 2.028241e31f);  // 2^104: the largest numbers'
+    if (kFar * T < step) {
+      T = step * (1.f / 64.f);
+      ch = kPerOctaveH / T;
+      cl = kPerOctaveL / T;
+    }
+  }
+  const Weigh W{mx, __fsub_ru(mx, kFar * T), ch, cl, &S.table};
 
   const bool with_k = A.a.top_k > 0 && (uint32_t)A.a.top_k < finite;
   const float span = fminf(mx - mn, (with_k ? kSpanK : kSpan) * T);
@@ -878,14 +899,14 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
     seg_cnt = warp_upto(seg_cnt);
     if (warp == 0 && lane < kSegs) S.base_cnt[lane] = seg_cnt;
 #pragma unroll 1
-    for (int s = 0; s < segs; ++s) S.second.acc[s][tid] = make_float2(0.f, 0.f);
+    for (int s = 0; s < segs; ++s) S.second.acc[s][tid] = make_float2(1.f, 0.f);
     __syncthreads();
 
     // ---- 3. exact sums, candidates
     if (n <= kCap) {
       auto add = [&](int cls, float2 w) {
         const float2 a = S.second.acc[cls][tid];
-        Pair p;
+        Sum p;
         p.h = a.x;
         p.l = a.y;
         p.add(w);
@@ -922,10 +943,10 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
       });
 #pragma unroll 1
       for (int s = 0; s < segs; ++s) {
-        Pair p;
+        Sum p;
         p.h = S.second.acc[s][tid].x;
         p.l = S.second.acc[s][tid].y;
-        const unsigned long long w = warp_sum(p.fixed());
+        const unsigned long long w = warp_sum(p.value());
         if (lane == 0) S.red64[s][warp] = w;
       }
       __syncthreads();
@@ -986,10 +1007,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
       const float2 f = weight(W, value_of(sorted[j]));
-      Pair p;
-      p.h = f.x;
-      p.l = f.y;
-      const unsigned long long w = p.fixed();
+      const unsigned long long w = fixed(f.x, f.y);
       S.first.w[j] = w;
       S.second.place[j] = with_m && at_least(f, A.a.min_p) ? 0x80000000u : 0u;
       own += w;
@@ -1052,7 +1070,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
         if ((S.second.place[j] & 0x7FFFFFFFu) <= n_keep && to > t && to - S.first.w[j] <= t) {
           const unsigned long long order = sorted[j];
           A.a.token[m] = (int32_t)(uint32_t)order;
-          if (A.a.logprob) A.a.logprob[m] = share_log(value_of(order), mx, T, s_keep);
+          if (A.a.logprob) A.a.logprob[m] = share_log(value_of(order), mx, A.a.temperature, s_keep);
           if (A.a.kept) A.a.kept[m] = (int32_t)n_keep;
           S.found[3] = 1;
         }
@@ -1067,21 +1085,23 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
-  static const SaTable table = [] {  // made once for the process
-    SaTable t;
-    for (int i = 0; i < 256; ++i) {
-      const double x = std::exp2(-i / 256.0);
-      t.h[i] = (float)x;
-      t.l[i] = (float)(x - (double)t.h[i]);
-    }
+  static const SaFactors factors = [] {  // made once for the process
+    SaFactors t;
+    auto power = [](float2& to, double x) {
+      x = std::exp2(x);
+      to.x = (float)x;
+      to.y = (float)(x - (double)to.x);
+    };
+    for (int i = 0; i < kTable / kFine; ++i) power(t.coarse[i], -i * (double)kFine / kTable);
+    for (int i = 0; i < kFine; ++i) power(t.fine[i], -i / (double)kTable);
     return t;
   }();
   SaArgs A;
   A.a = a;
-  const double c = a.temperature > 0.f ? 256.0 * 1.4426950408889634 / (double)a.temperature : 0.0;
+  const double c = a.temperature > 0.f ? kPerOctave / (double)a.temperature : 0.0;
   A.ch = (float)c;
   A.cl = (float)(c - (double)A.ch);
-  A.table = table;
+  A.factors = factors;
   static PerDeviceFlag attr_set;
   const int dev = current_device();
   if (!attr_set.done(dev)) {

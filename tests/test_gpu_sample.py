@@ -3,7 +3,7 @@
 Tokens and kept counts are whole numbers: they are equal to the definition's
 wherever no border lies closer than 2^-30 of the sum to a decision (the kernel's
 sums are within that: 8192 threads' shares rounded to 2^-45 each, five a thread,
-and weights within 2^-38 of themselves).  Log probabilities are (x - max) / T less log1p of the
+and weights within 2^-36 of themselves).  Log probabilities are (x - max) / T less log1p of the
 kept sum without its largest weight, both at most 0 in fp32: a difference and a
 quotient of 2^-24 each, log1p within 2^-23, their sum 2^-24, less than 2^-22 in all;
 the sum within 2^-30.
@@ -41,7 +41,7 @@ def reference(x, u, T, k=0, p=1.0, mp=0.0):
         n = min(n, n_p)
     if mp > 0:
         n_m = int((w >= mp).sum())
-        # relative, as a weight is known to 2^-38 of itself; the largest is 1 exactly
+        # relative, as a weight is known to 2^-36 of itself; the largest is 1 exactly
         near += [abs(v - mp) / mp for v in w[max(0, n_m - 1): n_m + 1] if v < 1]
         n = min(n, n_m)
     t = (float(min(max(u, 0.0), 1 - 2.0 ** -24)) if u == u else 0.0) * c[n - 1]
