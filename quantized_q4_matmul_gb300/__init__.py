@@ -174,6 +174,7 @@ _F64 = ("torch.float64",)
 _I8 = ("torch.int8",)
 _I32 = ("torch.int32",)
 _U8 = ("torch.uint8",)
+_F16U8 = _F16 + _U8
 
 
 _dtype_names = {}  # torch dtype -> its name: str() of a dtype takes longer than the lookup
@@ -651,10 +652,13 @@ def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, 
     M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
     pos0, window, sinks = int(pos0), int(window), int(sinks)
     qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
-    need = max(0, lib().qk_gqa_attention_q4_scratch_bytes(M, H, H_kv, D, pos0, window, sinks))
+    # fp16 rows of all positions are as much as any call needs: no need to ask then
+    need = 0
+    if scratch is not None and not isinstance(scratch, int) and scratch.nbytes < 512 * H_kv * (pos0 + M):
+        need = max(0, lib().qk_gqa_attention_q4_scratch_bytes(M, H, H_kv, D, pos0, window, sinks))
     a = _bufs("qk_gqa_attention_q4", (q_f16, 2 * qn, _F16, "q_f16"), (k_q4, cn // 2, _U8, "k_q4"),
               (k_dm, cn // 8, _F16, "k_dm"), (v_q4, cn // 2, _U8, "v_q4"), (v_dm, cn // 8, _F16, "v_dm"),
-              (out_f16, 2 * qn, _F16, "out_f16"), (scratch if need else None, need, _F16 + _U8, "scratch"))
+              (out_f16, 2 * qn, _F16, "out_f16"), (scratch, need, _F16U8, "scratch"))
     _check(lib().qk_gqa_attention_q4(a[0], a[1], a[2], a[3], a[4], a[5], M, H, H_kv, D, pos0, L_max, float(scale),
                                      window, sinks, a[6], _stream(stream)), "qk_gqa_attention_q4")
 

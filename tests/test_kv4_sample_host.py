@@ -84,6 +84,12 @@ def test_attention_q4_scratch(qk_lib):
     assert f(1, 8, 2, 128, 32766, none) == 0
     assert 0 < f(1, 8, 2, 128, 32767, none) <= 1 << 20 and 0 < f(8, 8, 2, 128, 10 ** 6, none) <= 4 << 20
     assert f(1, 8, 2, 128, 10 ** 6, 4096, 4) == 0
+    # never more than the fp16 rows of all positions, which the binding relies on
+    for M in (1, 3, 7, 8, 9, 40, 700):
+        for H, Hkv in ((1, 1), (8, 8), (24, 8), (32, 4), (1024, 1024), (1024, 128), (40, 40)):
+            for pos0 in (0, 1, 63, 64, 500, 9000, 65536, 10 ** 6, (1 << 30) - 701):
+                for window, sinks in ((none, 0), (0, 5), (1, 0), (700, 3), (10 ** 5, 0)):
+                    assert 0 <= f(M, H, Hkv, 128, pos0, window, sinks) <= 512 * Hkv * (pos0 + M)
     for bad in ((-1, 8, 2, 128, 0, 1), (1, 8, 3, 128, 0, 1), (1, 8, 2, 64, 0, 1), (1, 8, 2, 128, -1, 1), (1, 8, 2, 128, 0, -1),
                 (1, 8, 2, 128, 0, 1, -1), (1, 8, 2, 128, 1 << 30, 1), (1, 18, 2, 128, 0, 1)):
         with pytest.raises(ValueError):
