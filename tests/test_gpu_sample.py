@@ -263,6 +263,8 @@ def test_more_than_2_31_logits(qk_lib, cuda):
     assert torch.equal(tok[rows], t2) and torch.equal(kept[rows], k2) and (tok >= 0).all()
     qk_lib.qk_sample(x, u, tok, None, None, M, V, 0.0)
     assert torch.equal(tok[rows].long(), x[rows].argmax(1))
+    del x
+    torch.cuda.empty_cache()
 
 
 def test_sample_in_a_graph_with_new_numbers(qk_lib, cuda):
