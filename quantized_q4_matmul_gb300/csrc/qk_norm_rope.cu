@@ -49,40 +49,56 @@ __device__ __forceinline__ uint32_t pack2h(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// max(a, b), NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // kN of the 32 values of a group, which 32 / kN lanes hold: their nibbles in order,
 // and (d, m) as two fp16.  Every lane of the warp takes part.
 template <int kN>
 __device__ __forceinline__ uint32_t quantize(const float* y, uint32_t& dm) {
-  float lo = y[0], hi = y[0], far = 0.f;
+  float lo = y[0], hi = y[0];
 #pragma unroll
-  for (int e = 0; e < kN; ++e) {
+  for (int e = 1; e < kN; ++e) {
     lo = fminf(lo, y[e]);
-    hi = fmaxf(hi, y[e]);
-    far = fmaf(y[e], 0.f, far);  // NaN where a value is not finite
+    hi = max_nan(hi, y[e]);
   }
-  if (far != 0.f) hi = INFINITY;
 #pragma unroll
   for (int o = 1; o < 32 / kN; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   const float m = __half2float(__float2half_rn(lo));
-  const float d = __half2float(__float2half_rn(fmaxf(hi - m, 0.f) / 15.f));
+  const float d = __half2float(__float2half_rn(max_nan(hi - m, 0.f) / 15.f));
   // a value that is not finite, or m or 15 d past fp16, makes the group NaN (d is
-  // infinite then, or NaN where m is: infinity less infinity)
+  // infinite then, or NaN)
   const bool fine = fabsf(m) < INFINITY && d <= 4366.f;
   uint32_t q = 0;
   if (d > 0.f) {
-    // (y - m) / d by the reciprocal is within 2^-22 of the quotient, 2^-18 at most
-    // here; a quotient nearer to a border than that is divided
+    // (y - m) / (15 d) by the reciprocal, clamped to 0 .. 1, is within 2^-21 of the
+    // quotient, and 15 times it within 2^-17 of the level; where one is nearer to a
+    // border than that, the lane divides.  The levels add up in q with the bits of
+    // kMagic, which come off in the end.
     constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer in the low bits
-    const float r = 1.0f / d;
+    constexpr uint32_t kBits = 0x4B400000u, kSum = kN == 4 ? kBits * 0x1111u : kBits * 0x11111111u;
+    const float r = __fdividef(1.0f / 15.0f, d);
+    float n[kN], far = 0.f;
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const float n = y[e] - m, t = n * r;
-      float k = __fadd_rn(t, kMagic);
-      if (fabsf(t - __fsub_rn(k, kMagic)) > 0.4999f) k = __fadd_rn(n / d, kMagic);
-      q |= (uint32_t)min(max((int)__float_as_uint(k) - 0x4B400000, 0), 15) << (4 * e);
+    for (int e = kN - 1; e >= 0; --e) {
+      n[e] = y[e] - m;
+      const float t = __saturatef(n[e] * r), k = fmaf(t, 15.f, kMagic);
+      far = fmaxf(far, fabsf(fmaf(t, 15.f, -__fsub_rn(k, kMagic))));
+      q = (q << 4) + __float_as_uint(k);
+    }
+    q -= kSum;
+    if (far > 0.4999f) {
+      q = 0;
+#pragma unroll
+      for (int e = kN - 1; e >= 0; --e)
+        q = (q << 4) + __float_as_uint(__fadd_rn(fminf(fmaxf(n[e] / d, 0.f), 15.f), kMagic)) - kBits;
     }
   }
   dm = fine ? pack2h(d, m) : 0x7FFF7FFFu;
