@@ -34,6 +34,7 @@
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
+#include "qk_packed.cuh"
 #include "qk_rope.cuh"
 
 namespace qk {
@@ -198,11 +199,14 @@ __global__ void __launch_bounds__(kNrThreads, kPer == 1 ? 4 : 2)
     // every lane takes the same path through the shuffles: a head without a norm (v,
     // or no gamma) only drops the result
     if (N.q_gamma || N.k_gamma) {
-      float ss = 0.f;
+      Two sums(0.f);
 #pragma unroll
       for (int r = 0; r < kPer; ++r)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[r][e], y[r][e], ss);
+        for (int e = 0; e < 8; e += 2) sums = fma2(Two(y[r][e], y[r][e + 1]), Two(y[r][e], y[r][e + 1]), sums);
+      float ss, odd;
+      sums.get(ss, odd);
+      ss += odd;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1)
         if (o < lph) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -215,8 +219,7 @@ __global__ void __launch_bounds__(kNrThreads, kPer == 1 ? 4 : 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 gg = __half22float2(*reinterpret_cast<const __half2*>(&g[e]));
-            y[r][2 * e] = y[r][2 * e] * inv * gg.x;
-            y[r][2 * e + 1] = y[r][2 * e + 1] * inv * gg.y;
+            mul2(mul2(Two(y[r][2 * e], y[r][2 * e + 1]), Two(inv)), Two(gg.x, gg.y)).get(y[r][2 * e], y[r][2 * e + 1]);
           }
         }
       }
@@ -225,12 +228,12 @@ __global__ void __launch_bounds__(kNrThreads, kPer == 1 ? 4 : 2)
       if (turns && on && 8 * c < A.D) {
         const float4 cc = *reinterpret_cast<const float4*>(cosines[tok] + 4 * c);
         const float4 ss = *reinterpret_cast<const float4*>(sines[tok] + 4 * c);
-        const float tc[4] = {cc.x, cc.y, cc.z, cc.w}, ts[4] = {ss.x, ss.y, ss.z, ss.w};
+        const Two tc[2] = {Two(cc.x, cc.y), Two(cc.z, cc.w)}, ts[2] = {Two(ss.x, ss.y), Two(ss.z, ss.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = y[0][e], b = y[0][4 + e];
-          y[0][e] = a * tc[e] - b * ts[e];
-          y[0][4 + e] = b * tc[e] + a * ts[e];
+        for (int e = 0; e < 2; ++e) {
+          const Two a(y[0][2 * e], y[0][2 * e + 1]), b(y[0][4 + 2 * e], y[0][5 + 2 * e]);
+          fma2(a, tc[e], mul2(mul2(b, ts[e]), Two(-1.f))).get(y[0][2 * e], y[0][2 * e + 1]);
+          fma2(b, tc[e], mul2(a, ts[e])).get(y[0][4 + 2 * e], y[0][5 + 2 * e]);
         }
       }
     } else if (h2 > 0 && __any_sync(0xffffffffu, turns && on)) {

@@ -47,6 +47,7 @@
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
+#include "qk_packed.cuh"
 
 namespace qk {
 
@@ -165,32 +166,6 @@ struct Sum {
   }
   __device__ __forceinline__ unsigned long long value() const { return fixed(h, l) - (1ull << 44); }
 };
-
-// Two numbers in one register pair, for the instructions that take both.
-struct Two {
-  unsigned long long v;
-  __device__ __forceinline__ Two() {}
-  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
-  __device__ __forceinline__ void get(float& a, float& b) const {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-  }
-};
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return d;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  Two d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
 
 constexpr double kPerOctave = kTable * 1.44269504088896340736;  // kTable log2(e)
 constexpr float kPerOctaveH = (float)kPerOctave, kPerOctaveL = (float)(kPerOctave - (double)kPerOctaveH);
