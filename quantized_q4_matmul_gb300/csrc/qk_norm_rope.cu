@@ -24,8 +24,9 @@
 // twice as long.
 //
 // Every input is read once: 4095 tokens of 24 + 8 + 8 heads of 128 into 4 bits move 115
-// MB (17 us at a copy's rate) in 25 us, bound by instructions (178 for a row and warp,
-// issue slots 79 % busy); into fp16 25.3 us.  Four CTAs an SM: three took 18.7 us where four
+// MB (17 us at a copy's rate) in 22 us, bound by instructions (156 for a row and warp,
+// issue slots 78 % busy; 178 with clamps and looks for borders value by value, and 25
+// us); into fp16 25.3 us.  Four CTAs an SM: three took 18.7 us where four
 // took 15.9 (2047 tokens into fp16).  One token 2.1 us, latency.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -33,7 +33,7 @@
 // does not, or the candidates are too many (equal logits), it searches the order
 // bit by bit instead, with an exact sum over the row at each step.
 //
-// Bound by latency for one row (9.2 us for 128256 logits with top_k 40: two passes of
+// Bound by latency for one row (9.3 us for 128256 logits with top_k 40: two passes of
 // 1 us, two cluster barriers, then a dozen short steps of one CTA whose code is
 // fetched once), and by instructions where all weights count: 512 rows of 128256
 // without bounds 288 us (weights for nothing would leave 235: 21 packed instructions for
