@@ -340,8 +340,11 @@ qk_status qk_rope_kv_append(const float *q, const float *k, const float *v, cons
  *   q = the nearest of 0 .. 15 to (x - m) / d (ties to even; 0 where d = 0),
  * from the fp32 values and in fp32.  Byte j of a group has the q of value 2 j in
  * its low and of 2 j + 1 in its high half; dm has d, then m.  A group with a value
- * that is not finite or beyond fp16, or whose values lie more than about 65000
- * apart (15 d is a finite fp16 number), is stored as NaN (d and m).
+ * that is not finite or not below 65520 in size (fp16 has none for it), or with d
+ * above 4366 (values more than about 65490 apart: 15 d would not be a finite fp16
+ * number), is stored as NaN (d and m).  Where 15 d + m would be 65520 or more, as d
+ * was rounded up, d is the next fp16 number below: d q + m is a finite fp16 number
+ * for every q of a group that is not NaN.
  */
 qk_status qk_norm_rope_kv_append(const float *q, const float *k, const float *v, const uint16_t *q_gamma_f16,
                                  const uint16_t *k_gamma_f16, float eps, const double *inv_freq, uint16_t *q_f16,

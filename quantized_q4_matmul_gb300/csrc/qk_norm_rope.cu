@@ -10,7 +10,8 @@
 // its first n_rot dimensions turn as in qk_rope.cu, and q (fp16) and the cache
 // rows are written.  A 4-bit row holds groups of 32 values as v = d q + m:
 //   m = fp16(min x),  d = fp16(max(max x - m, 0) / 15),
-//   q = (x - m) / d rounded to the nearest of 0 .. 15 (0 where d = 0).
+//   q = (x - m) / d rounded to the nearest of 0 .. 15 (0 where d = 0),
+// d one step lower where 15 d + m would not be a finite fp16 number.
 //
 // A CTA has a few tokens and computes their sines and cosines together, while its
 // first rows are on their way; a row is a head of a token, 8 dimensions a lane, and two
@@ -74,10 +75,14 @@ __device__ __forceinline__ uint32_t quantize(const float* y, uint32_t& dm) {
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   const float m = __half2float(__float2half_rn(lo));
-  const float d = __half2float(__float2half_rn(max_nan(hi - m, 0.f) / 15.f));
-  // a value that is not finite, or m or 15 d past fp16, makes the group NaN (d is
-  // infinite then, or NaN)
-  const bool fine = fabsf(m) < INFINITY && d <= 4366.f;
+  __half dh = __float2half_rn(max_nan(hi - m, 0.f) / 15.f);
+  // a value that is not finite or rounds to an infinite fp16 number, or a 15 d that does,
+  // makes the group NaN (hi is NaN where a value is)
+  const bool fine = lo > -65520.f && hi < 65520.f && __half2float(dh) <= 4366.f;
+  // where d was rounded up so far that level 15 would be infinite as fp16, the number below d:
+  // that is less than (hi - m) / 15, and level 15 less than hi
+  if (fmaf(15.f, __half2float(dh), m) >= 65520.f) dh = __ushort_as_half((unsigned short)(__half_as_ushort(dh) - 1u));
+  const float d = __half2float(dh);
   uint32_t q = 0;
   if (d > 0.f) {
     // (y - m) / (15 d) by the reciprocal, clamped to 0 .. 1, is within 2^-21 of the
