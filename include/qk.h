@@ -520,10 +520,11 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * temperature 0 gives the first token in the order, a logprob of 0 and kept 1.  A
  * row that holds NaN or +inf, or nothing but -inf, gives token -1, a NaN logprob
  * and kept 0.  u below 0 or NaN counts as 0, u of 1 or more as the largest fp32
- * number below 1.  A weight is within 2^-36 of itself, and an addition rounds 2^-40
- * of the largest off at most, so that a token follows from the definition, but where
- * a border lies closer than about 2^-33 of the sum to a decision, rather than from
- * the order of a sum.
+ * number below 1.  A weight is within 2^-36 of itself.  An addition rounds off at most
+ * 3 2^-48 of its thread's sum, which starts at the largest weight, and what the threads
+ * hold is rounded to 2^-44 of that: together less than 2^-28 of the sum (2^-27 for V above
+ * 2^18).  A token therefore follows from the definition rather than from the order of a
+ * sum, but where a border lies closer than that to a decision.
  * How many CTAs share a row follows M and the device, and with it the sums' last
  * bits; the same call repeats its bits.  temperature is 0 or 1e-6 .. 1e6, top_p
  * 0 .. 1, min_p 0 or 1e-12 .. 1, V at most 524288, M at most 2^31 - 1.  Rows need
