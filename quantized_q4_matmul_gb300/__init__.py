@@ -229,6 +229,18 @@ def _n(v) -> int:
     return v if v > 0 else 0
 
 
+def _c_int(v, where: str, name: str, most: int = (1 << 63) - 1) -> int:
+    """An integer argument for a C integer whose largest value is `most`: ctypes would
+    take one out of range modulo its size."""
+    v = int(v)
+    if -most - 1 <= v <= most:
+        return v
+    raise ValueError("%s: %s %d does not fit a C integer" % (where, name, v))
+
+
+_INT_MAX = (1 << 31) - 1
+
+
 def _size(a: int, b: int, c: int = 1) -> int:
     """a * b * c, or 0 where one of them is not positive."""
     return a * b * c if a > 0 and b > 0 and c > 0 else 0
@@ -453,7 +465,8 @@ def qk_rope_kv_append(q, k, v, inv_freq, q_f16, k_cache, v_cache, M: int, H: int
                                    _buf(q_f16, 2 * qn, "qk_rope_kv_append: q_f16", _F16),
                                    _buf(k_cache, 2 * cn, "qk_rope_kv_append: k_cache", _F16),
                                    _buf(v_cache, 2 * cn, "qk_rope_kv_append: v_cache", _F16), M, H, H_kv, D,
-                                   int(n_rot), int(pos0), L_max, int(layout), float(magnitude),
+                                   int(n_rot), _c_int(pos0, "qk_rope_kv_append", "pos0"), L_max,
+                                   _c_int(layout, "qk_rope_kv_append", "layout", _INT_MAX), float(magnitude),
                                    _stream(stream)), "qk_rope_kv_append")
 
 
@@ -464,12 +477,17 @@ def qk_norm_rope_kv_append(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv_fr
     include/qk.h): gammas fp16 [D], or None for heads that are not normalized."""
     M, H, H_kv, D, n_rot, L_max = int(M), int(H), int(H_kv), int(D), int(n_rot), int(L_max)
     cn = 2 * _size(H_kv, L_max, D)
+    pos0, layout = _append_ints("qk_norm_rope_kv_append", pos0, layout)
     a = _bufs("qk_norm_rope_kv_append",
               *_append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot),
               (k_cache, cn, _F16, "k_cache"), (v_cache, cn, _F16, "v_cache"))
     _check(lib().qk_norm_rope_kv_append(a[0], a[1], a[2], a[3], a[4], float(eps), a[5], a[6], a[7], a[8], M, H, H_kv, D,
-                                        n_rot, int(pos0), L_max, int(layout), float(magnitude), _stream(stream)),
+                                        n_rot, pos0, L_max, layout, float(magnitude), _stream(stream)),
            "qk_norm_rope_kv_append")
+
+
+def _append_ints(where, pos0, layout):
+    return _c_int(pos0, where, "pos0"), _c_int(layout, where, "layout", _INT_MAX)
 
 
 def _append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot):
@@ -486,12 +504,13 @@ def qk_norm_rope_kv_append_q4(q, k, v, q_gamma_f16, k_gamma_f16, eps: float, inv
     uint8 [H_kv][L_max][D / 2], k_dm, v_dm fp16 [H_kv][L_max][D / 32][2]."""
     M, H, H_kv, D, n_rot, L_max = int(M), int(H), int(H_kv), int(D), int(n_rot), int(L_max)
     cn = _size(H_kv, L_max, D)
+    pos0, layout = _append_ints("qk_norm_rope_kv_append_q4", pos0, layout)
     a = _bufs("qk_norm_rope_kv_append_q4",
               *_append_args(q, k, v, q_gamma_f16, k_gamma_f16, inv_freq, q_f16, M, H, H_kv, D, n_rot),
               (k_q4, cn // 2, _U8, "k_q4"), (k_dm, cn // 8, _F16, "k_dm"), (v_q4, cn // 2, _U8, "v_q4"),
               (v_dm, cn // 8, _F16, "v_dm"))
     _check(lib().qk_norm_rope_kv_append_q4(a[0], a[1], a[2], a[3], a[4], float(eps), a[5], a[6], a[7], a[8], a[9], a[10],
-                                           M, H, H_kv, D, n_rot, int(pos0), L_max, int(layout), float(magnitude),
+                                           M, H, H_kv, D, n_rot, pos0, L_max, layout, float(magnitude),
                                            _stream(stream)), "qk_norm_rope_kv_append_q4")
 
 
@@ -501,7 +520,8 @@ def qk_dequant_kv_q4(q4, dm, out_f16, H_kv: int, D: int, pos0: int, M: int, L_ma
     cn = _size(H_kv, L_max, D)
     a = _bufs("qk_dequant_kv_q4", (q4, cn // 2, _U8, "q4"), (dm, cn // 8, _F16, "dm"),
               (out_f16, 2 * _size(H_kv, M, D), _F16, "out_f16"))
-    _check(lib().qk_dequant_kv_q4(a[0], a[1], a[2], H_kv, D, int(pos0), M, L_max, _stream(stream)), "qk_dequant_kv_q4")
+    _check(lib().qk_dequant_kv_q4(a[0], a[1], a[2], H_kv, D, _c_int(pos0, "qk_dequant_kv_q4", "pos0"), M, L_max,
+                                  _stream(stream)), "qk_dequant_kv_q4")
 
 
 def qk_rmsnorm_scratch_bytes(qtype, M: int, K: int, gateup: bool = False) -> int:
@@ -619,7 +639,7 @@ def qk_gqa_attention(q_f16, k_cache, v_cache, out, M: int, H: int, H_kv: int, D:
                                   _buf(k_cache, 2 * cn, what + ": k_cache", _F16),
                                   _buf(v_cache, 2 * cn, what + ": v_cache", _F16),
                                   _buf(out, 4 * qn, what + ": out", _F32), int(M), int(H), int(H_kv), int(D),
-                                  int(pos0), int(L_max), float(scale), _stream(stream)), what)
+                                  _c_int(pos0, what, "pos0"), int(L_max), float(scale), _stream(stream)), what)
 
 
 def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_kv: int, D: int, pos0: int,
@@ -627,19 +647,25 @@ def qk_gqa_attention_window(q_f16, k_cache, v_cache, out_f16, M: int, H: int, H_
     """qk_gqa_attention with a sliding window of `window` positions and the first
     `sinks` positions always visible (see include/qk.h); out [M][H][D] fp16."""
     M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
+    pos0, window, sinks = _window_ints("qk_gqa_attention_window", pos0, window, sinks)
     qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
     _check(lib().qk_gqa_attention_window(_buf(q_f16, 2 * qn, "qk_gqa_attention_window: q_f16", _F16),
                                          _buf(k_cache, 2 * cn, "qk_gqa_attention_window: k_cache", _F16),
                                          _buf(v_cache, 2 * cn, "qk_gqa_attention_window: v_cache", _F16),
                                          _buf(out_f16, 2 * qn, "qk_gqa_attention_window: out_f16", _F16), M, H, H_kv,
-                                         D, int(pos0), L_max, float(scale), int(window), int(sinks),
-                                         _stream(stream)), "qk_gqa_attention_window")
+                                         D, pos0, L_max, float(scale), window, sinks, _stream(stream)),
+           "qk_gqa_attention_window")
+
+
+def _window_ints(where, pos0, window, sinks):
+    return _c_int(pos0, where, "pos0"), _c_int(window, where, "window"), _c_int(sinks, where, "sinks")
 
 
 def qk_gqa_attention_q4_scratch_bytes(M: int, H: int, H_kv: int, D: int, pos0: int, window: int, sinks: int = 0) -> int:
     """Scratch bytes that qk_gqa_attention_q4 needs (0: none); host only."""
-    r = int(lib().qk_gqa_attention_q4_scratch_bytes(int(M), int(H), int(H_kv), int(D), int(pos0), int(window),
-                                                    int(sinks)))
+    where = "qk_gqa_attention_q4_scratch_bytes"
+    M, H, H_kv, D = (_c_int(v, where, "size") for v in (M, H, H_kv, D))
+    r = int(lib().qk_gqa_attention_q4_scratch_bytes(M, H, H_kv, D, *_window_ints(where, pos0, window, sinks)))
     if r < 0:
         raise ValueError("qk_gqa_attention_q4_scratch_bytes: invalid sizes")
     return r
@@ -650,7 +676,7 @@ def qk_gqa_attention_q4(q_f16, k_q4, k_dm, v_q4, v_dm, out_f16, M: int, H: int, 
     """qk_gqa_attention_window over a cache held in 4 bits (see include/qk.h); scratch:
     qk_gqa_attention_q4_scratch_bytes of device memory where that is not 0."""
     M, H, H_kv, D, L_max = int(M), int(H), int(H_kv), int(D), int(L_max)
-    pos0, window, sinks = int(pos0), int(window), int(sinks)
+    pos0, window, sinks = _window_ints("qk_gqa_attention_q4", pos0, window, sinks)
     qn, cn = _size(M, H, D), _size(H_kv, L_max, D)
     # fp16 rows of all positions are as much as any call needs: no need to ask then
     need = 0
@@ -673,7 +699,8 @@ def qk_logprobs(logits, tokens, logprob, entropy, top_n: int, top_ids, top_logpr
     m = 4 * _n(M)
     _check(lib().qk_logprobs(_buf(logits, m * _n(V), "qk_logprobs: logits", _F32),
                              _buf(tokens, m, "qk_logprobs: tokens", _I32), _buf(logprob, m, "qk_logprobs: logprob", _F32),
-                             _buf(entropy, m, "qk_logprobs: entropy", _F32), int(top_n),
+                             _buf(entropy, m, "qk_logprobs: entropy", _F32),
+                             _c_int(top_n, "qk_logprobs", "top_n", _INT_MAX),
                              _buf(top_ids, m * _n(top_n), "qk_logprobs: top_ids", _I32),
                              _buf(top_logprobs, m * _n(top_n), "qk_logprobs: top_logprobs", _F32), int(M), int(V),
                              _stream(stream)), "qk_logprobs")
@@ -687,8 +714,9 @@ def qk_sample(logits, u, token, logprob, kept, M: int, V: int, temperature: floa
     m = 4 * _n(M)
     a = _bufs("qk_sample", (logits, m * _n(V), _F32, "logits"), (u, m, _F32, "u"), (token, m, _I32, "token"),
               (logprob, m, _F32, "logprob"), (kept, m, _I32, "kept"))
-    _check(lib().qk_sample(a[0], a[1], a[2], a[3], a[4], M, V, float(temperature), int(top_k), float(top_p),
-                           float(min_p), _stream(stream)), "qk_sample")
+    _check(lib().qk_sample(a[0], a[1], a[2], a[3], a[4], M, V, float(temperature),
+                           _c_int(top_k, "qk_sample", "top_k", _INT_MAX), float(top_p), float(min_p), _stream(stream)),
+           "qk_sample")
 
 
 def qk_get_device_status(stream=None) -> None:
