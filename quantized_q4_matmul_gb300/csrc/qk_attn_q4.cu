@@ -22,29 +22,28 @@
 // sits 4 bits higher); for K the offsets come off with the product of (d, m).
 // Rounded to fp16: weights (against a reference 7 below the largest, so that those
 // down to 2^-32 of it count), d (q - 8), and the outputs.  The 2-norm of the error is
-// 2.7e-4 of the output's after 500 positions, 3.3e-4 after 65536; the output's own
+// 2.8e-4 of the output's after 500 positions, 3.3e-4 after 65536; the output's own
 // rounding is 2.1e-4 of it.  With fp16(d q + m) for K and fp16(d q) for V it was 6.0e-4
-// and 7.4e-4 (in 3.8 and 21.8 us instead of 4.0 and 22.4).
+// and 7.4e-4 (0.1 and 0.6 us faster).
 // Every warp keeps its own running maximum, sums and O; the warps of a CTA join
 // in order through shared memory.  The CTAs of a key/value head join
 //   - as a cluster of up to 16 through distributed shared memory, each writing a
 //     share of the outputs; or,
 //   - from 65536 positions of all heads on, through the scratch and a second kernel
 //     (attn_q4_join_kernel): a GPC takes few clusters of 16, so that 8 heads' leave
-//     SMs idle, while this split uses all of them.  24 heads over 8, clusters / all
-//     SMs, us: 2048 positions 5.7 / 7.2, 4096 6.8 / 8.0, 8192 9.0 / 8.9, 16384 13.3 /
-//     10.9, 32768 21.5 / 15.9, 131072 69 / 35; 32 over 4: 4096 5.6 / 8.7.
+//     SMs idle, while this split uses all of them (kQSplitFrom).
 //
-// One token, 24 heads over 8, 65536 positions (84 MB: 12.4 us at a copy's rate): 22.4 us.
+// One token, 24 heads over 8, 65536 positions (84 MB: 12.4 us at a copy's rate): 22.5 us.
 // Bound by instructions at long lengths (375 for a warp's 16 positions, issued in
 // 57 % of the cycles, the ends included; the DRAM is 48 % busy) and by the latency of
 // a launch, or two, at short ones.
 //
-// More tokens: the visible rows are written as fp16(d q + m) to the caller's scratch
-// once and the windowed prefill runs over them: a query tile's 128 rows would unpack
-// each key again.  1023 tokens after 7001, 24 heads over 8: 117 us, 9 of them for
-// the rows; 104 CTAs of two query tiles each on 152 SMs.  (Clusters of 2, 4 and 8 that
-// share the keys of a pair of tiles: 134, 118, 171.)
+// More tokens: the visible rows are written as fp16(d q + m) to the caller's scratch once
+// and the windowed prefill runs over them: a query tile's 128 rows would unpack each key
+// again.  K and V are rounded there, and the error is 5.8e-4 of the output's.  1023 tokens
+// after 7001, 24 heads over 8: 117 us, 10 of them for the rows; 104 CTAs of two query
+// tiles each on 152 SMs.  (Clusters of 2, 4 and 8 that share the keys of a pair of tiles:
+// 134, 118, 171.)
 //
 // The kernels have no waits but the cluster barriers, which every thread reaches.
 #include <cuda_fp16.h>
@@ -62,9 +61,25 @@ namespace qk {
 namespace {
 
 constexpr int kQMaxCluster = 16;
+// Columns that read the 4-bit rows directly: four tiles of 8, whose O and scores are what the
+// registers of a warp hold.  us over 8 key/value heads, 24 columns so / through fp16 rows and
+// the prefill: 500 positions 9.4 / 10.0, 2000 11.7 / 11.7, 8000 20.3 / 26.3, 20000 24.4 / 55.4,
+// 65536 49 / 165; 32 columns 9.9 / 10.6, 12.4 / 11.7, 21.0 / 26.4, 24.9 / 55.5, 50 / 165.  33
+// to 64 take what the fp16 rows take: 10.5, 11.9, 26.5, 55.7, 165.
 constexpr int kQMaxCols = 32;
 constexpr int kQMaxSplit = 160;   // CTAs of a call that join through the scratch
-constexpr int64_t kQSplitFrom = 8 * 8192;  // positions of all key/value heads from which they do
+// Positions of all key/value heads from which a call's CTAs need not be clusters.  us as
+// clusters / over all SMs, one token:
+//   24 heads over 8: 4096 positions 7.1 / 8.3, 8192 9.2 / 9.6, 16384 13.5 / 12.2, 32768 21.3 / 15.4,
+//   131072 68 / 35; 32 over 4: 8192 7.6 / 9.8, 16384 11.7 / 11.1, 32768 19.6 / 13.8;
+//   8 over 2: 16384 8.7 / 9.4, 32768 13.3 / 10.7; 8 over 1: 16384 8.8 / 10.8, 32768 13.4 / 11.7.
+// More tokens cross a little earlier, at half as many positions with 32 columns:
+//   15 columns of each of 8: 4096 9.8 / 9.9, 8192 13.4 / 11.8; 30 of 8: 4096 15.3 / 14.8, 8192 20.9 /
+//   17.8; 32 of 4: 8192 15.9 / 15.3, 16384 21.5 / 18.4; 20 of 2: 8192 14.3 / 14.0, 16384 19.9 / 15.8;
+//   32 of 1: 8192 15.1 / 16.7, 16384 20.9 / 17.1, 32768 31.8 / 19.1.
+// With one or two heads the product is thus late: one token over 65535 positions of one head
+// takes 22.5 us where all SMs would take 12.9.
+constexpr int64_t kQSplitFrom = 8 * 8192;
 constexpr int kUnit = 16;  // positions of a warp's step
 
 // The shape of a CTA for NT tiles of 8 columns and W warps.
@@ -686,10 +701,10 @@ struct DqArgs {
 };
 
 // The values of rows of a 4-bit cache, into fp16. A thread has one word of 8 values: a warp reads
-// 128 bytes and writes 512, and the many small CTAs of a call hide the latency. Two, four and
-// eight words a thread, all in flight, take 10.9, 11.6 and 13.8 us where one takes 10.7 (a
-// 512-token append with both exports of 4 x 2050 rows of 128), 38.6, 40.7 and 43.8 against 38.4
-// with 8 x 4200 rows.
+// 128 bytes and writes 512, and the many small CTAs of a call hide the latency: 8 x 4200 rows of
+// 128 in 3.6 us (11.3 MB, 1.7 us at a copy's rate), K and V of 8 x 8024 rows of a chunk in about
+// 10. Two, four and eight words a thread, all in flight, made calls with both exports of 8 x 4200
+// rows 0.2, 2.3 and 5.4 us longer.
 __global__ void __launch_bounds__(kDqThreads) dequant_kv_q4_kernel(const __grid_constant__ DqArgs A) {
   const int rr = threadIdx.x / A.per_row, c = threadIdx.x - rr * A.per_row;
   const int64_t r = (int64_t)blockIdx.x * A.step + rr;

@@ -177,8 +177,8 @@ struct Q4Cache {
   const uint8_t *k_q4, *v_q4;
   const uint16_t *k_dm, *v_dm;
 };
-// fp16 rows out[g][r] of `count` tensors (1 or 2): row r is position r where r <
-// sinks, else r + gap.
+// fp16 rows k_out[g][r] and, unless v_out is null (c.v_q4 and c.v_dm are not read then),
+// v_out[g][r]: row r is position r where r < sinks, else r + gap.
 cudaError_t launch_dequant_kv_q4(const Q4Cache& c, uint16_t* k_out, uint16_t* v_out, int Hkv, int D, int64_t Lmax,
                                  int64_t rows, int64_t sinks, int64_t gap, cudaStream_t s);
 // qk_gqa_attention_q4: few tokens by the decode kernel, others through the

@@ -19,15 +19,15 @@
 // meet by shuffles.  Where a whole head of the half layout turns, a lane has two runs of
 // four dimensions, each other's mates; otherwise a run of eight, and the half layout's
 // mates, which other lanes hold, pass through shared memory (2047 tokens of 32 + 4 + 4
-// heads of 128 in the half layout: 14.7 us with mates in a lane, 20.1 through shared
-// memory; the interleaved layout 15.7).  A value's level comes from a reciprocal, and from
+// heads of 128 in the half layout: 15.3 us with mates in a lane, a third more through shared
+// memory; the interleaved layout 16.3).  A value's level comes from a reciprocal, and from
 // a division where that is near a border between two levels: a division for each took
 // twice as long.
 //
 // Every input is read once: 4095 tokens of 24 + 8 + 8 heads of 128 into 4 bits move 115
-// MB (17 us at a copy's rate) in 22 us, bound by instructions (156 for a row and warp,
-// issue slots 78 % busy; 178 with clamps and looks for borders value by value, and 25
-// us); into fp16 25.3 us.  Four CTAs an SM: three took 18.7 us where four
+// MB (17 us at a copy's rate) in 28.9 us, bound by instructions (159 for a row and warp,
+// issue slots 77 % busy; 178 with clamps and looks for borders value by value, 3 us more);
+// into fp16 126 MB in 25.8 us.  Four CTAs an SM: three took 18.7 us where four
 // took 15.9 (2047 tokens into fp16).  One token 2.1 us, latency.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

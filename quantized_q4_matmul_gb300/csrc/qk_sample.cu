@@ -36,9 +36,13 @@
 // Bound by latency for one row (9.3 us for 128256 logits with top_k 40: two passes of
 // 1 us, two cluster barriers, then a dozen short steps of one CTA whose code is
 // fetched once), and by instructions where all weights count: 512 rows of 128256
-// without bounds 288 us (weights for nothing would leave 235: 21 packed instructions for
-// two, as the table of 2048 spares a polynomial in pairs; with one of 256 it was 321); HBM
-// 28 %.
+// without bounds 294 us, HBM 27 % (the weights are 53 of them: 21 packed instructions for
+// two, as the table of 2048 spares a polynomial in pairs; with one of 256 it took 33 more.
+// Sums that lose nothing are 8 of them).  One row with top_p 0.9 20.4 us, one without bounds
+// 18.1, the largest logit of one (temperature 0) 4.3 and of 512 rows 83.
+//
+// A row that is searched (equal logits by the thousand) takes up to 8 ms at 128256 logits and
+// 34 at 524288: up to 32 + 20 passes by one CTA for each border.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1092,9 +1096,13 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   }
   // CTAs for each row: as many as fill two CTAs an SM, up to 8; 16 for four rows at
   // most.  Where a long row's sums are needed, which keep the SMs busy, some SMs may
-  // have more.  us with 1, 2, 4, 8, 16 CTAs, 128256 logits: one row, top_k 40: 29.8, 21.4,
-  // 16.8, 10.2, 9.3; 8 rows 30.6, 21.7, 17.9, 12.1, 12.9; 64 rows, top_p 0.9: 137, 98, 62, 79,
-  // 125; 80 rows 129, 99, 89; 160 rows 179, 151, 145; 512 rows 341, 333, 394.
+  // have more.  us with 1, 2, 4, 8, 16 CTAs, 128256 logits from HBM: one row, top_k 40: 33.4, 23.8,
+  // 18.5, 11.7, 11.2; 8 rows 34.2, 24.8, 19.8, 13.3, 14.5; 64 rows 45, 34, 28, 28, 51; 512 rows
+  // 108, 119, 170, 195, 361.  top_p 0.9: one row 95, 57, 36, 26, 21; 8 rows 100, 60, 39, 35, 29;
+  // 64 rows 144, 89, 59, 77, 126; 80 rows 146, 92, 85, 100, 152; 160 rows 164, 139, 136, 176.
+  // No bounds: 200 rows 166, 141, 154; 300 rows 174, 180, 217; 512 rows 308, 302, 357; 1216
+  // rows 612, 669, 814.  Greedy: one row 22, 13, 7.9, 5.4, 4.3; 64 rows 30, 19, 13, 17; 512
+  // rows 83, 76, 91.
   const bool sums = a.temperature > 0.f && (a.top_k == 0 ? a.top_p < 1.f || a.min_p == 0.f : a.top_k > kSaThreads);
   const int64_t fill = (sums && a.V >= 65536 ? 5 : 4) * (int64_t)device_sms() / 2;
   int C = 1;
