@@ -839,7 +839,8 @@ qk_status qk_sample(const float* logits, const float* u, int32_t* token, float* 
   qk_status st = check_spans_host(b, c);
   if (st == QK_OK) st = check_spans_device(b, c);
   if (st != QK_OK) return st;
-  const qk::SampleArgs a{logits, u, token, logprob, kept, M, (int)V, top_k, temperature, top_p, min_p};
+  // a top_p of -0 is 0: the kernel takes its bits apart
+  const qk::SampleArgs a{logits, u, token, logprob, kept, M, (int)V, top_k, temperature, std::fabs(top_p), min_p};
   return map_cuda(qk::launch_sample(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

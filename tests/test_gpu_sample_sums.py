@@ -1,5 +1,6 @@
 """Sums of long rows of equal logits far below the largest: what an addition rounds off must not
-add up.  The definition has a closed form here, in 64 bits: weights 1 and n times w."""
+add up.  The definition has a closed form here, in 64 bits: weights 1 and n times w.  And zeros
+of either sign in the settings."""
 import math
 
 import numpy as np
@@ -48,3 +49,21 @@ def test_many_equal_logits_far_below_the_largest(qk_lib, cuda, x, V, M):
             continue
         tok, kept = _call(qk_lib, cuda, row, u[:3] * 0, 1.0, p=float(p))
         assert (tok == at).all() and (kept == 1 + math.ceil(n)).all(), (kept, n)
+
+
+def test_zeros_of_either_sign(qk_lib, cuda):
+    """A top_p, min_p or temperature of -0 is 0."""
+    import torch
+    x = torch.from_numpy(np.random.default_rng(603).standard_normal((4, 3000)).astype(np.float32)).to(cuda)
+    u = torch.tensor([0.0, 0.3, 0.6, 0.9], device=cuda)
+    for kw in (dict(top_p=0.0), dict(top_p=0.0, top_k=40), dict(temperature=0.0), dict(min_p=0.0, top_p=0.9)):
+        got = []
+        for sign in (1.0, -1.0):
+            tok, kept = (torch.full((4,), -7, dtype=torch.int32, device=cuda) for _ in range(2))
+            lp = torch.full((4,), 7.0, device=cuda)
+            qk_lib.qk_sample(x, u, tok, lp, kept, 4, 3000, **{n: v * sign if v == 0 else v for n, v in kw.items()})
+            got.append((tok, lp, kept))
+        for a, b in zip(*got):
+            assert torch.equal(a, b), kw
+        if "min_p" not in kw:
+            assert bool((got[1][2] == 1).all()) and torch.equal(got[1][0].long(), x.argmax(1))
