@@ -527,7 +527,7 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * number below 1.  A weight is within 2^-36 of itself.  An addition rounds off at most
  * 3 2^-48 of its thread's sum, which starts at the largest weight, and what the threads
  * hold is rounded to 2^-44 of that: together less than 2^-28 of the sum (2^-27 for V above
- * 2^18).  A token therefore follows from the definition rather than from the order of a
+ * 2^17).  A token therefore follows from the definition rather than from the order of a
  * sum, but where a border lies closer than that to a decision.
  * How many CTAs share a row follows M and the device, and with it the sums' last
  * bits; the same call repeats its bits.  temperature is 0 or 1e-6 .. 1e6, top_p
@@ -536,7 +536,8 @@ qk_status qk_logprobs(const float *logits, const int32_t *tokens, float *logprob
  * an input.  Thousands of equal logits around the last kept token, or around the
  * chosen one (logits of few bits), make a row slow: it is then searched by one CTA, a
  * pass for every bit.  Up to 8 ms were measured for a row of 128256 logits and 34 ms
- * for one of 524288; 18 and 80 ms for calls of 300 such rows.  M = 0 is a no-op; V = 0 is QK_ERR_SHAPE.
+ * for one of 524288; 18 and 80 ms for calls of 300 such rows.  M = 0 is a no-op;
+ * V = 0 is QK_ERR_SHAPE.
  */
 qk_status qk_sample(const float *logits, const float *u, int32_t *token, float *logprob, int32_t *kept, int64_t M,
                     int64_t V, float temperature, int top_k, float top_p, float min_p, qk_stream_t stream);
